@@ -2,7 +2,8 @@
  * coli_moe.h -- C ABI of the MI355X (gfx950) routed mixture-of-experts FFN
  * layer used by GLM-5.3-Flash-style models, with the pieces around it that
  * the same pages describe: the dense FFN of the first layers, a double-banked
- * device expert cache, and the sparse attention's index top-k selection.
+ * device expert cache, the sparse attention's index top-k selection, and the
+ * paged key-value cache with the attention of new tokens over it.
  *
  * The layer, per token x (length D):
  *   z      = W_router x + b                         (E logits, bias inside the sigmoid)
@@ -296,6 +297,104 @@ size_t coli_index_topk_workspace_bytes(int32_t rows, int32_t L, int32_t k);
 coli_status coli_index_topk(const float *scores, int32_t rows, int32_t L, int64_t ld,
                             const int32_t *lens, int32_t k, int32_t tail, int32_t *idx,
                             void *ws, size_t ws_bytes, void *stream);
+
+/* ---- paged key-value cache and the attention of new tokens -----------------
+ * The cache, read by the attention of one new token per sequence, that goes
+ * with the index selection above ([glm5next] "MLA/DSA": latent attention with
+ * an absorbed key-value cache, softmax over the selected positions;
+ * [glm53-hip] "Key changes": paged latent caches).  The keys and values of
+ * every sequence live in pages of `page` positions taken from one pool:
+ *   k [n_pages][Hkv][page][Dk], v [n_pages][Hkv][page][Dv] in the shape's dtype
+ *   table [B][max_pages] int32: the pages of each sequence in order, so
+ *     position p of sequence b is row p % page of page table[b][p / page]
+ *   lens [B] int32: positions held by each sequence (values outside
+ *     [0, max_pages * page] are clamped to it)
+ * v = NULL makes a latent cache: the value of a position is the first Dv
+ * elements of its key, stored once.  Query head i reads cache head
+ * i / (Hq / Hkv).  Page ids outside [0, n_pages) hide their positions (no
+ * weight, nothing written), wherever they stand; entries of the table behind
+ * a sequence's length are not used.
+ * Supported: B >= 0, 1 <= Hkv <= Hq <= 1024 with Hq % Hkv = 0, page a power
+ * of two <= 4096, n_pages and max_pages >= 1, Dk and Dv multiples of 8, both
+ * <= 256 (a latent cache: Dv <= Dk, Dk <= 576, Dv <= 512),
+ * n_pages * Hkv * page and B * Hq * (max_pages * page / 32 + 1) below 2^31,
+ * max_pages * page <= 2^24. */
+typedef struct {
+    int32_t B;         /* sequences of the call */
+    int32_t Hq, Hkv;   /* query heads; heads of the cache */
+    int32_t Dk, Dv;    /* width of a key (and query), of a value (and output) */
+    int32_t page;      /* positions per page */
+    int32_t n_pages;   /* pages in the pool */
+    int32_t max_pages; /* columns of the page table */
+    int32_t dtype;     /* coli_dtype of the cache, the queries and the output */
+} coli_kv_shape;
+
+typedef struct {
+    void *k;
+    void *v;              /* NULL: latent cache */
+    const int32_t *table;
+    const int32_t *lens;
+} coli_kv_cache;
+
+/* Writes the keys and values of new tokens into their sequences' pages.
+ * lens are the lengths WITH the new tokens.  start [B+1] int32, ascending:
+ * sequence b's new tokens are rows start[b] .. start[b+1]-1 of k_new
+ * [rows][Hkv][Dk] and v_new [rows][Hkv][Dv] (NULL for a latent cache) and its
+ * last positions; rows behind start[B] and rows that would come before
+ * position 0 are not written anywhere.  start = NULL: one new token per
+ * sequence (rows = B), a sequence of length 0 taking none.  A page shared by
+ * sequences must not be written through two of them.  Hq is ignored. */
+coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void *v_new, int32_t rows,
+                           const int32_t *start, const coli_kv_cache *c, void *stream);
+
+/* Attention of one new token per sequence over its cache.  With t = scale
+ * q.k_p over the positions p < lens[b] of the sequence:
+ *   out[b][i] = sum_p w_p v_p,  w = softmax(t),  lse[b][i] = log sum_p exp(t_p)
+ * q [B][Hq][Dk], out [B][Hq][Dv] in the dtype; lse [B][Hq] fp32, nullable.
+ * scale is finite (as is scale * log2 e in fp32; else COLI_E_SHAPE).
+ * A row without positions gives out = 0 and lse = -inf.  Softmax statistics
+ * and sums are fp32; in bf16 the weights enter the products as two bf16
+ * parts each (16 bits), so the output's own rounding is the one that counts.
+ *   idx (nullable, int32 [B][idx_k], as coli_index_topk writes it): only the
+ *     listed positions take part; entries outside [0, lens[b]) are skipped
+ *     (the -1 padding among them), a position listed twice counts twice.
+ *   acc_out (nullable, fp32 [B][Hkv][ld], ld a multiple of 4, at least
+ *     max_pages * page): the running attention weight of each position for
+ *     the eviction below,
+ *       acc_out[b][h][p] = acc_in[b][h][p] + sum of w_p over the heads of h
+ *     for p < lens[b]; entries from lens[b] on are not written.  acc_in NULL:
+ *     counted from 0; acc_in may be acc_out itself (any other overlap is an
+ *     error).  Not together with idx.
+ * ws: coli_kv_attn_workspace_bytes(s, idx_k, acc != 0) bytes (0 for an
+ * invalid shape; idx_k = 0 without idx).  Calls that may run at the same time
+ * need a workspace each. */
+size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32_t acc);
+coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
+                         const int32_t *idx, int32_t idx_k, const float *acc_in, float *acc_out,
+                         int64_t ld, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Eviction by accumulated attention weight: of each sequence b and cache head
+ * h the k positions with the largest acc stay, by the rules of
+ * coli_index_topk (the last min(tail, k) always, ties to the lower position),
+ * and are copied in ascending order to positions 0, 1, ... of new pages of
+ * the same pool.  Sequences of at most k positions are copied whole.
+ *   acc [B][Hkv][ld] fp32, ld a multiple of 4, at least max_pages * page
+ *   new_table [B][new_max_pages] int32: the pages to fill, new_max_pages *
+ *     page >= k; the first ceil(min(lens[b], k) / page) of a row are used.
+ *     They must differ from each other and from every page being read (the
+ *     old pages can be freed afterwards, or stay with other sequences that
+ *     share them).
+ *   new_lens [B] int32 receives min(lens[b], k)
+ *   kept [B][Hkv][k] int32 receives the old positions, -1 behind them
+ *   new_acc (nullable, fp32 [B][Hkv][new_ld], new_ld >= k) receives their
+ *     acc, and 0 from there to new_ld (the next tokens count from 0)
+ * Each cache head keeps its own positions; a position listed by `idx` above
+ * means the same token for all heads only while Hkv = 1 or nothing was
+ * evicted.  1 <= k <= 1 << 24, tail >= 0.  Hq is ignored.  No workspace. */
+coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const float *acc, int64_t ld,
+                          int32_t k, int32_t tail, const int32_t *new_table, int32_t new_max_pages,
+                          int32_t *new_lens, int32_t *kept, float *new_acc, int64_t new_ld,
+                          void *stream);
 
 /* Static description of a status code. */
 const char *coli_moe_status_str(coli_status st);

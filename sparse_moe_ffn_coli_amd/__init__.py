@@ -19,6 +19,10 @@ The entry points keep the C names:
   coli_moe_bank_acquire(compute_stream, ready_event) / coli_moe_bank_release(compute_stream, free_event)
   coli_index_topk_workspace_bytes(rows, L, k) -> int
   coli_index_topk(scores, k, idx, tail=0, lens=None, ws=None, stream=None)
+  coli_kv_append(shape, k_new, v_new, cache, start=None, stream=None)
+  coli_kv_attn_workspace_bytes(shape, idx_k=0, acc=False) -> int
+  coli_kv_attn(shape, q, cache, out, scale, idx=None, acc_in=None, acc_out=None, lse=None, ws, stream=None)
+  coli_kv_evict(shape, cache, acc, k, new_table, new_lens, kept, tail=0, new_acc=None, stream=None)
   coli_moe_status_str(code) -> str
 
 If the library has not been built the import still works, but every call
@@ -43,6 +47,7 @@ EXPORTED = ("coli_moe_workspace_bytes", "coli_moe_route", "coli_moe_ffn", "coli_
             "coli_moe_dense_workspace_bytes", "coli_moe_dense_ffn",
             "coli_moe_bank_fill", "coli_moe_bank_acquire", "coli_moe_bank_release",
             "coli_index_topk_workspace_bytes", "coli_index_topk", "coli_moe_ffn_noalloc",
+            "coli_kv_append", "coli_kv_attn_workspace_bytes", "coli_kv_attn", "coli_kv_evict",
             "coli_moe_status_str", "coli_moe_version")
 ROUTE_STAGES = ("router", "topk", "perm")
 FFN_STAGES = ("gate_up", "down", "combine")
@@ -83,6 +88,14 @@ class CWeightsInt4(C.Structure):
 
 class CDenseWeights(C.Structure):
     _fields_ = [("gate", C.c_void_p), ("up", C.c_void_p), ("down", C.c_void_p)]
+
+
+class CKvShape(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "Hq", "Hkv", "Dk", "Dv", "page", "n_pages", "max_pages", "dtype")]
+
+
+class CKvCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p), ("lens", C.c_void_p)]
 
 
 _lib = None
@@ -135,6 +148,15 @@ def lib():
         L.coli_moe_ffn_noalloc.restype = C.c_int
         L.coli_moe_ffn_noalloc.argtypes = [sp, vp, C.POINTER(CRouting), C.POINTER(CWeights), vp, vp,
                                            vp, vp]
+        kp, cp, i32, i64 = C.POINTER(CKvShape), C.POINTER(CKvCache), C.c_int32, C.c_int64
+        L.coli_kv_append.restype = C.c_int
+        L.coli_kv_append.argtypes = [kp, vp, vp, i32, vp, cp, vp]
+        L.coli_kv_attn_workspace_bytes.restype = sz
+        L.coli_kv_attn_workspace_bytes.argtypes = [kp, i32, i32]
+        L.coli_kv_attn.restype = C.c_int
+        L.coli_kv_attn.argtypes = [kp, vp, cp, C.c_float, vp, i32, vp, vp, i64, vp, vp, vp, sz, vp]
+        L.coli_kv_evict.restype = C.c_int
+        L.coli_kv_evict.argtypes = [kp, cp, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp]
         L.coli_moe_status_str.restype = C.c_char_p
         L.coli_moe_status_str.argtypes = [C.c_int]
         L.coli_moe_version.restype = C.c_int32
@@ -396,6 +418,140 @@ def coli_index_topk(scores, k: int, idx, tail: int = 0, lens=None, ws=None, ws_b
     _check(lib().coli_index_topk(scores.data_ptr(), rows, L, ld, _ptr(lens), k, tail, _ptr(idx),
                                  _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
            "coli_index_topk")
+
+
+# ---------------------------------------------------------------------------
+# the paged key-value cache
+# ---------------------------------------------------------------------------
+
+@dataclass(frozen=True)
+class KvShape:
+    """Sizes of a paged cache and of the calls on it, see coli_kv_shape."""
+    B: int
+    Hq: int
+    Hkv: int
+    Dk: int
+    Dv: int
+    page: int
+    n_pages: int
+    max_pages: int
+    dtype: int = COLI_BF16
+
+    def c(self) -> CKvShape:
+        return CKvShape(self.B, self.Hq, self.Hkv, self.Dk, self.Dv, self.page, self.n_pages, self.max_pages,
+                        self.dtype)
+
+
+@dataclass(frozen=True)
+class KvCache:
+    """The pools, the page table and the lengths (device tensors), see
+    coli_kv_cache.  v None: a latent cache."""
+    k: object
+    v: object
+    table: object
+    lens: object
+
+    def c(self) -> CKvCache:
+        return CKvCache(_ptr(self.k), _ptr(self.v), _ptr(self.table), _ptr(self.lens))
+
+
+def _kv_dtype(shape: KvShape):
+    import torch
+    return torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16
+
+
+def _kv_check(where: str, device, *args) -> None:
+    """(name, tensor, dtype, shape) each: the C ABI takes addresses only, so
+    types, sizes and devices are checked here."""
+    for name, t, dtype, size in args:
+        if t is None:
+            continue
+        if t.dtype != dtype or tuple(t.shape) != size:
+            raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, the cache on {device}")
+
+
+def _kv_cache_args(shape: KvShape, cache: KvCache):
+    import torch
+    dt, i32 = _kv_dtype(shape), torch.int32
+    pool = (shape.n_pages, shape.Hkv, shape.page)
+    return (("cache.k", cache.k, dt, pool + (shape.Dk,)), ("cache.v", cache.v, dt, pool + (shape.Dv,)),
+            ("cache.table", cache.table, i32, (shape.B, shape.max_pages)), ("cache.lens", cache.lens, i32, (shape.B,)))
+
+
+class _OnDevice:
+    """The cache's device as the current one, so that its stream and kernels are the ones used."""
+
+    def __init__(self, device):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"the cache must be on a GPU, not on {device}")
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def coli_kv_append(shape: KvShape, k_new, v_new, cache: KvCache, start=None, stream=None) -> None:
+    """k_new [rows][Hkv][Dk], v_new [rows][Hkv][Dv] (None for a latent cache); start int32 [B + 1] or None."""
+    import torch
+    rows, dev = k_new.shape[0], cache.k.device
+    _kv_check("coli_kv_append", dev, *_kv_cache_args(shape, cache),
+              ("k_new", k_new, _kv_dtype(shape), (rows, shape.Hkv, shape.Dk)),
+              ("v_new", v_new, _kv_dtype(shape), (rows, shape.Hkv, shape.Dv)),
+              ("start", start, torch.int32, (shape.B + 1,)))
+    cs, cc = shape.c(), cache.c()
+    with _OnDevice(dev):
+        _check(lib().coli_kv_append(C.byref(cs), _ptr(k_new), _ptr(v_new), rows, _ptr(start), C.byref(cc),
+                                    _stream(stream)), "coli_kv_append")
+
+
+def coli_kv_attn_workspace_bytes(shape: KvShape, idx_k: int = 0, acc: bool = False) -> int:
+    cs = shape.c()
+    return lib().coli_kv_attn_workspace_bytes(C.byref(cs), idx_k, 1 if acc else 0)
+
+
+def coli_kv_attn(shape: KvShape, q, cache: KvCache, out, scale: float, idx=None, acc_in=None, acc_out=None, lse=None,
+                 ws=None, ws_bytes=None, stream=None) -> None:
+    """q [B][Hq][Dk], out [B][Hq][Dv], lse fp32 [B][Hq], idx int32 [B][idx_k], acc fp32 [B][Hkv][ld]."""
+    import torch
+    B, f32, dev = shape.B, torch.float32, cache.k.device
+    ld = 0 if acc_out is None else acc_out.shape[-1]
+    idx_k = 0 if idx is None else idx.shape[-1]
+    _kv_check("coli_kv_attn", dev, *_kv_cache_args(shape, cache),
+              ("q", q, _kv_dtype(shape), (B, shape.Hq, shape.Dk)),
+              ("out", out, _kv_dtype(shape), (B, shape.Hq, shape.Dv)),
+              ("lse", lse, f32, (B, shape.Hq)), ("idx", idx, torch.int32, (B, idx_k)),
+              ("acc_in", acc_in, f32, (B, shape.Hkv, ld)), ("acc_out", acc_out, f32, (B, shape.Hkv, ld)))
+    cs, cc = shape.c(), cache.c()
+    with _OnDevice(dev):
+        _check(lib().coli_kv_attn(C.byref(cs), _ptr(q), C.byref(cc), scale, _ptr(idx), idx_k, _ptr(acc_in),
+                                  _ptr(acc_out), ld, _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws, ws_bytes),
+                                  _stream(stream)), "coli_kv_attn")
+
+
+def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_lens, kept, tail: int = 0, new_acc=None,
+                  stream=None) -> None:
+    """acc fp32 [B][Hkv][ld], new_table int32 [B][pages], new_lens int32 [B], kept int32 [B][Hkv][k],
+    new_acc fp32 [B][Hkv][new_ld]."""
+    import torch
+    B, H, f32, i32, dev = shape.B, shape.Hkv, torch.float32, torch.int32, cache.k.device
+    ld, cols = acc.shape[-1], new_table.shape[-1]
+    new_ld = 0 if new_acc is None else new_acc.shape[-1]
+    _kv_check("coli_kv_evict", dev, *_kv_cache_args(shape, cache), ("acc", acc, f32, (B, H, ld)),
+              ("new_table", new_table, i32, (B, cols)), ("new_lens", new_lens, i32, (B,)),
+              ("kept", kept, i32, (B, H, k)), ("new_acc", new_acc, f32, (B, H, new_ld)))
+    cs, cc = shape.c(), cache.c()
+    with _OnDevice(dev):
+        _check(lib().coli_kv_evict(C.byref(cs), C.byref(cc), _ptr(acc), ld, k, tail, _ptr(new_table), cols,
+                                   _ptr(new_lens), _ptr(kept), _ptr(new_acc), new_ld, _stream(stream)),
+               "coli_kv_evict")
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -152,6 +152,68 @@ coli_status check_dense_shape(const coli_moe_shape *s, coli_moe_shape *inner)
     return COLI_OK;
 }
 
+// ---- the paged key-value cache ------------------------------------------------
+coli_status check_kv_shape(const coli_kv_shape *s, bool latent)
+{
+    if (!s) return COLI_E_NULL;
+    if (s->dtype != COLI_F32 && s->dtype != COLI_BF16) return COLI_E_DTYPE;
+    if (s->B < 0 || s->Hkv < 1 || s->Hq < s->Hkv || s->Hq > 1024 || s->Hq % s->Hkv) return COLI_E_SHAPE;
+    if (s->Dk < 8 || s->Dv < 8 || s->Dk % 8 || s->Dv % 8) return COLI_E_SHAPE;
+    if (latent ? (s->Dv > s->Dk || s->Dk > 576 || s->Dv > 512) : (s->Dk > 256 || s->Dv > 256)) return COLI_E_SHAPE;
+    if (s->page < 1 || s->page > 4096 || (s->page & (s->page - 1))) return COLI_E_SHAPE;
+    if (s->n_pages < 1 || s->max_pages < 1) return COLI_E_SHAPE;
+    const int64_t cap = (int64_t)s->max_pages * s->page;
+    if (cap > (1 << 24)) return COLI_E_SHAPE;
+    // pool rows, and the attention's work in steps, fit in int32
+    if ((int64_t)s->n_pages * s->Hkv * s->page > INT32_MAX) return COLI_E_SHAPE;
+    if ((int64_t)s->B * s->Hq * (cap / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    return COLI_OK;
+}
+
+int page_shift(const coli_kv_shape *s)
+{
+    int n = 0;
+    while ((1 << n) < s->page) ++n;
+    return n;
+}
+
+size_t kv_elt(const coli_kv_shape *s) { return s->dtype == COLI_F32 ? 4 : 2; }
+size_t kv_pool_rows(const coli_kv_shape *s) { return (size_t)s->n_pages * s->Hkv * s->page; }
+
+coli_status check_kv_cache(const coli_kv_shape *s, const coli_kv_cache *c)
+{
+    if (!c) return COLI_E_NULL;
+    coli_status st = check_kv_shape(s, !c->v);
+    if (st != COLI_OK) return st;
+    if (s->B == 0) return COLI_OK;
+    if (!c->k || !c->table || !c->lens) return COLI_E_NULL;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->table) || !aligned16(c->lens)) return COLI_E_ALIGN;
+    return COLI_OK;
+}
+
+struct AttnWs {
+    size_t part_o, part_ml, stats, scores, total;
+    int q_tiles, n_wg, min_units;
+    long s_ld;
+};
+
+AttnWs attn_ws(const coli_kv_shape *s, bool acc)
+{
+    AttnWs w{};
+    const size_t heads = (size_t)s->B * s->Hq, cap = (size_t)s->max_pages * s->page;
+    w.q_tiles = coli::attn_q_tiles(s->Hq, s->Hkv);
+    w.n_wg = coli::attn_workgroups();
+    w.min_units = 8;
+    w.s_ld = (long)((cap + 31) / 32 * 32);
+    const size_t part_rows = (size_t)2 * w.n_wg * coli::attn_tile_rows();
+    w.part_o = 0;
+    w.part_ml = align_up(w.part_o + part_rows * s->Dv * 4);
+    w.stats = align_up(w.part_ml + part_rows * 8);
+    w.scores = align_up(w.stats + (acc ? heads * 8 : 0));
+    w.total = align_up(w.scores + (acc ? heads * (size_t)w.s_ld * 4 : 0));
+    return w;
+}
+
 // Kind of memory behind a pointer: 1 device, 2 pinned (registered or
 // hipHostMalloc) host memory, 0 anything else (pageable host memory, or a
 // pointer the runtime does not know).
@@ -198,7 +260,7 @@ coli_status scratch_for_current_device(void **out)
 
 extern "C" {
 
-int32_t coli_moe_version(void) { return 100; }
+int32_t coli_moe_version(void) { return 200; }
 
 const char *coli_moe_status_str(coli_status st)
 {
@@ -561,9 +623,135 @@ coli_status coli_index_topk(const float *scores, int32_t rows, int32_t L, int64_
     if (any_overlap(outs, 1, ins, 2)) return COLI_E_ALIAS;
     coli_status st = check_device();
     if (st != COLI_OK) return st;
-    return coli::launch_index_topk(scores, rows, L, (long)ld, lens, k, tail, idx, (hipStream_t)stream) == hipSuccess
+    return coli::launch_index_topk(scores, rows, L, (long)ld, lens, 1, k, tail, idx, (hipStream_t)stream) == hipSuccess
                ? COLI_OK
                : COLI_E_LAUNCH;
+}
+
+coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void *v_new, int32_t rows,
+                           const int32_t *start, const coli_kv_cache *c, void *stream)
+{
+    coli_status st = check_kv_cache(s, c);
+    if (st != COLI_OK) return st;
+    if (rows < 0 || (!start && rows != s->B)) return COLI_E_SHAPE;
+    if (s->B == 0 || rows == 0) return check_device();
+    if (!k_new || !v_new != !c->v) return COLI_E_NULL;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(start)) return COLI_E_ALIGN;
+    const size_t elt = kv_elt(s), pool = kv_pool_rows(s), news = (size_t)rows * s->Hkv;
+    const Region outs[] = {{c->k, pool * s->Dk * elt}, {c->v, pool * s->Dv * elt}};
+    const Region ins[] = {{k_new, news * s->Dk * elt}, {v_new, news * s->Dv * elt},
+                          {start, ((size_t)s->B + 1) * 4}, {c->table, (size_t)s->B * s->max_pages * 4},
+                          {c->lens, (size_t)s->B * 4}};
+    if (any_overlap(outs, 2, ins, 5)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    coli::AppendLaunch a{};
+    a.B = s->B; a.Hkv = s->Hkv; a.rows = rows;
+    a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
+    a.cap = s->max_pages * s->page;
+    a.k_chunks = (int)(s->Dk * elt / 16);
+    a.v_chunks = c->v ? (int)(s->Dv * elt / 16) : 0;
+    a.k_new = k_new; a.v_new = v_new; a.start = start;
+    a.table = c->table; a.lens = c->lens; a.k = c->k; a.v = c->v;
+    return coli::launch_kv_append(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+}
+
+size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32_t acc)
+{
+    // a shape that either kind of cache allows
+    if (check_kv_shape(s, false) != COLI_OK && check_kv_shape(s, true) != COLI_OK) return 0;
+    if (idx_k < 0 || idx_k > (1 << 24) || (idx_k && acc)) return 0;
+    const size_t n = attn_ws(s, acc != 0).total;
+    return n > 256 ? n : 256;
+}
+
+coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
+                         const int32_t *idx, int32_t idx_k, const float *acc_in, float *acc_out,
+                         int64_t ld, void *out, float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    coli_status st = check_kv_cache(s, c);
+    if (st != COLI_OK) return st;
+    const int32_t cap = s->max_pages * s->page;
+    const double sc = (double)scale * 1.4426950408889634074;     // exponents are taken to base 2
+    if (!(sc >= -3e38 && sc <= 3e38)) return COLI_E_SHAPE;
+    if (idx ? (idx_k < 1 || idx_k > (1 << 24) || acc_out) : idx_k != 0) return COLI_E_SHAPE;
+    if (idx && (int64_t)s->B * s->Hq * (idx_k / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if (acc_in && !acc_out) return COLI_E_NULL;
+    if (acc_out && (ld < cap || ld % 4)) return COLI_E_SHAPE;
+    if (s->B == 0) return check_device();
+    if (!q || !out || !ws) return COLI_E_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || !aligned16(idx) || !aligned16(acc_in) ||
+        !aligned16(acc_out) || !aligned16(lse))
+        return COLI_E_ALIGN;
+    const AttnWs L = attn_ws(s, acc_out != nullptr);
+    if (ws_bytes < L.total) return COLI_E_WORKSPACE;
+    const size_t elt = kv_elt(s), pool = kv_pool_rows(s), heads = (size_t)s->B * s->Hq;
+    const size_t accb = acc_out ? (size_t)s->B * s->Hkv * ld * 4 : 0;
+    const Region outs[] = {{out, heads * s->Dv * elt}, {lse, heads * 4}, {acc_out, accb}, {ws, L.total}};
+    const Region ins[] = {{q, heads * s->Dk * elt}, {c->k, pool * s->Dk * elt}, {c->v, pool * s->Dv * elt},
+                          {c->table, (size_t)s->B * s->max_pages * 4}, {c->lens, (size_t)s->B * 4},
+                          {idx, (size_t)s->B * idx_k * 4}, {acc_in, accb}};
+    if (any_overlap(outs, 4, ins, 7, acc_in == acc_out ? (const void *)acc_out : nullptr)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    coli::AttnLaunch a{};
+    a.B = s->B; a.Hq = s->Hq; a.Hkv = s->Hkv; a.Dk = s->Dk; a.Dv = s->Dv;
+    a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
+    a.cap = cap;
+    a.bf16 = s->dtype == COLI_BF16;
+    a.q = q; a.k = c->k; a.v = c->v;
+    a.table = c->table; a.lens = c->lens; a.idx = idx; a.idx_k = idx_k;
+    // scale * log2(e) as the sum of two floats, without the error that one
+    // rounded factor would put on every large score
+    a.scale_hi = (float)sc;
+    a.scale_lo = (float)(sc - (double)a.scale_hi);
+    a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
+    a.q_tiles = L.q_tiles; a.n_wg = L.n_wg; a.min_units = L.min_units;
+    char *base = (char *)ws;
+    a.part_o = (float *)(base + L.part_o);
+    a.part_ml = (float *)(base + L.part_ml);
+    a.stats = acc_out ? (float *)(base + L.stats) : nullptr;
+    a.scores = acc_out ? (float *)(base + L.scores) : nullptr;
+    a.s_ld = L.s_ld;
+    return coli::launch_attn(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+}
+
+coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const float *acc, int64_t ld,
+                          int32_t k, int32_t tail, const int32_t *new_table, int32_t new_max_pages,
+                          int32_t *new_lens, int32_t *kept, float *new_acc, int64_t new_ld,
+                          void *stream)
+{
+    coli_status st = check_kv_cache(s, c);
+    if (st != COLI_OK) return st;
+    const int32_t cap = s->max_pages * s->page;
+    if (k < 1 || k > (1 << 24) || tail < 0 || ld < cap || ld % 4) return COLI_E_SHAPE;
+    if (new_max_pages < 1 || (int64_t)new_max_pages * s->page < k) return COLI_E_SHAPE;
+    if (new_acc && (new_ld < k || new_ld > (1 << 25))) return COLI_E_SHAPE;
+    const int64_t span = new_acc && new_ld > k ? new_ld : k;
+    if ((int64_t)s->B * s->Hkv * (span / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if (s->B == 0) return check_device();
+    if (!acc || !new_table || !new_lens || !kept) return COLI_E_NULL;
+    if (!aligned16(acc) || !aligned16(new_table) || !aligned16(new_lens) || !aligned16(kept) || !aligned16(new_acc))
+        return COLI_E_ALIGN;
+    const size_t elt = kv_elt(s), pool = kv_pool_rows(s), heads = (size_t)s->B * s->Hkv;
+    const Region outs[] = {{new_lens, (size_t)s->B * 4}, {kept, heads * k * 4},
+                           {new_acc, new_acc ? heads * new_ld * 4 : 0}, {c->k, pool * s->Dk * elt},
+                           {c->v, pool * s->Dv * elt}};
+    const Region ins[] = {{acc, heads * ld * 4}, {c->table, (size_t)s->B * s->max_pages * 4},
+                          {c->lens, (size_t)s->B * 4}, {new_table, (size_t)s->B * new_max_pages * 4}};
+    if (any_overlap(outs, 5, ins, 4)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    coli::EvictLaunch a{};
+    a.B = s->B; a.Hkv = s->Hkv;
+    a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
+    a.new_max_pages = new_max_pages; a.cap = cap;
+    a.k_chunks = (int)(s->Dk * elt / 16);
+    a.v_chunks = c->v ? (int)(s->Dv * elt / 16) : 0;
+    a.k = c->k; a.v = c->v; a.table = c->table; a.lens = c->lens;
+    a.acc = acc; a.ld = (long)ld; a.keep = k; a.tail = tail;
+    a.new_table = new_table; a.new_lens = new_lens; a.kept = kept; a.new_acc = new_acc; a.new_ld = (long)new_ld;
+    return coli::launch_kv_evict(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
 }
 
 coli_status coli_moe_ffn_noalloc(const coli_moe_shape *s, const void *x, const coli_moe_routing *r,

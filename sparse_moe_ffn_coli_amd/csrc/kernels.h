@@ -1,5 +1,5 @@
 // kernels.h -- internal launch interface between the C ABI (api.hip) and the
-// kernels (route.hip, ffn.hip).  Not part of the public interface.
+// kernels (route.hip, ffn.hip, select.hip, attend.hip, kvcache.hip).  Not part of the public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -61,9 +61,62 @@ struct FfnLaunch {
     StageMarks *marks;     // nullable
 };
 
+struct AttnLaunch {
+    int B, Hq, Hkv, Dk, Dv;
+    int page_shift, n_pages, max_pages;
+    int cap;               // max_pages * page: the longest length
+    bool bf16;
+    const void *q, *k, *v; // v NULL: latent cache
+    const int32_t *table, *lens, *idx;
+    int idx_k;
+    float scale_hi, scale_lo;   // scale * log2(e) in two floats
+    void *out;
+    float *lse;            // nullable
+    const float *acc_in;
+    float *acc_out;        // nullable
+    long ld;
+    int q_tiles;           // query tiles per cache head
+    int n_wg, min_units;   // ranges of the main kernel; fewest steps in one
+    float *part_o;         // workspace [2 n_wg][tile rows][Dv]: unnormalised parts
+    float *part_ml;        // workspace [2 n_wg][tile rows][2]: their references and sums
+    float *stats;          // workspace [B][Hq][2]: reference and 1 / sum (running weights only)
+    float *scores;         // workspace [B][Hq][s_ld]: scores in units of log2 e (running weights only)
+    long s_ld;
+};
+
+struct AppendLaunch {
+    int B, Hkv, rows, page_shift, n_pages, max_pages, cap;
+    int k_chunks, v_chunks;     // 16-byte chunks of a key and a value (0: latent)
+    const void *k_new, *v_new;
+    const int32_t *start, *table, *lens;
+    void *k, *v;
+};
+
+struct EvictLaunch {
+    int B, Hkv, page_shift, n_pages, max_pages, new_max_pages, cap;
+    int k_chunks, v_chunks;
+    void *k, *v;
+    const int32_t *table, *lens;
+    const float *acc;
+    long ld;
+    int keep, tail;
+    const int32_t *new_table;
+    int32_t *new_lens, *kept;
+    float *new_acc;        // nullable
+    long new_ld;
+};
+
+hipError_t launch_attn(const AttnLaunch &a, hipStream_t st);
+hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
+hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
+int attn_workgroups();
+int attn_q_tiles(int Hq, int Hkv);
+int attn_tile_rows();
+
 hipError_t launch_route(const RouteLaunch &a, hipStream_t st);
-hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, const int32_t *lens, int k, int tail,
-                             int32_t *idx, hipStream_t st);
+// rows_per_len consecutive rows share an entry of lens
+hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, const int32_t *lens, int rows_per_len,
+                             int k, int tail, int32_t *idx, hipStream_t st);
 hipError_t launch_ffn(const FfnLaunch &a, hipStream_t st);
 
 int perm_tiles(int T);

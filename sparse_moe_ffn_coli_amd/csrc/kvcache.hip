@@ -1,0 +1,117 @@
+// kvcache.hip -- writing a paged key-value cache: new tokens' rows into their
+// sequences' pages, and the copy of an eviction's kept rows into new pages.
+// Both move rows of 16-byte chunks and nothing else: bound by the bytes read
+// and written.
+#include "device_common.h"
+#include "kernels.h"
+
+namespace coli {
+
+constexpr int KVC_NT = 256;
+
+// Pool row of position p of cache head h, -1 where the page id is none.
+__device__ __forceinline__ int pool_row(const int32_t *__restrict__ table_row, int p, int h, int Hkv, int page_shift,
+                                        int n_pages)
+{
+    const int pg = table_row[p >> page_shift];
+    if (pg < 0 || pg >= n_pages) return -1;
+    return (int)((((uint32_t)pg * (uint32_t)Hkv + (uint32_t)h) << page_shift) +
+                 (uint32_t)(p & ((1 << page_shift) - 1)));
+}
+
+// One workgroup per new token.  The sequence of row r is the last b with
+// start[b] <= r (found by halving; start ascends), its position lens[b] -
+// (start[b + 1] - r).
+__global__ __launch_bounds__(KVC_NT) void kv_append_kernel(AppendLaunch a)
+{
+    const int r = blockIdx.x;
+    int b = r, p;
+    if (a.start) {
+        int lo = 0, hi = a.B;                     // start[lo] <= r < start[hi], if any
+        if (r < a.start[0] || r >= a.start[a.B]) return;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.start[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        p = min(max(a.lens[b], 0), a.cap) - a.start[b + 1] + r;
+    } else {
+        p = min(max(a.lens[b], 0), a.cap) - 1;
+    }
+    if (p < 0 || p >= a.cap) return;
+    const int per = a.k_chunks + a.v_chunks;
+    const u32x4 *kn = (const u32x4 *)a.k_new, *vn = (const u32x4 *)a.v_new;
+    u32x4 *k = (u32x4 *)a.k, *v = (u32x4 *)a.v;
+    const int32_t *row = a.table + (size_t)b * a.max_pages;
+    for (int i = threadIdx.x; i < a.Hkv * per; i += KVC_NT) {
+        const int h = i / per, c = i % per;
+        const int to = pool_row(row, p, h, a.Hkv, a.page_shift, a.n_pages);
+        if (to < 0) return;
+        const size_t from = (size_t)r * a.Hkv + h;
+        if (c < a.k_chunks) k[(size_t)to * a.k_chunks + c] = kn[from * a.k_chunks + c];
+        else v[(size_t)to * a.v_chunks + c - a.k_chunks] = vn[from * a.v_chunks + c - a.k_chunks];
+    }
+}
+
+hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st)
+{
+    if (a.rows == 0 || a.B == 0) return hipSuccess;
+    kv_append_kernel<<<a.rows, KVC_NT, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+// The kept rows of one (sequence, cache head), EV_ROWS a workgroup: their old
+// and new pool rows go through LDS once, then the chunks of all of them are
+// copied side by side.  The same workgroups write the kept weights, the zeros
+// behind them and the new length.
+constexpr int EV_ROWS = 64;
+
+__global__ __launch_bounds__(KVC_NT) void kv_evict_copy_kernel(EvictLaunch a, int blocks)
+{
+    __shared__ int32_t from[EV_ROWS], to[EV_ROWS];
+    const int tid = threadIdx.x;
+    const int bh = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    const int b = bh / a.Hkv, h = bh % a.Hkv;
+    const int n = min(max(a.lens[b], 0), a.cap), m = min(n, a.keep);
+    const int j0 = blk * EV_ROWS;
+    if (blk == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
+    if (tid < EV_ROWS && j0 + tid < max((long)m, a.new_acc ? a.new_ld : 0)) {
+        const int j = j0 + tid;
+        float w = 0.f;
+        if (j < m) {
+            const int p = a.kept[(size_t)bh * a.keep + j];
+            from[tid] = pool_row(a.table + (size_t)b * a.max_pages, p, h, a.Hkv, a.page_shift, a.n_pages);
+            to[tid] = pool_row(a.new_table + (size_t)b * a.new_max_pages, j, h, a.Hkv, a.page_shift, a.n_pages);
+            w = a.acc[(size_t)bh * a.ld + p];
+        }
+        if (a.new_acc && j < a.new_ld) a.new_acc[(size_t)bh * a.new_ld + j] = w;
+    }
+    __syncthreads();
+    const int rows = min(EV_ROWS, m - j0);
+    u32x4 *k = (u32x4 *)a.k, *v = (u32x4 *)a.v;
+    for (int i = tid; i < rows * a.k_chunks; i += KVC_NT) {
+        const int r = i / a.k_chunks, c = i % a.k_chunks;
+        if (from[r] >= 0 && to[r] >= 0)
+            k[(size_t)to[r] * a.k_chunks + c] = k[(size_t)from[r] * a.k_chunks + c];
+    }
+    for (int i = tid; i < rows * a.v_chunks; i += KVC_NT) {
+        const int r = i / a.v_chunks, c = i % a.v_chunks;
+        if (from[r] >= 0 && to[r] >= 0)
+            v[(size_t)to[r] * a.v_chunks + c] = v[(size_t)from[r] * a.v_chunks + c];
+    }
+}
+
+hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st)
+{
+    if (a.B == 0) return hipSuccess;
+    const hipError_t e =
+        launch_index_topk(a.acc, a.B * a.Hkv, a.cap, a.ld, a.lens, a.Hkv, a.keep, a.tail, a.kept, st);
+    if (e != hipSuccess) return e;
+    const long span = a.new_acc && a.new_ld > a.keep ? a.new_ld : a.keep;
+    const int blocks = (int)((span + EV_ROWS - 1) / EV_ROWS);
+    kv_evict_copy_kernel<<<a.B * a.Hkv * blocks, KVC_NT, 0, st>>>(a, blocks);
+    return hipGetLastError();
+}
+
+}  // namespace coli

@@ -310,8 +310,9 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
 // a cached row is being selected, the next row's scores are already loading
 // into registers, so the row reads overlap the selection work.
 __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restrict__ scores, int rows, int L,
-                                                            long ld, const int32_t *__restrict__ lens, int k,
-                                                            int tail, int32_t *__restrict__ idx)
+                                                            long ld, const int32_t *__restrict__ lens,
+                                                            int rows_per_len, int k, int tail,
+                                                            int32_t *__restrict__ idx)
 {
     __shared__ __attribute__((aligned(16))) uint32_t keys[SEL_CAP];
     __shared__ int32_t hist[2048];
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
     __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
     __shared__ __attribute__((aligned(16))) int32_t staged[SEL_MAX_K];   // the output row
     const int tid = threadIdx.x;
-    auto row_len = [&](int r) { return lens ? min(max(lens[r], 0), L) : L; };
+    auto row_len = [&](int r) { return lens ? min(max(lens[r / rows_per_len], 0), L) : L; };
     for (int b = tid; b < 2048; b += SEL_NT) hist[b] = 0;
     f32x4 v[SEL_PER];
     int have = -1;                                // the row whose scores are in v
@@ -389,10 +390,13 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
     }
 }
 
-// Rows longer than SEL_CAP: one workgroup per row, every pass re-reading the
-// scores; the other rows are left to index_topk_kernel.
+// Rows longer than `skip` positions: one workgroup per row, every pass
+// re-reading the scores; the other rows are left to index_topk_kernel (skip =
+// SEL_CAP), or there are none (skip = -1: k past SEL_MAX_K, whose output row
+// the other kernels cannot stage).
 __global__ __launch_bounds__(SEL_NT) void index_topk_long_kernel(const float *__restrict__ scores, int L, long ld,
-                                                                 const int32_t *__restrict__ lens, int k, int tail,
+                                                                 const int32_t *__restrict__ lens,
+                                                                 int rows_per_len, int skip, int k, int tail,
                                                                  int32_t *__restrict__ idx)
 {
     __shared__ int32_t hist[2048];
@@ -400,8 +404,12 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_long_kernel(const float *__
     __shared__ int32_t sel_s[2];
     __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
     const int r = blockIdx.x;
-    const int n = lens ? min(max(lens[r], 0), L) : L;
-    if (n <= SEL_CAP) return;
+    const int n = lens ? min(max(lens[r / rows_per_len], 0), L) : L;
+    if (n <= skip) return;
+    if (n <= k) {                                 // the whole row, then -1
+        for (int j = threadIdx.x; j < k; j += SEL_NT) idx[(size_t)r * k + j] = j < n ? j : -1;
+        return;
+    }
     for (int b = threadIdx.x; b < 2048; b += SEL_NT) hist[b] = 0;
     __syncthreads();
     select_uncached(scores + (size_t)r * ld, n, n - min(tail, k), k, hist, ws, sel_s, wave_gt, wave_eq,
@@ -475,8 +483,8 @@ __device__ __forceinline__ int sr_pick_bin(int32_t *hist, int nb, int need, int3
 }
 
 __global__ __launch_bounds__(SR_NT) __attribute__((amdgpu_waves_per_eu(SR_NT / 128))) void index_topk_reg_kernel(
-    const float *__restrict__ scores, int L, long ld, const int32_t *__restrict__ lens, int k, int tail,
-    int32_t *__restrict__ idx)
+    const float *__restrict__ scores, int L, long ld, const int32_t *__restrict__ lens, int rows_per_len, int k,
+    int tail, int32_t *__restrict__ idx)
 {
     __shared__ int32_t hist[2048];
     __shared__ int32_t ws[SR_WAVES];
@@ -485,7 +493,7 @@ __global__ __launch_bounds__(SR_NT) __attribute__((amdgpu_waves_per_eu(SR_NT / 1
     __shared__ __attribute__((aligned(16))) int32_t staged[SEL_MAX_K];        // the output row
     const int r = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n = lens ? min(max(lens[r], 0), L) : L;
+    const int n = lens ? min(max(lens[r / rows_per_len], 0), L) : L;
     int32_t *__restrict__ out = idx + (size_t)r * k;
     if (n <= k) {                                 // the whole row, then -1
         for (int j = tid; j < k; j += SR_NT) out[j] = j < n ? j : -1;
@@ -618,22 +626,27 @@ __global__ __launch_bounds__(SR_NT) __attribute__((amdgpu_waves_per_eu(SR_NT / 1
     }
 }
 
-hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, const int32_t *lens, int k, int tail,
-                             int32_t *idx, hipStream_t st)
+hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, const int32_t *lens, int rows_per_len,
+                             int k, int tail, int32_t *idx, hipStream_t st)
 {
     if (rows == 0) return hipSuccess;
+    if (k > SEL_MAX_K) {
+        index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, -1, k, tail, idx);
+        return hipGetLastError();
+    }
     // more rows than CUs: the register-key kernel; otherwise one workgroup
     // per CU (the key cache fills most of a CU's LDS), each walking its
     // share of the rows
     if (rows > SEL_REG_MIN_ROWS) {
         // two rows in flight per CU (64 rows: 28.2 us here against 24.4 us
         // for one cached-row workgroup per CU, each row's latency deciding)
-        index_topk_reg_kernel<<<rows, SR_NT, 0, st>>>(scores, L, ld, lens, k, tail, idx);
+        index_topk_reg_kernel<<<rows, SR_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, k, tail, idx);
     } else {
         const int grid = min(rows, 256);
-        index_topk_kernel<<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, k, tail, idx);
+        index_topk_kernel<<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
     }
-    if (L > SEL_CAP && L > k) index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, k, tail, idx);
+    if (L > SEL_CAP && L > k)
+        index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, SEL_CAP, k, tail, idx);
     return hipGetLastError();
 }
 

@@ -1,0 +1,550 @@
+"""Paged key-value cache (append, attention of one new token, eviction by
+running weight) through the C ABI against plain 64-bit forms
+(tests/kv_reference.py, which also derives the bounds).  Rows of the pools
+that no position owns hold NaN and infinities throughout."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+from sparse_moe_ffn_coli_amd import (COLI_BF16, COLI_F32, KvCache, KvShape, coli_index_topk, coli_kv_append,
+                                     coli_kv_attn, coli_kv_attn_workspace_bytes, coli_kv_evict)
+
+pytestmark = pytest.mark.gpu
+
+
+def shape_of(c, B, Hq):
+    return KvShape(B=B, Hq=Hq, Hkv=c["Hkv"], Dk=c["Dk"], Dv=c["Dv"], page=c["page"], n_pages=c["n_pages"],
+                   max_pages=c["max_pages"], dtype=COLI_F32 if c["dtype"] == "f32" else COLI_BF16)
+
+
+def cache_of(c):
+    return KvCache(c["k"].cuda(), None if c["v"] is None else c["v"].cuda(), c["table"].cuda(), c["lens"].cuda())
+
+
+def bits(t):
+    import torch
+    return t.view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+def guarded(shape, dtype, fill):
+    """A tensor inside a larger buffer of `fill`; the second value checks that the buffer's rest is untouched."""
+    import torch
+    n = int(np.prod(shape))
+    buf = torch.full((n + 512,), fill, dtype=dtype, device="cuda")
+    view = buf[256:256 + n].view(shape)
+
+    def check():
+        rest = torch.cat([buf[:256], buf[256 + n:]])
+        assert bool((rest == fill).all()), "written outside an output"
+    return view, check
+
+
+def queries(c, B, Hq, seed=1):
+    import torch
+    q = np.random.default_rng(seed).standard_normal((B, Hq, c["Dk"])).astype(np.float32)
+    return torch.from_numpy(q).to(torch.float32 if c["dtype"] == "f32" else torch.bfloat16)
+
+
+def within(got, want, tol, label):
+    got = np.asarray(got, np.float64)
+    empty = np.isneginf(want)
+    assert np.array_equal(np.isneginf(got), empty), f"{label}: other rows are empty"
+    got, want, tol = got[~empty], want[~empty], tol[~empty]
+    assert np.all(np.isfinite(got)), f"{label}: not finite"
+    over = np.abs(got - want) - tol
+    assert over.size == 0 or over.max() <= 0, f"{label}: {over.max():.3e} over the bound, worst error {np.abs(got - want).max():.3e}"
+
+
+def run_attn(c, Hq, scale, idx=None, acc_in=None, in_place=False, q=None, want=True):
+    import torch
+    B = len(c["lens"])
+    q = queries(c, B, Hq) if q is None else q
+    s, cache = shape_of(c, B, Hq), cache_of(c)
+    dt = q.dtype
+    out, out_ok = guarded((B, Hq, c["Dv"]), dt, 7.0)
+    lse, lse_ok = guarded((B, Hq), torch.float32, 7.0)
+    kw, checks = {}, [out_ok, lse_ok]
+    if idx is not None:
+        kw["idx"] = torch.from_numpy(idx).cuda()
+    acc_out = None
+    if acc_in is not None:
+        acc_out, ok = guarded(acc_in.shape, torch.float32, 7.0)
+        checks.append(ok)
+        kw["acc_out"] = acc_out
+        if in_place:
+            acc_out.copy_(torch.from_numpy(acc_in))
+            kw["acc_in"] = acc_out
+        else:
+            kw["acc_in"] = torch.from_numpy(acc_in).cuda()
+    nb = coli_kv_attn_workspace_bytes(s, idx_k=0 if idx is None else idx.shape[1], acc=acc_in is not None)
+    ws, ws_ok = guarded((nb,), torch.uint8, 0xA5)
+    # a second pass on the same workspace: nothing may depend on what the first left there
+    coli_kv_attn(s, q.cuda(), cache, out, scale, lse=lse, ws=ws, **kw)
+    if not in_place:
+        coli_kv_attn(s, q.cuda(), cache, out, scale, lse=lse, ws=ws, **kw)
+    torch.cuda.synchronize()
+    for ok in checks + [ws_ok]:
+        ok()
+    if not want:
+        return out.cpu(), lse.cpu(), None if acc_out is None else acc_out.cpu()
+    r = ref.attn(c, q, scale, idx, acc_in)
+    label = f"{c['dtype']} B={B} Hq={Hq} Hkv={c['Hkv']} D={c['Dk']}/{c['Dv']} page={c['page']}"
+    within(out.double().cpu().numpy(), r["out"], r["tol_out"], label + " out")
+    within(lse.cpu().numpy(), r["lse"], r["tol_lse"], label + " lse")
+    if acc_in is not None:
+        got = acc_out.cpu().numpy()
+        for b, n in enumerate(c["lens"].tolist()):
+            within(got[b, :, :n], r["acc"][b, :, :n], r["tol_acc"][b, :, :n], label + " acc")
+            rest = got[b, :, n:]
+            assert np.array_equal(rest, acc_in[b, :, n:] if in_place else np.full_like(rest, 7.0)), "acc behind a length"
+    print(label, "ok", flush=True)
+    return out.cpu(), lse.cpu(), None if acc_out is None else acc_out.cpu()
+
+
+BORDERS = [0, 1, 2, 31, 32, 33, 63, 65, 127, 128, 129, 257, 500]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,Dk,Dv,page,latent", [
+    (8, 2, 64, 64, 16, False),
+    (3, 3, 8, 8, 1, False),               # the smallest heads, one position a page
+    (12, 12, 80, 80, 2, False),           # widths that fill no tile
+    (14, 2, 128, 128, 64, False),
+    (5, 1, 96, 40, 4, False),             # values narrower than keys
+    (4, 2, 72, 136, 8, False),            # and wider
+    (34, 2, 192, 128, 32, False),         # 17 query heads: a second tile of one
+    (16, 1, 256, 256, 128, False),
+    (6, 2, 256, 200, 512, False),         # pages longer than every sequence
+    (32, 1, 128, 64, 16, True),           # a latent cache of a small width
+    (16, 1, 576, 512, 64, True),
+    (20, 1, 576, 512, 16, True),
+    (33, 1, 512, 512, 16, True),
+    (100, 1, 320, 256, 32, True),
+    (8, 4, 296, 264, 8, True),            # several latent heads, widths just past a tile
+    (64, 1, 576, 512, 64, True),
+    (128, 1, 576, 512, 64, True),
+])
+def test_attn_layouts(dtype, Hq, Hkv, Dk, Dv, page, latent):
+    c = ref.make_cache(BORDERS, Hkv, Dk, Dv, page, dtype, latent, seed=Hq * 1000 + Dk)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_attn_scales(scale):
+    # 3.0: scores of several hundred, weights that underflow, references that move far
+    c = ref.make_cache([700, 1, 45], 2, 128, 128, 16, "f32", seed=4)
+    run_attn(c, 8, scale)
+
+
+@pytest.mark.parametrize("dtype,latent,Hq,Dk,Dv", [("bf16", False, 8, 128, 128), ("f32", False, 2, 64, 64),
+                                                   ("bf16", True, 64, 576, 512)])
+def test_attn_one_long_sequence(dtype, latent, Hq, Dk, Dv):
+    # cut over every range; the parts are joined
+    c = ref.make_cache([20011], 1 if latent else 2, Dk, Dv, 16, dtype, latent, seed=5)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk))
+
+
+def test_attn_one_position():
+    c = ref.make_cache([1], 2, 64, 64, 16, "bf16", seed=6)
+    out, lse, _ = run_attn(c, 4, 0.125)
+
+
+def test_attn_more_sequences_than_threads():
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 150, size=700)
+    lens[:300] = 0                        # a run of empty ones longer than a scan's width
+    c = ref.make_cache(lens, 1, 64, 64, 16, "bf16", seed=7)
+    run_attn(c, 3, 0.25)
+
+
+def test_attn_nothing_anywhere():
+    c = ref.make_cache([0, 0, 0], 2, 64, 64, 16, "bf16", seed=8)
+    out, lse, _ = run_attn(c, 4, 0.125)
+    assert bool((out == 0).all())
+
+
+def test_attn_lengths_outside_the_table():
+    import torch
+    c = ref.make_cache([40, 64], 1, 64, 64, 16, "f32", seed=9, extra_cols=0)
+    want = run_attn(c, 2, 0.2)
+    c["lens"] = torch.tensor([40, 1 << 30], dtype=torch.int32)        # clamped to max_pages * page = 64
+    got = run_attn(c, 2, 0.2, want=False)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c["lens"] = torch.tensor([-5, 64], dtype=torch.int32)
+    got = run_attn(c, 2, 0.2, want=False)
+    assert bool((got[0][0] == 0).all()) and torch.equal(got[0][1], want[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("latent,Hq,Dk,Dv", [(False, 6, 128, 128), (True, 40, 576, 512)])
+def test_attn_hidden_pages(dtype, latent, Hq, Dk, Dv):
+    # pages that do not exist inside a sequence; the second has none at all
+    c = ref.make_cache([200, 90, 33], 1 if latent else 2, Dk, Dv, 8, dtype, latent, seed=10)
+    c["table"][0, 3] = -1
+    c["table"][0, 7:9] = c["n_pages"]
+    c["table"][1, :] = -7
+    c["table"][2, 0] = 1 << 30
+    acc = np.random.default_rng(1).random((3, c["Hkv"], c["max_pages"] * 8)).astype(np.float32)
+    run_attn(c, Hq, 0.1, acc_in=acc)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,Dk,Dv,page,latent", [
+    ("bf16", 8, 2, 128, 128, 16, False), ("f32", 4, 4, 80, 80, 32, False), ("bf16", 34, 2, 64, 64, 4, False),
+    ("bf16", 64, 1, 576, 512, 64, True), ("f32", 18, 1, 576, 512, 64, True), ("bf16", 7, 1, 256, 256, 16, False)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_attn_running_weights(dtype, Hq, Hkv, Dk, Dv, page, latent, in_place):
+    c = ref.make_cache([0, 1, 33, 1030, 515, 2048], Hkv, Dk, Dv, page, dtype, latent, seed=11)
+    ld = -(-c["max_pages"] * page // 4) * 4 + 8
+    acc = np.random.default_rng(2).random((6, Hkv, ld)).astype(np.float32)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), acc_in=acc, in_place=in_place)
+
+
+def test_attn_running_weights_from_zero():
+    import torch
+    c = ref.make_cache([100, 64], 2, 64, 64, 16, "f32", seed=12)
+    s, cache, q = shape_of(c, 2, 4), cache_of(c), queries(c, 2, 4)
+    acc = torch.full((2, 2, c["max_pages"] * 16), 5.0, device="cuda")
+    out = torch.empty((2, 4, 64), device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s, acc=True), dtype=torch.uint8, device="cuda")
+    coli_kv_attn(s, q.cuda(), cache, out, 0.25, acc_out=acc, ws=ws)
+    r = ref.attn(c, q, 0.25, acc_in=np.zeros(acc.shape, np.float32))
+    for b, n in enumerate([100, 64]):
+        within(acc[b, :, :n].cpu().numpy(), r["acc"][b, :, :n], r["tol_acc"][b, :, :n], "acc")
+        # the weights of a cache head's query heads sum to their number
+        assert np.abs(acc[b, :, :n].double().sum(-1).cpu().numpy() - 2.0).max() < 1e-4
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,Dk,Dv,page,latent,k", [
+    ("bf16", 8, 2, 128, 128, 16, False, 77), ("f32", 3, 3, 64, 64, 1, False, 32), ("bf16", 64, 1, 576, 512, 64, True, 300),
+    ("f32", 20, 1, 576, 512, 8, True, 65), ("bf16", 16, 1, 576, 512, 64, True, 1)])
+def test_attn_listed_positions(dtype, Hq, Hkv, Dk, Dv, page, latent, k):
+    lens = [0, 1, 40, 1000, 512, 77]
+    c = ref.make_cache(lens, Hkv, Dk, Dv, page, dtype, latent, seed=13)
+    rng = np.random.default_rng(3)
+    idx = rng.integers(-3, 1200, size=(6, k)).astype(np.int32)       # -1s in between, positions past the end, doubles
+    idx[4] = -1                                                      # nothing listed
+    idx[5, :] = 5                                                    # one position, k times
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), idx=idx)
+
+
+def test_attn_listed_extreme_positions():
+    c = ref.make_cache([100], 1, 64, 64, 16, "bf16", seed=14)
+    idx = np.array([[-2 ** 31, 2 ** 31 - 1, 99, 100, 0, -1]], np.int32)
+    run_attn(c, 4, 0.2, idx=idx)
+
+
+def test_attn_over_an_index_selection():
+    """The two together: positions selected by index scores, then attention over them."""
+    import torch
+    rng = np.random.default_rng(15)
+    lens, k, tail = [900, 100, 2500, 0], 256, 4
+    c = ref.make_cache(lens, 1, 576, 512, 64, "bf16", True, seed=15)
+    L = c["max_pages"] * 64
+    scores = torch.from_numpy(rng.standard_normal((4, L)).astype(np.float32)).cuda()
+    idx = torch.empty((4, k), dtype=torch.int32, device="cuda")
+    s, cache, q = shape_of(c, 4, 64), cache_of(c), queries(c, 4, 64)
+    coli_index_topk(scores, k, idx, tail=tail, lens=cache.lens)
+    out = torch.empty((4, 64, 512), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s, idx_k=k), dtype=torch.uint8, device="cuda")
+    coli_kv_attn(s, q.cuda(), cache, out, 0.08, idx=idx, ws=ws)
+    r = ref.attn(c, q, 0.08, idx=idx.cpu().numpy())
+    within(out.double().cpu().numpy(), r["out"], r["tol_out"], "out")
+
+
+def test_attn_repeats_bitwise():
+    import torch
+    c = ref.make_cache([3000, 17, 900], 2, 128, 128, 16, "bf16", seed=16)
+    a = run_attn(c, 8, 0.2, want=False)
+    for _ in range(3):
+        b = run_attn(c, 8, 0.2, want=False)
+        assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(bits(a[1]), bits(b[1]))
+
+
+def test_attn_offsets_past_32_bits():
+    """A pool of more than 2^32 elements; the sequence's pages lie at its end and its start."""
+    import torch
+    page, D, Hkv = 4096, 256, 4
+    n_pages = 1100                        # 1100 * 4 * 4096 * 256 = 4.6e9 elements, 9.2 GB a pool
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros((n_pages, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    for pg in (0, n_pages - 1):
+        k[pg] = torch.randn(k[pg].shape, generator=g, device="cuda").bfloat16()
+        v[pg] = torch.randn(k[pg].shape, generator=g, device="cuda").bfloat16()
+    table = torch.tensor([[n_pages - 1, 0]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([page + 100], dtype=torch.int32, device="cuda")
+    s = KvShape(1, 4, Hkv, D, D, page, n_pages, 2, COLI_BF16)
+    q = torch.randn((1, 4, D), generator=g, device="cuda").bfloat16()
+    out = torch.empty((1, 4, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    coli_kv_attn(s, q, KvCache(k, v, table, lens), out, 0.1, ws=ws)
+    c = dict(k=torch.cat([k[-1:], k[:1]]).cpu(), v=torch.cat([v[-1:], v[:1]]).cpu(), table=torch.tensor([[0, 1]]),
+             lens=lens.cpu(), page=page, n_pages=2, max_pages=2, Hkv=Hkv, Dk=D, Dv=D, dtype="bf16")
+    r = ref.attn(c, q.cpu(), 0.1)
+    within(out.double().cpu().numpy(), r["out"], r["tol_out"], "out")
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+
+def same_pool(got, want, label):
+    import torch
+    assert torch.equal(bits(got.cpu()), bits(want)), f"{label}: the pool differs"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("latent,Hkv,Dk,Dv,page", [(False, 2, 64, 64, 16), (False, 5, 80, 40, 1), (True, 1, 576, 512, 64),
+                                                   (False, 12, 128, 128, 8), (False, 1, 8, 8, 2)])
+def test_append_ragged(dtype, latent, Hkv, Dk, Dv, page):
+    import torch
+    lens, news = [50, 0, 7, 130, 1, 64], [50, 0, 3, 30, 1, 0]
+    c = ref.make_cache(lens, Hkv, Dk, Dv, page, dtype, latent, seed=21)
+    start = np.concatenate([[2], 2 + np.cumsum(news)]).astype(np.int32)      # two rows before the first sequence
+    rows = int(start[-1]) + 3                                               # three behind the last
+    rng = np.random.default_rng(1)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    k_new = torch.from_numpy(rng.standard_normal((rows, Hkv, Dk)).astype(np.float32)).to(dt)
+    v_new = None if latent else torch.from_numpy(rng.standard_normal((rows, Hkv, Dv)).astype(np.float32)).to(dt)
+    s, cache = shape_of(c, 6, Hkv), cache_of(c)
+    coli_kv_append(s, k_new.cuda(), None if latent else v_new.cuda(), cache, start=torch.from_numpy(start).cuda())
+    k2, v2 = ref.append(c, k_new, v_new, start)
+    same_pool(cache.k, k2, "k")
+    if not latent:
+        same_pool(cache.v, v2, "v")
+
+
+def test_append_one_each_and_more_rows_than_positions():
+    import torch
+    c = ref.make_cache([5, 0, 1, 33], 2, 64, 64, 16, "bf16", seed=22)
+    s, cache = shape_of(c, 4, 2), cache_of(c)
+    new = torch.randn(4, 2, 64).bfloat16()
+    coli_kv_append(s, new.cuda(), new.cuda(), cache)
+    k2, v2 = ref.append(c, new, new)
+    same_pool(cache.k, k2, "k")
+    same_pool(cache.v, v2, "v")
+    # 9 rows for a sequence of 5 positions: the first 4 have no place; a page that does not exist takes nothing
+    c["table"][3, 2] = -1
+    start = torch.tensor([0, 9, 9, 10, 20], dtype=torch.int32)
+    new = torch.randn(20, 2, 64).bfloat16()
+    cache = cache_of(c)
+    coli_kv_append(s, new.cuda(), new.cuda(), cache, start=start.cuda())
+    k2, v2 = ref.append(c, new, new, start.numpy())
+    same_pool(cache.k, k2, "k")
+    same_pool(cache.v, v2, "v")
+
+
+# ---------------------------------------------------------------------------
+# evict
+# ---------------------------------------------------------------------------
+
+def run_evict(lens, Hkv, Dk, Dv, page, k, tail, dtype="bf16", latent=False, ties=False, new_extra=5, with_acc=True, seed=31,
+              edit=None):
+    import torch
+    B = len(lens)
+    cols = -(-k // page)
+    c = ref.make_cache(lens, Hkv, Dk, Dv, page, dtype, latent, seed=seed, spare_pages=B * cols)
+    ld = -(-c["max_pages"] * page // 4) * 4
+    rng = np.random.default_rng(seed)
+    acc = (rng.integers(0, 5, size=(B, Hkv, ld)) if ties else rng.random((B, Hkv, ld)) ** 4).astype(np.float32)
+    for b, n in enumerate(lens):
+        acc[b, :, n:] = np.nan            # behind a length: never looked at
+    new_table = c["free"][:B * cols].reshape(B, cols).copy()
+    if edit:
+        edit(c, acc, new_table)
+    s, cache = shape_of(c, B, Hkv), cache_of(c)
+    new_lens, l_ok = guarded((B,), torch.int32, -9)
+    kept, k_ok = guarded((B, Hkv, k), torch.int32, -9)
+    new_acc, a_ok = guarded((B, Hkv, k + new_extra), torch.float32, -9.0)
+    coli_kv_evict(s, cache, torch.from_numpy(acc).cuda(), k, torch.from_numpy(new_table).cuda(), new_lens, kept, tail=tail,
+                  new_acc=new_acc if with_acc else None)
+    torch.cuda.synchronize()
+    for ok in (l_ok, k_ok, a_ok):
+        ok()
+    r = ref.evict(c, acc, k, tail, new_table, new_acc.cpu().numpy() if with_acc else None)
+    assert np.array_equal(new_lens.cpu().numpy(), r["new_lens"])
+    assert np.array_equal(kept.cpu().numpy(), r["kept"])
+    if with_acc:
+        assert np.array_equal(new_acc.cpu().numpy(), r["new_acc"])
+    same_pool(cache.k, r["k"], "k")
+    if not latent:
+        same_pool(cache.v, r["v"], "v")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hkv,Dk,Dv,page,latent,k,tail", [
+    (2, 64, 64, 16, False, 40, 4), (3, 80, 40, 1, False, 33, 0), (1, 576, 512, 64, True, 100, 7),
+    (2, 8, 8, 2, False, 1, 0), (2, 128, 128, 8, False, 64, 1000), (1, 64, 64, 4, False, 1, 3),
+])
+def test_evict(dtype, Hkv, Dk, Dv, page, latent, k, tail):
+    run_evict([0, 1, 39, 40, 41, 300], Hkv, Dk, Dv, page, k, tail, dtype, latent)
+
+
+def test_evict_ties_and_no_weights_out():
+    run_evict([500, 501], 2, 64, 64, 16, 128, 4, ties=True)
+    run_evict([500, 20], 2, 64, 64, 16, 128, 4, with_acc=False)
+
+
+def test_evict_budget_past_the_index_selections():
+    run_evict([9000, 100, 4097], 1, 8, 8, 64, 4097, 16, ties=True)
+
+
+def test_evict_budget_longer_than_the_table():
+    run_evict([30, 17], 2, 64, 64, 16, 100, 4)
+
+
+def test_evict_many_rows():
+    run_evict(list(np.random.default_rng(3).integers(0, 90, size=70)), 4, 8, 8, 16, 24, 2, ties=True)
+
+
+def test_evict_pages_that_do_not_exist():
+    def edit(c, acc, new_table):
+        c["table"][1, 1] = -1
+        new_table[0, 1] = c["n_pages"]
+    run_evict([100, 90], 2, 64, 64, 16, 40, 4, edit=edit)
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,latent,Hq,Hkv,Dk,Dv", [("bf16", False, 8, 2, 64, 64), ("f32", True, 6, 1, 320, 256)])
+def test_serving_run(dtype, latent, Hq, Hkv, Dk, Dv):
+    """Prompts go in, tokens are decoded with running weights kept, the cache is cut to a budget, decoding goes on in
+    the new pages: every step against the plain forms."""
+    import torch
+    page, k, tail, steps = 8, 48, 4, 5
+    prompts = [60, 3, 100]
+    B = 3
+    rng = np.random.default_rng(41)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    cols = -(-(max(prompts) + steps + 1) // page)
+    n_pages = B * cols * 2
+    ids = rng.permutation(n_pages).astype(np.int32)
+    table, new_table = ids[:B * cols].reshape(B, cols), ids[B * cols:].reshape(B, cols)
+    c = dict(k=torch.full((n_pages, Hkv, page, Dk), float("nan"), dtype=dt),
+             v=None if latent else torch.full((n_pages, Hkv, page, Dv), float("nan"), dtype=dt),
+             table=torch.from_numpy(table), lens=torch.tensor(prompts, dtype=torch.int32), page=page, n_pages=n_pages,
+             max_pages=cols, Hkv=Hkv, Dk=Dk, Dv=Dv, dtype=dtype)
+    s, dev = shape_of(c, B, Hq), cache_of(c)
+    scale = 1.5 / np.sqrt(Dk)
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s, acc=True), dtype=torch.uint8, device="cuda")
+    acc = torch.zeros((B, Hkv, cols * page), device="cuda")
+    acc_ref, acc_tol = np.zeros(acc.shape), np.zeros(acc.shape)
+
+    def fresh(*size):
+        return torch.from_numpy(rng.standard_normal(size).astype(np.float32)).to(dt)
+
+    def put(rows, start):
+        kn, vn = fresh(rows, Hkv, Dk), None if latent else fresh(rows, Hkv, Dv)
+        coli_kv_append(s, kn.cuda(), None if latent else vn.cuda(), dev, start=None if start is None else torch.from_numpy(start).cuda())
+        c["k"], c["v"] = ref.append(c, kn, vn, start)
+
+    def decode():
+        nonlocal acc_ref, acc_tol
+        q = fresh(B, Hq, Dk)
+        out = torch.empty((B, Hq, Dv), dtype=dt, device="cuda")
+        coli_kv_attn(s, q.cuda(), dev, out, scale, acc_in=acc, acc_out=acc, ws=ws)
+        r = ref.attn(c, q, scale, acc_in=acc_ref)
+        within(out.double().cpu().numpy(), r["out"], r["tol_out"], "out")
+        acc_ref, acc_tol = r["acc"], acc_tol + r["tol_acc"]
+        within(acc.cpu().numpy(), acc_ref, acc_tol, "acc")
+
+    start = np.concatenate([[0], np.cumsum(prompts)]).astype(np.int32)
+    put(int(start[-1]), start)
+    decode()
+    for _ in range(steps):
+        c["lens"] += 1
+        dev.lens.add_(1)
+        put(B, None)
+        decode()
+    # the kept positions go by the weights that the device holds (ties and rounding are its own)
+    host_acc = acc.cpu().numpy()
+    new_lens = torch.empty(B, dtype=torch.int32, device="cuda")
+    kept = torch.empty((B, Hkv, k), dtype=torch.int32, device="cuda")
+    new_acc = torch.empty((B, Hkv, cols * page), device="cuda")
+    nt = torch.from_numpy(new_table).cuda()
+    coli_kv_evict(s, dev, acc, k, nt, new_lens, kept, tail=tail, new_acc=new_acc)
+    r = ref.evict(c, host_acc, k, tail, new_table, new_acc.cpu().numpy())
+    assert np.array_equal(kept.cpu().numpy(), r["kept"]) and np.array_equal(new_acc.cpu().numpy(), r["new_acc"])
+    c.update(k=r["k"], v=r["v"], table=torch.from_numpy(new_table), lens=torch.from_numpy(r["new_lens"]))
+    same_pool(dev.k, c["k"], "k after the eviction")
+    dev = KvCache(dev.k, dev.v, nt, new_lens)
+    acc, acc_ref, acc_tol = new_acc, new_acc.cpu().numpy().astype(np.float64), np.zeros(acc.shape)
+    for _ in range(steps):
+        c["lens"] += 1
+        dev.lens.add_(1)
+        put(B, None)
+        decode()
+
+
+def test_graph_replays():
+    """A captured decode step (append, attention with running weights) replayed with eager work in between."""
+    import torch
+    c = ref.make_cache([300, 40, 0, 77], 2, 128, 128, 16, "bf16", seed=51)
+    s, dev = shape_of(c, 4, 8), cache_of(c)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn((4, 8, 128), generator=g, device="cuda").bfloat16()
+    new = torch.randn((4, 2, 128), generator=g, device="cuda").bfloat16()
+    ld = c["max_pages"] * 16
+    acc_in = torch.rand((4, 2, ld), generator=g, device="cuda")
+    acc_out = torch.zeros((4, 2, ld), device="cuda")
+    out, lse = torch.empty((4, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((4, 8), device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s, acc=True), dtype=torch.uint8, device="cuda")
+
+    def step(stream=None):
+        coli_kv_append(s, new, new, dev, stream=stream)
+        coli_kv_attn(s, q, dev, out, 0.2, acc_in=acc_in, acc_out=acc_out, lse=lse, ws=ws, stream=stream)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        q.copy_(torch.randn((4, 8, 128), generator=g, device="cuda").bfloat16())
+        new.copy_(torch.randn((4, 2, 128), generator=g, device="cuda").bfloat16())
+        dev.lens.copy_(torch.tensor([300 - i, 40 + i, i, 77], dtype=torch.int32))
+        step()
+        want = [t.clone() for t in (out, lse, acc_out)]
+        for t in (out, lse):
+            t.fill_(3.0)
+        ws.fill_(0x5A)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want[0])) and torch.equal(lse, want[1]) and torch.equal(acc_out, want[2])
+
+
+def test_two_streams_at_once():
+    """Two calls in flight, a workspace each, on streams of their own."""
+    import torch
+    c = ref.make_cache([4000, 100], 2, 128, 128, 16, "bf16", seed=52)
+    s, dev = shape_of(c, 2, 8), cache_of(c)
+    qs = [queries(c, 2, 8, seed=i).cuda() for i in range(2)]
+    outs = [torch.empty((2, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    wss = [torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for i in range(2):
+        coli_kv_attn(s, qs[i], dev, outs[2 + i], 0.2, ws=wss[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            coli_kv_attn(s, qs[i], dev, outs[i], 0.2, ws=wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(bits(outs[i]), bits(outs[2 + i]))
+
+
+def test_refusals_of_the_binding():
+    import torch
+    c = ref.make_cache([40], 2, 64, 64, 16, "bf16", seed=53)
+    s, dev = shape_of(c, 1, 4), cache_of(c)
+    q, out = queries(c, 1, 4).cuda(), torch.empty((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:, :2]), dict(q=q.cpu()), dict(out=out.float()),
+                dict(q=q.transpose(0, 1).contiguous().transpose(0, 1).expand(1, 4, 64)[..., ::1].permute(0, 2, 1)),
+                dict(lse=torch.empty(4, device="cuda")), dict(idx=torch.zeros((1, 3), dtype=torch.int64, device="cuda"))):
+        kw = dict(q=q, out=out) | bad
+        with pytest.raises(ValueError):
+            coli_kv_attn(s, kw.pop("q"), dev, kw.pop("out"), 0.1, ws=ws, **kw)
