@@ -193,7 +193,7 @@ coli_status check_kv_cache(const coli_kv_shape *s, const coli_kv_cache *c)
 
 struct AttnWs {
     size_t part_o, part_ml, stats, scores, total;
-    int q_tiles, n_wg, min_units;
+    coli::AttnPlan plan;
     long s_ld;
 };
 
@@ -201,13 +201,12 @@ AttnWs attn_ws(const coli_kv_shape *s, bool acc)
 {
     AttnWs w{};
     const size_t heads = (size_t)s->B * s->Hq, cap = (size_t)s->max_pages * s->page;
-    w.q_tiles = coli::attn_q_tiles(s->Hq, s->Hkv);
-    w.n_wg = coli::attn_workgroups();
-    w.min_units = 8;
+    w.plan = coli::attn_plan(s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16);
     w.s_ld = (long)((cap + 31) / 32 * 32);
-    const size_t part_rows = (size_t)2 * w.n_wg * coli::attn_tile_rows();
+    // a range leaves at most two parts: of the row it begins in and of the one it ends in
+    const size_t part_rows = (size_t)2 * w.plan.n_wg * w.plan.tile_rows;
     w.part_o = 0;
-    w.part_ml = align_up(w.part_o + part_rows * s->Dv * 4);
+    w.part_ml = align_up(w.part_o + part_rows * w.plan.out_cols * 4);
     w.stats = align_up(w.part_ml + part_rows * 8);
     w.scores = align_up(w.stats + (acc ? heads * 8 : 0));
     w.total = align_up(w.scores + (acc ? heads * (size_t)w.s_ld * 4 : 0));
@@ -706,7 +705,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     a.scale_hi = (float)sc;
     a.scale_lo = (float)(sc - (double)a.scale_hi);
     a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
-    a.q_tiles = L.q_tiles; a.n_wg = L.n_wg; a.min_units = L.min_units;
+    a.q_tiles = L.plan.q_tiles; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
     char *base = (char *)ws;
     a.part_o = (float *)(base + L.part_o);
     a.part_ml = (float *)(base + L.part_ml);

@@ -76,6 +76,78 @@ __device__ __forceinline__ int kv_range(const AttnLaunch &a, int units)
     return max((units + a.n_wg - 1) / a.n_wg, a.min_units);
 }
 
+// A workgroup's range: units u .. u_end - 1, beginning at step s0 of row `row`
+// (cache head and query tile) of sequence b.
+struct KvRange {
+    int u, u_end, b, n, steps, row, s0;
+};
+
+// False: the range is empty (the same for every thread).  R rows a sequence.
+__device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, int32_t *scan, int32_t *found, KvRange &rg)
+{
+    const int tid = threadIdx.x;
+    int sum = 0;
+    for (int i = tid; i < a.B; i += KV_NT) sum += kv_steps(kv_len(a, i));
+    const int total = block_sum(sum, scan) * R;
+    const int range = kv_range(a, total);
+    const int u = blockIdx.x * range;         // at most total + n_wg * min_units: below 2^31 by the host's check
+    if (u >= total) return false;
+    int base = 0;
+    if (tid == 0) found[0] = -1;
+    for (int c = 0; c < a.B; c += KV_NT) {
+        const int st = (c + tid < a.B) ? kv_steps(kv_len(a, c + tid)) : 0;
+        __syncthreads();
+        const int incl = block_scan_incl<KV_WAVES>(st, scan) + base;
+        if (u >= (incl - st) * R && u < incl * R) {
+            found[0] = c + tid;
+            found[1] = (incl - st) * R;
+        }
+        __syncthreads();
+        base += scan[KV_WAVES - 1];
+        if (found[0] >= 0) break;
+    }
+    rg.u = u;
+    rg.u_end = min(u + range, total);
+    rg.b = found[0];
+    rg.n = kv_len(a, rg.b);
+    rg.steps = kv_steps(rg.n);
+    rg.row = (u - found[1]) / rg.steps;
+    rg.s0 = (u - found[1]) % rg.steps;
+    return true;
+}
+
+// The next row of a range (past the last sequence: one step, never taken).
+__device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, int &n, int &steps, int &row)
+{
+    if (++row < R) return;
+    row = 0;
+    do {
+        ++b;
+        n = b < a.B ? kv_len(a, b) : 1;
+        steps = kv_steps(n);
+    } while (steps == 0);
+}
+
+__device__ __forceinline__ int kv_pool_row(const AttnLaunch &a, int pg, int h, int p)
+{
+    return (int)((((uint32_t)pg * (uint32_t)a.Hkv + (uint32_t)h) << a.page_shift) +
+                 (uint32_t)(p & ((1 << a.page_shift) - 1)));
+}
+
+// Pool row of entry p of sequence b's positions (of its list, where there is
+// one) for cache head h; -1: hidden.
+__device__ __forceinline__ int kv_row(const AttnLaunch &a, int b, int h, int n, int len, int p)
+{
+    bool ok = p < n;
+    if (a.idx) {
+        p = ok ? a.idx[(size_t)b * a.idx_k + p] : -1;
+        ok = p >= 0 && p < len;
+    }
+    if (!ok) return -1;
+    const int pg = a.table[(size_t)b * a.max_pages + (p >> a.page_shift)];
+    return (pg >= 0 && pg < a.n_pages) ? kv_pool_row(a, pg, h, p) : -1;
+}
+
 // ---- operands -----------------------------------------------------------------
 // A lane reads 16 bytes of a row at a time: EPL elements.  Keys: lane (j, g)
 // (j = lane & 15, g = lane >> 4) holds elements (4 c + g) EPL .. of key j,
@@ -116,6 +188,16 @@ struct KvTile {
     static_assert(VW == 4 || VW == 2, "8 or 16 bytes of a value row");
 };
 
+// lse of a query row, and its reference and 1 / sum for the running weights.
+__device__ __forceinline__ void kv_write_stats(const AttnLaunch &a, size_t q, float m, float l)
+{
+    if (a.lse) a.lse[q] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (a.stats) {
+        a.stats[2 * q] = m == -INFINITY ? 0.f : m;
+        a.stats[2 * q + 1] = l > 0.f ? 1.f / l : 0.f;
+    }
+}
+
 // (max, +) over the four lanes of a query head (lanes j, j + 16, j + 32, j + 48).
 __device__ __forceinline__ float quad_max(float v)
 {
@@ -145,37 +227,10 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
     const int G = a.Hq / a.Hkv;
     const int R = a.Hkv * a.q_tiles;
 
-    // ---- this workgroup's range and its first sequence ----
-    int total;
-    {
-        int sum = 0;
-        for (int i = tid; i < a.B; i += KV_NT) sum += kv_steps(kv_len(a, i));
-        total = block_sum(sum, scan) * R;
-    }
-    const int range = kv_range(a, total);
-    int u = blockIdx.x * range;               // at most n_wg * range: below 2^31 by the host's check
-    if (u >= total) return;
-    const int u_end = min(u + range, total);
-    {
-        int base = 0;
-        if (tid == 0) found[0] = -1;
-        for (int c = 0; c < a.B; c += KV_NT) {
-            const int st = (c + tid < a.B) ? kv_steps(kv_len(a, c + tid)) : 0;
-            __syncthreads();
-            const int incl = block_scan_incl<KV_WAVES>(st, scan) + base;
-            if (u >= (incl - st) * R && u < incl * R) {
-                found[0] = c + tid;
-                found[1] = (incl - st) * R;
-            }
-            __syncthreads();
-            base += scan[KV_WAVES - 1];
-            if (found[0] >= 0) break;
-        }
-    }
-    int b = found[0];
-    int n = kv_len(a, b), steps = kv_steps(n);
-    int row = (u - found[1]) / steps, s0 = (u - found[1]) % steps;
-    const int u_begin = u;
+    KvRange rg;
+    if (!kv_first(a, R, scan, found, rg)) return;
+    int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
+    const int u_begin = u, u_end = rg.u_end;
 
     const T *kpool = (const T *)a.k;
     const T *vpool = (const T *)(a.v ? a.v : a.k);
@@ -205,22 +260,7 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
         float m = -INFINITY, l = 0.f;
 
         // pool row of position `lane & 31` of step s (-1: hidden)
-        auto rows_of = [&](int s) {
-            int p = s * KV_STEP + (lane & 31);
-            bool ok = p < n && s < s1;
-            if (a.idx) {
-                p = ok ? a.idx[(size_t)b * a.idx_k + p] : -1;
-                ok = p >= 0 && p < len;
-            }
-            int r = -1;
-            if (ok) {
-                const int pg = a.table[(size_t)b * a.max_pages + (p >> a.page_shift)];
-                if (pg >= 0 && pg < a.n_pages)
-                    r = (int)((((uint32_t)pg * (uint32_t)a.Hkv + (uint32_t)h) << a.page_shift) +
-                              (uint32_t)(p & ((1 << a.page_shift) - 1)));
-            }
-            return r;
-        };
+        auto rows_of = [&](int s) { return s < s1 ? kv_row(a, b, h, n, len, s * KV_STEP + (lane & 31)) : -1; };
         u32x4 kf[2][KC];
         auto load_keys = [&](int rows) {
 #pragma unroll
@@ -418,13 +458,7 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
                 const float y = lq > 0.f ? v / lq : 0.f;
                 if constexpr (BF16) ((uint16_t *)a.out)[(qrow + q) * a.Dv + d] = f32_to_bf16_bits(y);
                 else ((float *)a.out)[(qrow + q) * a.Dv + d] = y;
-                if (d == 0) {
-                    if (a.lse) a.lse[qrow + q] = lq > 0.f ? (mq + log2f(lq)) * 0.6931471805599453f : -INFINITY;
-                    if (a.stats) {
-                        a.stats[2 * (qrow + q)] = mq == -INFINITY ? 0.f : mq;
-                        a.stats[2 * (qrow + q) + 1] = lq > 0.f ? 1.f / lq : 0.f;
-                    }
-                }
+                if (d == 0) kv_write_stats(a, qrow + q, mq, lq);
             } else {
                 a.part_o[((size_t)slot * KV_QT + q) * a.Dv + d] = v;
                 if (d == 0) {
@@ -437,14 +471,7 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
 
         u += s1 - s0;
         s0 = 0;
-        if (++row == R) {
-            row = 0;
-            do {
-                ++b;
-                n = b < a.B ? kv_len(a, b) : 1;
-                steps = kv_steps(n);
-            } while (steps == 0);
-        }
+        kv_next_row(a, R, b, n, steps, row);
     }
 }
 
@@ -467,10 +494,7 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
             if (a.bf16) ((uint16_t *)a.out)[(size_t)blockIdx.x * a.Dv + d] = 0;
             else ((float *)a.out)[(size_t)blockIdx.x * a.Dv + d] = 0.f;
         }
-        if (tid == 0) {
-            if (a.lse) a.lse[blockIdx.x] = -INFINITY;
-            if (a.stats) a.stats[2 * blockIdx.x] = a.stats[2 * blockIdx.x + 1] = 0.f;
-        }
+        if (tid == 0) kv_write_stats(a, blockIdx.x, -INFINITY, 0.f);
         return;
     }
     const int range = kv_range(a, total * R);
@@ -513,13 +537,488 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
             else ((float *)a.out)[at] = y;
         }
     }
-    if (tid == 0) {
-        if (a.lse) a.lse[blockIdx.x] = l > 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (a.stats) {
-            a.stats[2 * blockIdx.x] = ref;
-            a.stats[2 * blockIdx.x + 1] = l > 0.f ? 1.f / l : 0.f;
+    if (tid == 0) kv_write_stats(a, blockIdx.x, mx, l);
+}
+
+// ---- wide latent caches -------------------------------------------------------
+// One latent row of up to 576 elements serves all query heads of its cache
+// head (up to 128 a workgroup) as key and as value, so the products weigh as
+// much as the reading: 64 heads are 100 products a byte.  Hence each row is
+// brought into LDS once (copies that pass no registers, a ring of four
+// 32-position stages) and every wave takes 32 query heads on 32 x 32 x 16
+// matrix tiles (twice the rate of the 16 x 16 x 32 form):
+//   scores  D[key][query] = K Q^T       36 tiles a stage, keys read as rows
+//   output  O^T[column][query] += V^T w  32 tiles a stage and part of the
+//           weights, values read column-wise out of the same rows (the LDS
+//           transposing read: 16 lanes take a block of 4 rows x 16 columns
+//           and each gets one column's 4 rows)
+// A lane's 16 scores belong to one query, so the softmax needs one lane
+// exchange, and the weights are in place as the second product's operand:
+// its reduction slots are given to the positions in the order the lanes hold
+// them.  O^T (256 registers) and the queries (144) stay in registers.
+// Waves that share a stage: WQ = 4, 2, 1 query tiles for up to 128, 64, 32
+// heads; with WQ < 4 the waves also split the positions (WK = 4 / WQ stages
+// at a time), and the parts are joined in LDS at the end of a row.
+// LDS layout: chunk c (16 bytes) of row r sits at c with its low three bits
+// XORed by bits 1, 2, 3 of r reversed.  The row stride is half a bank round
+// more than whole rounds, so 16 rows of one chunk (scores) and 4 rows of 4
+// chunks (output) both fall in distinct banks.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int KW_ROWS = 32;                   // positions of a stage
+constexpr int KW_RING = 4;                    // stages in LDS
+constexpr int KW_BLOCK = 64;                  // stages whose pool rows are looked up at a time
+
+// what hidden positions read: they must count as zeros, whatever their memory holds
+static __device__ const u32x4 kw_zeros = {0, 0, 0, 0};
+
+__device__ __forceinline__ int kw_swz(int row) { return ((row >> 1) & 1) * 4 + ((row >> 2) & 1) * 2 + ((row >> 3) & 1); }
+
+template <int N>
+__device__ __forceinline__ void kw_wait_copies()
+{
+    static_assert(N >= 0 && N <= 63, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+__device__ __forceinline__ void kw_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// d += a b on vector registers.  The compiler gives every product of a kernel
+// its accumulator in the 256 accumulation registers; with the output's 256
+// there, the scores must be in the others.  Two wait states: an operand may
+// have been written by the instruction before.
+__device__ __forceinline__ void kw_mfma_v(f32x16 &d, bf16x8 a, bf16x8 b)
+{
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+}
+
+template <int DK, int DV, int WQ>
+__global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_kernel(AttnLaunch a)
+{
+    constexpr int WK = KV_WAVES / WQ;
+    constexpr int RS = DK / 8;                // chunks of a row
+    static_assert(RS % 16 == 8, "row stride: half a bank round past whole ones");
+    constexpr int STAGE = KW_ROWS * RS * 16;  // bytes
+    constexpr int CPS = RS / 2;               // copy instructions of a stage
+    constexpr int CPW = WQ == 1 ? CPS : CPS / KV_WAVES;   // of them, this wave's (WQ = 1: a stage of its own)
+    static_assert(WQ == 1 || CPS % KV_WAVES == 0, "copies split evenly");
+    constexpr int AHEAD = KW_RING / WK - 1;   // rounds in flight beside the one computed
+    constexpr int KS = DK / 16, DT = DV / 32;
+    static_assert(KS % 4 == 0, "fragments in fours");
+    constexpr int OUT = 32 * DV;              // floats of a query tile's output
+    static_assert(2 * OUT * 4 <= KW_RING * STAGE, "two outputs fit the ring");
+    __shared__ __attribute__((aligned(16))) char ring[KW_RING * STAGE];
+    __shared__ int32_t rows_s[KW_BLOCK * KW_ROWS];
+    __shared__ uint32_t hidden_s[KW_RING];
+    __shared__ float red_m[KV_WAVES][32], red_l[KV_WAVES][32];
+    __shared__ int32_t scan[KV_WAVES];
+    __shared__ int32_t found[2];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);    // uniform: the copies' LDS addresses are
+    const int qt = wave % WQ, kb = wave / WQ;
+    const int G = a.Hq / a.Hkv;
+    const int R = a.Hkv * a.q_tiles;
+    KvRange rg;
+    if (!kv_first(a, R, scan, found, rg)) return;
+    int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
+    const int u_begin = u, u_end = rg.u_end;
+    const char *pool = (const char *)a.k;
+    const int row_bytes = a.Dk * 2, chunks = a.Dk / 8;
+
+    while (u < u_end) {
+        // The lane number is made opaque here (and in issue): the offsets that
+        // follow from it are cheap to form again, and kept over the whole row
+        // loop they would push the operands out of the registers.
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));
+        const int ql = lane & 31, hi = lane >> 5;
+        // this lane's offsets inside a stage: key fragments (by chunk pair) ...
+        int koff[4];
+    #pragma unroll
+        for (int x = 0; x < 4; ++x) koff[x] = ql * (RS * 16) + (((2 * x + hi) ^ kw_swz(ql)) * 16);
+        // ... and the transposing value reads (by half of 8 rows and parity of the column tile)
+        int voff[2][2];
+        {
+            const int rr = (lane & 15) >> 2, g1 = (lane >> 4) & 1;
+    #pragma unroll
+            for (int half = 0; half < 2; ++half)
+    #pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    const int r = 8 * half + 4 * hi + rr;
+                    const int c = (4 * odd + 2 * g1 + ((lane >> 1) & 1)) ^ kw_swz(r);
+                    voff[half][odd] = r * (RS * 16) + c * 16 + (lane & 1) * 8;
+                }
+        }
+        const int s1 = min(steps, s0 + (u_end - u));
+        const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
+        const int nq = G - q0;                // query heads of this wave's tile (may be none)
+        const size_t qrow = (size_t)b * a.Hq + h * G + q0;
+        const int len = min(max(a.lens[b], 0), a.cap);
+        const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
+
+        bf16x8 qf[KS];
+        {
+            // no branches: lanes without a query, and columns past its width, load something valid and take zeros
+            const char *qp = (const char *)a.q + ((size_t)b * a.Hq + h * G + min(q0 + ql, G - 1)) * row_bytes;
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+                const int ch = 2 * c + hi;
+                u32x4 v = *reinterpret_cast<const u32x4 *>(qp + (ch < chunks ? ch * 16 : 0));
+                const uint32_t keep = (ql < nq && ch < chunks) ? ~0u : 0u;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] &= keep;
+                qf[c] = as_bf16(v);
+            }
+        }
+        f32x16 o[DT];
+        float m = -INFINITY, l, top;          // m: the reference; top: the largest score
+
+        // pool rows of the block of stages that holds stage t0 (a multiple of KW_BLOCK)
+        auto look_up = [&](int t0) {
+            constexpr int PER = KW_BLOCK * KW_ROWS / KV_NT;
+            const int first = (s0 + t0) * KV_STEP + tid, end = min(n, s1 * KV_STEP);
+            int p[PER];
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {   // no branches: all loads of a kind in flight together
+                const int e = first + x * KV_NT;
+                p[x] = a.idx ? a.idx[(size_t)b * a.idx_k + min(e, n - 1)] : e;
+                p[x] = (e < end && p[x] >= 0 && p[x] < len) ? p[x] : -1;
+            }
+            int pg[PER];
+#pragma unroll
+            for (int x = 0; x < PER; ++x) pg[x] = a.table[(size_t)b * a.max_pages + (max(p[x], 0) >> a.page_shift)];
+#pragma unroll
+            for (int x = 0; x < PER; ++x)
+                rows_s[tid + x * KV_NT] = (p[x] >= 0 && pg[x] >= 0 && pg[x] < a.n_pages) ? kv_pool_row(a, pg[x], h, p[x]) : -1;
+        };
+        // copies of stage t: this wave's share (WQ = 1: all of them)
+        auto issue = [&](int t) {
+            char *dst = ring + (t % KW_RING) * STAGE;
+            const int32_t *rows = rows_s + (t % KW_BLOCK) * KW_ROWS;
+            const uint32_t hid = (uint32_t)__ballot(rows[ql] < 0);
+            if (lane == 0) hidden_s[t % KW_RING] = hid;
+            int first = (WQ == 1 ? 0 : wave * 64) + lane;
+            asm volatile("" : "+v"(first));
+#pragma unroll
+            for (int i = 0; i < CPW; ++i) {
+                constexpr int NEXT = WQ == 1 ? 64 : KV_NT;
+                const int slot = first + i * NEXT, r = slot / RS, pos = slot % RS;
+                const int c = pos ^ kw_swz(r);              // kw_swz < 8: stays in its group of eight
+                const int pr = rows[r];
+                uint64_t src = (uint64_t)pool + (uint64_t)(uint32_t)max(pr, 0) * (uint32_t)row_bytes + c * 16;
+                asm volatile("" : "+v"(src));               // formed for every lane: a select, not a branch
+                src = (pr >= 0 && c < chunks) ? src : (uint64_t)&kw_zeros;
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                                 (__attribute__((address_space(3))) void *)(dst + ((WQ == 1 ? 0 : wave) + i * (NEXT / 64)) * 1024),
+                                                 16, 0, 0);
+            }
+        };
+
+        // The reference is the largest score of the wave's first stage and stays:
+        // weights are numbers of fp32's and bf16's whole range, so a later score
+        // may pass it by up to 2^60 without harm, and O^T never has to be moved to
+        // another one.  A row where some score passes it further is run again with
+        // its largest score as the reference, by all waves (they share the stages).
+        for (;;) {
+            l = 0.f;
+            top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+                asm volatile("" : "+a"(o[t]));    // at home in the accumulation registers
+            }
+            look_up(0);
+            __syncthreads();
+            if constexpr (AHEAD > 0) {
+#pragma unroll
+                for (int r = 0; r < AHEAD; ++r)
+                    if (r < rounds) {
+#pragma unroll
+                        for (int x = 0; x < WK; ++x) issue(r * WK + x);
+                    }
+            }
+            for (int r = 0; r < rounds; ++r) {
+                if constexpr (AHEAD > 0) {
+                    // this wave's copies of round r have landed, then everyone's; round r - 1 is done with its stages
+                    if (r + AHEAD <= rounds) kw_wait_copies<(AHEAD - 1) * WK * CPW>();
+                    else kw_wait_copies<0>();
+                    kw_barrier();
+                    if (r + AHEAD < rounds) {
+                        const int t = (r + AHEAD) * WK;
+                        if (t % KW_BLOCK == 0) {
+                            look_up(t);
+                            kw_barrier();
+                        }
+#pragma unroll
+                        for (int x = 0; x < WK; ++x) issue(t + x);
+                    }
+                } else {
+                    // a stage of the wave's own: the other three waves' work covers its copies
+                    if (r > 0 && r * WK % KW_BLOCK == 0) {
+                        kw_barrier();
+                        look_up(r * WK);
+                        kw_barrier();
+                    }
+                    issue(r * WK + kb);
+                    kw_wait_copies<0>();
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                }
+                const int t = r * WK + kb;
+                if (t >= seg || nq <= 0) continue;              // the same for the whole wave
+                const char *st = ring + (t % KW_RING) * STAGE;
+
+                // ---- scores ----
+                f32x16 sc;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+                {
+                    // fragments four at a time, read one group ahead (the order is fixed: left to itself the compiler
+                    // reads all 36 ahead and spills)
+                    bf16x8 kf[2][4];
+                    auto frags = [&](int grp) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            kf[grp & 1][x] = *reinterpret_cast<const bf16x8 *>(st + koff[x] + grp * 128);
+                    };
+                    frags(0);
+#pragma unroll
+                    for (int grp = 0; grp < KS / 4; ++grp) {
+                        if (grp + 1 < KS / 4) frags(grp + 1);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            kw_mfma_v(sc, kf[grp & 1][x], qf[4 * grp + x]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    // the last product's result: 18 cycles of wait states before a vector instruction may read it
+                    asm volatile("s_nop 15\n\ts_nop 7" : "+v"(sc));
+                }
+                // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
+                const uint32_t hid = __builtin_amdgcn_readfirstlane(hidden_s[t % KW_RING]) >> (4 * hi);
+                float w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = fmaf(sc[i], a.scale_hi, sc[i] * a.scale_lo);
+                if (__ballot(hid != 0)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (hid >> (8 * (i >> 2) + (i & 3)) & 1) w[i] = -INFINITY;
+                }
+                if (a.scores && ql < nq) {
+                    float *dst = a.scores + (qrow + ql) * a.s_ld + (s0 + t) * KV_STEP + 4 * hi;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<f32x4 *>(dst + 8 * x) = f32x4{w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]};
+                }
+                float mx = w[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, w[i]);
+                top = fmaxf(top, mx);
+                if (__ballot(m == -INFINITY)) {             // nothing seen yet
+                    mx = fmaxf(mx, __shfl_xor(mx, 32));
+                    m = m == -INFINITY ? mx : m;
+                }
+                const float ref = (m == -INFINITY) ? 0.f : m;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    w[i] = __builtin_amdgcn_exp2f(w[i] - ref);
+                    l += w[i];
+                }
+                u32x4 whi[2], wlo[2];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float a0 = w[8 * ks + 2 * x], a1 = w[8 * ks + 2 * x + 1];
+                        whi[ks][x] = pack_bf16(a0, a1);
+                        wlo[ks][x] = pack_bf16(a0 - __uint_as_float(whi[ks][x] << 16),
+                                               a1 - __uint_as_float(whi[ks][x] & 0xffff0000u));
+                    }
+                // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further ----
+                s16x4 vf[2][2][2];
+                auto columns = [&](int x) {
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            vf[x & 1][ks][half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (__attribute__((address_space(3))) s16x4 *)(st + voff[half][x & 1] + ks * (16 * RS * 16) +
+                                                                            (x >> 1) * 128));
+                };
+                columns(0);
+#pragma unroll
+                for (int x = 0; x < DT; ++x) {
+                    if (x + 1 < DT) columns(x + 1);
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const s16x8 v = __builtin_shufflevector(vf[x & 1][ks][0], vf[x & 1][ks][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                        const bf16x8 vb = __builtin_bit_cast(bf16x8, v);
+                        o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(whi[ks]), o[x], 0, 0, 0);
+                        o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(wlo[ks]), o[x], 0, 0, 0);
+                    }
+                    asm volatile("" : "+a"(o[x]));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const bool past = top > m + 60.f;
+            if (!__syncthreads_or(past)) break;
+            m = top;
+        }
+
+        // ---- the waves of a query tile become one (the ring is free: its copies have landed and been read) ----
+        l += __shfl_xor(l, 32);
+        if (hi == 0) {
+            red_m[wave][ql] = m;
+            red_l[wave][ql] = l;
+        }
+        kw_barrier();
+        float ma = m, la = l;
+        if constexpr (WK > 1) {
+            ma = red_m[qt][ql];
+#pragma unroll
+            for (int w = 1; w < WK; ++w) ma = fmaxf(ma, red_m[w * WQ + qt][ql]);
+            la = 0.f;
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                const float mw = red_m[w * WQ + qt][ql];
+                la += mw == -INFINITY ? 0.f : red_l[w * WQ + qt][ql] * __builtin_amdgcn_exp2f(mw - ma);
+            }
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - ma);
+#pragma unroll
+            for (int x = 0; x < DT; ++x) o[x] *= f;
+            // two outputs at a time go through LDS: WK = 2: one from each tile's second wave; WK = 4: waves 1, 2, then 3
+            f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
+            constexpr int TURNS = WK == 2 ? 1 : 2;
+#pragma unroll
+            for (int turn = 0; turn < TURNS; ++turn) {
+                const int mine = WK == 2 ? (kb == 1 ? qt : -1) : (turn == 0 ? (kb == 1 || kb == 2 ? kb - 1 : -1) : (kb == 3 ? 0 : -1));
+                if (mine >= 0) {
+#pragma unroll
+                    for (int x = 0; x < DT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            buf[mine * (OUT / 4) + (x * 4 + i) * 64 + lane] =
+                                f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
+                }
+                kw_barrier();
+                if (kb == 0) {
+                    const int first = WK == 2 ? qt : 0, last = WK == 2 ? qt : (turn == 0 ? 1 : 0);
+                    for (int from = first; from <= last; ++from)
+#pragma unroll
+                        for (int x = 0; x < DT; ++x)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const f32x4 v = buf[from * (OUT / 4) + (x * 4 + i) * 64 + lane];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[x][4 * i + e] += v[e];
+                            }
+                }
+                kw_barrier();
+            }
+        }
+        if (kb == 0 && nq > 0) {
+            if (s0 == 0 && s1 == steps) {
+                if (ql < nq) {
+                    const float inv = la > 0.f ? 1.f / la : 0.f;
+                    uint16_t *dst = (uint16_t *)a.out + (qrow + ql) * a.Dv;
+#pragma unroll
+                    for (int x = 0; x < DT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int d = 32 * x + 8 * i + 4 * hi;
+                            if (d < a.Dv)                   // Dv is a multiple of 8: all four columns or none
+                                *reinterpret_cast<u32x2 *>(dst + d) =
+                                    u32x2{pack_bf16(o[x][4 * i] * inv, o[x][4 * i + 1] * inv),
+                                          pack_bf16(o[x][4 * i + 2] * inv, o[x][4 * i + 3] * inv)};
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    if (hi == 0) kv_write_stats(a, qrow + ql, ma, la);
+                }
+            } else {
+                // a part: lanes side by side (attn_wide_join_kernel reads it the same way)
+                const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
+                f32x4 *dst = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
+#pragma unroll
+                for (int x = 0; x < DT; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[(x * 4 + i) * 64] = f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
+                if (hi == 0) {
+                    a.part_ml[(slot * 32 + ql) * 2] = ma;
+                    a.part_ml[(slot * 32 + ql) * 2 + 1] = la;
+                }
+            }
+        }
+        kw_barrier();                                       // red_m, red_l and the ring are free again
+
+        u += s1 - s0;
+        s0 = 0;
+        kv_next_row(a, R, b, n, steps, row);
+    }
+}
+
+// Joins the parts that attn_wide_kernel left: a workgroup takes KJ_COLS
+// 32-column tiles of one query tile's output, a thread 4 columns of a query
+// in each, parts in the order of the positions.
+constexpr int KJ_COLS = 4;
+
+template <int DV, int WQ>
+__global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
+{
+    constexpr int SPLIT = DV / 32 / KJ_COLS;
+    __shared__ int32_t scan[KV_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int ql = lane & 31, hi = lane >> 5;
+    int at = blockIdx.x;
+    const int part = at % SPLIT;
+    at /= SPLIT;
+    const int qt = at % WQ;
+    at /= WQ;
+    const int R = a.Hkv * a.q_tiles, row = at % R, b = at / R;
+    const int G = a.Hq / a.Hkv, h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
+    const int nq = G - q0;
+    if (nq <= 0) return;
+    int before, total;
+    kv_prefix(a, b, scan, &before, &total);
+    const int steps = kv_steps(kv_len(a, b));
+    const size_t q = (size_t)b * a.Hq + h * G + q0 + ql;
+    uint16_t *out = (uint16_t *)a.out + q * a.Dv;
+    // wave i of the workgroup holds the i-th 8 columns of each tile: its lanes' are 8 i + 4 hi + 0..3
+    f32x4 sum[KJ_COLS];
+#pragma unroll
+    for (int x = 0; x < KJ_COLS; ++x) sum[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float mx = -INFINITY, l = 0.f;
+    if (steps > 0) {
+        const int range = kv_range(a, total * R);
+        const int u0 = before * R + row * steps, u1 = u0 + steps;
+        const int w0 = u0 / range, w1 = (u1 - 1) / range;
+        if (w0 == w1) return;                               // one range holds all of it
+        const int first = 2 * w0 + (u0 == w0 * range ? 0 : 1);
+        auto slot_of = [&](int w) { return (size_t)(w == w0 ? first : 2 * w) * WQ + qt; };
+        for (int w = w0; w <= w1; ++w) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        for (int w = w0; w <= w1; ++w) {
+            const size_t sl = slot_of(w);
+            const float f = __builtin_amdgcn_exp2f(a.part_ml[(sl * 32 + ql) * 2] - ref);
+            l += a.part_ml[(sl * 32 + ql) * 2 + 1] * f;
+            const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + sl * (32 * DV)) + lane;
+#pragma unroll
+            for (int x = 0; x < KJ_COLS; ++x) sum[x] += src[((part * KJ_COLS + x) * 4 + wave) * 64] * f;
         }
     }
+    if (ql >= nq) return;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int x = 0; x < KJ_COLS; ++x) {
+        const int d = 32 * (part * KJ_COLS + x) + 8 * wave + 4 * hi;
+        if (d < a.Dv)
+            *reinterpret_cast<u32x2 *>(out + d) = u32x2{pack_bf16(sum[x][0] * inv, sum[x][1] * inv),
+                                                        pack_bf16(sum[x][2] * inv, sum[x][3] * inv)};
+    }
+    if (part == 0 && wave == 0 && hi == 0) kv_write_stats(a, q, mx, l);
 }
 
 // Running weights: acc_out = acc_in + sum over the cache head's query heads
@@ -550,10 +1049,27 @@ __global__ __launch_bounds__(KV_NT) void attn_weights_kernel(AttnLaunch a)
     }
 }
 
-// Workgroups of the main kernel: its ranges.
-int attn_workgroups() { return 1024; }
-int attn_q_tiles(int Hq, int Hkv) { return (Hq / Hkv + KV_QT - 1) / KV_QT; }
-int attn_tile_rows() { return KV_QT; }
+// How a shape runs.  Rows past 256 elements are latent caches (host check);
+// in bf16 they take the LDS kernel.
+AttnPlan attn_plan(int Hq, int Hkv, int Dk, int Dv, bool bf16)
+{
+    AttnPlan p{};
+    const int G = Hq / Hkv;
+    p.wide = bf16 && Dk > 256;
+    if (p.wide) {
+        p.wq = G <= 32 ? 1 : G <= 64 ? 2 : 4;
+        p.tile_rows = 32 * p.wq;
+        p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
+        p.n_wg = 256;
+    } else {
+        p.tile_rows = KV_QT;
+        p.out_cols = Dv;
+        p.n_wg = 1024;
+    }
+    p.min_units = 8;
+    p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
+    return p;
+}
 
 template <bool BF16>
 static void launch_main(const AttnLaunch &a, hipStream_t st)
@@ -562,14 +1078,32 @@ static void launch_main(const AttnLaunch &a, hipStream_t st)
     if (d <= 64) attn_kernel<BF16, 64, 64><<<a.n_wg, KV_NT, 0, st>>>(a);
     else if (d <= 128) attn_kernel<BF16, 128, 128><<<a.n_wg, KV_NT, 0, st>>>(a);
     else if (d <= 256) attn_kernel<BF16, 256, 256><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else attn_kernel<BF16, 576, 512><<<a.n_wg, KV_NT, 0, st>>>(a);
+    else if constexpr (!BF16) attn_kernel<BF16, 576, 512><<<a.n_wg, KV_NT, 0, st>>>(a);
+    attn_join_kernel<<<a.B * a.Hq, KV_NT, 0, st>>>(a);
+}
+
+template <int DK, int DV, int WQ>
+static void launch_wide(const AttnLaunch &a, hipStream_t st)
+{
+    attn_wide_kernel<DK, DV, WQ><<<a.n_wg, KV_NT, 0, st>>>(a);
+    attn_wide_join_kernel<DV, WQ><<<a.B * a.Hkv * a.q_tiles * WQ * (DV / 32 / KJ_COLS), KV_NT, 0, st>>>(a);
+}
+
+template <int DK, int DV>
+static void launch_wide(const AttnLaunch &a, int wq, hipStream_t st)
+{
+    if (wq == 1) launch_wide<DK, DV, 1>(a, st);
+    else if (wq == 2) launch_wide<DK, DV, 2>(a, st);
+    else launch_wide<DK, DV, 4>(a, st);
 }
 
 hipError_t launch_attn(const AttnLaunch &a, hipStream_t st)
 {
-    if (a.bf16) launch_main<true>(a, st);
+    const AttnPlan p = attn_plan(a.Hq, a.Hkv, a.Dk, a.Dv, a.bf16);
+    if (p.wide && p.out_cols == 256) launch_wide<320, 256>(a, p.wq, st);
+    else if (p.wide) launch_wide<576, 512>(a, p.wq, st);
+    else if (a.bf16) launch_main<true>(a, st);
     else launch_main<false>(a, st);
-    attn_join_kernel<<<a.B * a.Hq, KV_NT, 0, st>>>(a);
     if (a.acc_out) {
         const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
         attn_weights_kernel<<<a.B * a.Hkv * chunks, KV_NT, 0, st>>>(a);

@@ -84,6 +84,15 @@ struct AttnLaunch {
     long s_ld;
 };
 
+// Which kernel an attention call takes and how its workspace is laid out.
+struct AttnPlan {
+    bool wide;             // bf16 rows past 256 elements: the LDS kernel
+    int wq;                // its query tiles per workgroup
+    int tile_rows, q_tiles;     // query heads a workgroup takes at a time, and how often per cache head
+    int out_cols;          // columns of a part's rows
+    int n_wg, min_units;
+};
+
 struct AppendLaunch {
     int B, Hkv, rows, page_shift, n_pages, max_pages, cap;
     int k_chunks, v_chunks;     // 16-byte chunks of a key and a value (0: latent)
@@ -109,9 +118,7 @@ struct EvictLaunch {
 hipError_t launch_attn(const AttnLaunch &a, hipStream_t st);
 hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
-int attn_workgroups();
-int attn_q_tiles(int Hq, int Hkv);
-int attn_tile_rows();
+AttnPlan attn_plan(int Hq, int Hkv, int Dk, int Dv, bool bf16);
 
 hipError_t launch_route(const RouteLaunch &a, hipStream_t st);
 // rows_per_len consecutive rows share an entry of lens

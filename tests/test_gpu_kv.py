@@ -548,3 +548,47 @@ def test_refusals_of_the_binding():
         kw = dict(q=q, out=out) | bad
         with pytest.raises(ValueError):
             coli_kv_attn(s, kw.pop("q"), dev, kw.pop("out"), 0.1, ws=ws, **kw)
+
+
+@pytest.mark.parametrize("Hq,Dk,Dv", [(20, 576, 512), (64, 576, 512), (100, 576, 512), (40, 320, 256)])
+@pytest.mark.parametrize("scale", [-0.2, 3.0])
+def test_attn_latent_scores_far_apart(Hq, Dk, Dv, scale):
+    # scores of several hundred, growing along the sequence: later ones pass the first stage's by far more than 2^60
+    c = ref.make_cache([1500, 1, 70, 0], 1, Dk, Dv, 16, "bf16", True, seed=61)
+    for b, n in enumerate(c["lens"].tolist()):
+        for p in range(n):
+            c["k"][c["table"][b, p // 16], :, p % 16] *= 0.05 + 1.5 * p / 1500
+    run_attn(c, Hq, scale)
+
+
+def test_attn_latent_growing_scores_of_one_head():
+    # one query head of 64 meets ever larger scores, the others stay near zero
+    import torch
+    c = ref.make_cache([900], 1, 576, 512, 64, "bf16", True, seed=62)
+    q = queries(c, 1, 64) * 0.01
+    q[0, 37] = 0
+    q[0, 37, 5] = 4.0
+    for p in range(900):
+        c["k"][c["table"][0, p // 64], :, p % 64, 5] = 0.25 * (p // 2)
+    run_attn(c, 64, 1.0, q=q)
+
+
+@pytest.mark.parametrize("Hq", [20, 64, 100])
+def test_attn_latent_long_ranges(Hq):
+    """Sequences that share their pages (a common prompt), so many positions that a workgroup's range is longer than
+    the block of positions it looks up at a time, and spans several sequences."""
+    import torch
+    B, n, page = 70, 16000, 64
+    c = ref.make_cache([n], 1, 320, 256, page, "bf16", True, seed=63)
+    lens = np.full(B, n)
+    lens[1::3] = np.random.default_rng(1).integers(0, n, size=len(lens[1::3]))
+    c["table"] = c["table"].expand(B, -1).contiguous()
+    c["lens"] = torch.from_numpy(lens.astype(np.int32))
+    s, dev, q = shape_of(c, B, Hq), cache_of(c), queries(c, B, Hq)
+    out = torch.empty((B, Hq, 256), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    coli_kv_attn(s, q.cuda(), dev, out, 0.1, ws=ws)
+    pick = [0, 1, 4, 35, 69]
+    few = dict(c, table=c["table"][pick], lens=c["lens"][pick])
+    r = ref.attn(few, q[pick], 0.1)
+    within(out[pick].double().cpu().numpy(), r["out"], r["tol_out"], "out")
