@@ -317,7 +317,7 @@ coli_status coli_index_topk(const float *scores, int32_t rows, int32_t L, int64_
  * Supported: B >= 0, 1 <= Hkv <= Hq <= 1024 with Hq % Hkv = 0, page a power
  * of two <= 4096, n_pages and max_pages >= 1, Dk and Dv multiples of 8, both
  * <= 256 (a latent cache: Dv <= Dk, Dk <= 576, Dv <= 512),
- * n_pages * Hkv * page and B * Hq * (max_pages * page / 32 + 1) below 2^31,
+ * n_pages * Hkv * page and B * Hq * (max_pages * page / 32 + 8) below 2^30,
  * max_pages * page <= 2^24. */
 typedef struct {
     int32_t B;         /* sequences of the call */

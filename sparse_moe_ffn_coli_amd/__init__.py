@@ -196,7 +196,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle alone (a Stream object around it costs 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -445,7 +446,9 @@ class KvShape:
 @dataclass(frozen=True)
 class KvCache:
     """The pools, the page table and the lengths (device tensors), see
-    coli_kv_cache.  v None: a latent cache."""
+    coli_kv_cache.  v None: a latent cache.  A handle that a program makes once
+    and uses in every step: its tensors are written in place (lens and table
+    change from step to step), not resized."""
     k: object
     v: object
     table: object
@@ -455,61 +458,58 @@ class KvCache:
         return CKvCache(_ptr(self.k), _ptr(self.v), _ptr(self.table), _ptr(self.lens))
 
 
-def _kv_dtype(shape: KvShape):
-    import torch
-    return torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16
-
-
 def _kv_check(where: str, device, *args) -> None:
     """(name, tensor, dtype, shape) each: the C ABI takes addresses only, so
     types, sizes and devices are checked here."""
     for name, t, dtype, size in args:
         if t is None:
             continue
-        if t.dtype != dtype or tuple(t.shape) != size:
+        if t.dtype is not dtype or t.shape != size:
             raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
         if t.device != device:
             raise ValueError(f"{where}: {name} is on {t.device}, the cache on {device}")
 
 
-def _kv_cache_args(shape: KvShape, cache: KvCache):
+def _kv_handles(where: str, shape: KvShape, cache: KvCache):
+    """The C forms of a shape and a cache and what calls on them share: (shape, cache, dtype, device).  Checked and
+    formed once for a pair of handles, and kept in the cache's."""
+    kept = cache.__dict__.get("_handles")
+    if kept is not None and kept[0] is shape:
+        return kept[1]
     import torch
-    dt, i32 = _kv_dtype(shape), torch.int32
+    dt, i32, dev = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32, cache.k.device
     pool = (shape.n_pages, shape.Hkv, shape.page)
-    return (("cache.k", cache.k, dt, pool + (shape.Dk,)), ("cache.v", cache.v, dt, pool + (shape.Dv,)),
-            ("cache.table", cache.table, i32, (shape.B, shape.max_pages)), ("cache.lens", cache.lens, i32, (shape.B,)))
+    _kv_check(where, dev, ("cache.k", cache.k, dt, pool + (shape.Dk,)), ("cache.v", cache.v, dt, pool + (shape.Dv,)),
+              ("cache.table", cache.table, i32, (shape.B, shape.max_pages)), ("cache.lens", cache.lens, i32, (shape.B,)))
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: the cache must be on a GPU, not on {dev}")
+    got = (C.byref(shape.c()), C.byref(cache.c()), dt, dev)
+    object.__setattr__(cache, "_handles", (shape, got))
+    return got
 
 
-class _OnDevice:
-    """The cache's device as the current one, so that its stream and kernels are the ones used."""
-
-    def __init__(self, device):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"the cache must be on a GPU, not on {device}")
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _kv_call(where: str, device, *args) -> None:
+    """The library's function with the cache's device as the current one, on its current stream where the last
+    argument (the stream) is None."""
+    import torch
+    f = getattr(lib(), where)
+    if torch.cuda.current_device() == device.index:
+        code = f(*args[:-1], _stream(args[-1]))
+    else:
+        with torch.cuda.device(device):
+            code = f(*args[:-1], _stream(args[-1]))
+    if code:
+        _check(code, where)
 
 
 def coli_kv_append(shape: KvShape, k_new, v_new, cache: KvCache, start=None, stream=None) -> None:
     """k_new [rows][Hkv][Dk], v_new [rows][Hkv][Dv] (None for a latent cache); start int32 [B + 1] or None."""
     import torch
-    rows, dev = k_new.shape[0], cache.k.device
-    _kv_check("coli_kv_append", dev, *_kv_cache_args(shape, cache),
-              ("k_new", k_new, _kv_dtype(shape), (rows, shape.Hkv, shape.Dk)),
-              ("v_new", v_new, _kv_dtype(shape), (rows, shape.Hkv, shape.Dv)),
-              ("start", start, torch.int32, (shape.B + 1,)))
-    cs, cc = shape.c(), cache.c()
-    with _OnDevice(dev):
-        _check(lib().coli_kv_append(C.byref(cs), _ptr(k_new), _ptr(v_new), rows, _ptr(start), C.byref(cc),
-                                    _stream(stream)), "coli_kv_append")
+    cs, cc, dt, dev = _kv_handles("coli_kv_append", shape, cache)
+    rows = k_new.shape[0]
+    _kv_check("coli_kv_append", dev, ("k_new", k_new, dt, (rows, shape.Hkv, shape.Dk)),
+              ("v_new", v_new, dt, (rows, shape.Hkv, shape.Dv)), ("start", start, torch.int32, (shape.B + 1,)))
+    _kv_call("coli_kv_append", dev, cs, _ptr(k_new), _ptr(v_new), rows, _ptr(start), cc, stream)
 
 
 def coli_kv_attn_workspace_bytes(shape: KvShape, idx_k: int = 0, acc: bool = False) -> int:
@@ -521,19 +521,17 @@ def coli_kv_attn(shape: KvShape, q, cache: KvCache, out, scale: float, idx=None,
                  ws=None, ws_bytes=None, stream=None) -> None:
     """q [B][Hq][Dk], out [B][Hq][Dv], lse fp32 [B][Hq], idx int32 [B][idx_k], acc fp32 [B][Hkv][ld]."""
     import torch
-    B, f32, dev = shape.B, torch.float32, cache.k.device
+    cs, cc, dt, dev = _kv_handles("coli_kv_attn", shape, cache)
+    B, Hq, f32 = shape.B, shape.Hq, torch.float32
     ld = 0 if acc_out is None else acc_out.shape[-1]
     idx_k = 0 if idx is None else idx.shape[-1]
-    _kv_check("coli_kv_attn", dev, *_kv_cache_args(shape, cache),
-              ("q", q, _kv_dtype(shape), (B, shape.Hq, shape.Dk)),
-              ("out", out, _kv_dtype(shape), (B, shape.Hq, shape.Dv)),
-              ("lse", lse, f32, (B, shape.Hq)), ("idx", idx, torch.int32, (B, idx_k)),
+    _kv_check("coli_kv_attn", dev, ("q", q, dt, (B, Hq, shape.Dk)), ("out", out, dt, (B, Hq, shape.Dv)),
+              ("lse", lse, f32, (B, Hq)), ("idx", idx, torch.int32, (B, idx_k)),
               ("acc_in", acc_in, f32, (B, shape.Hkv, ld)), ("acc_out", acc_out, f32, (B, shape.Hkv, ld)))
-    cs, cc = shape.c(), cache.c()
-    with _OnDevice(dev):
-        _check(lib().coli_kv_attn(C.byref(cs), _ptr(q), C.byref(cc), scale, _ptr(idx), idx_k, _ptr(acc_in),
-                                  _ptr(acc_out), ld, _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws, ws_bytes),
-                                  _stream(stream)), "coli_kv_attn")
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"coli_kv_attn: ws is on {ws.device}, the cache on {dev}")
+    _kv_call("coli_kv_attn", dev, cs, _ptr(q), cc, scale, _ptr(idx), idx_k, _ptr(acc_in), _ptr(acc_out), ld, _ptr(out),
+             _ptr(lse), _ptr(ws), _nbytes(ws, ws_bytes), stream)
 
 
 def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_lens, kept, tail: int = 0, new_acc=None,
@@ -541,17 +539,14 @@ def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_le
     """acc fp32 [B][Hkv][ld], new_table int32 [B][pages], new_lens int32 [B], kept int32 [B][Hkv][k],
     new_acc fp32 [B][Hkv][new_ld]."""
     import torch
-    B, H, f32, i32, dev = shape.B, shape.Hkv, torch.float32, torch.int32, cache.k.device
+    cs, cc, _, dev = _kv_handles("coli_kv_evict", shape, cache)
+    B, H, f32, i32 = shape.B, shape.Hkv, torch.float32, torch.int32
     ld, cols = acc.shape[-1], new_table.shape[-1]
     new_ld = 0 if new_acc is None else new_acc.shape[-1]
-    _kv_check("coli_kv_evict", dev, *_kv_cache_args(shape, cache), ("acc", acc, f32, (B, H, ld)),
-              ("new_table", new_table, i32, (B, cols)), ("new_lens", new_lens, i32, (B,)),
-              ("kept", kept, i32, (B, H, k)), ("new_acc", new_acc, f32, (B, H, new_ld)))
-    cs, cc = shape.c(), cache.c()
-    with _OnDevice(dev):
-        _check(lib().coli_kv_evict(C.byref(cs), C.byref(cc), _ptr(acc), ld, k, tail, _ptr(new_table), cols,
-                                   _ptr(new_lens), _ptr(kept), _ptr(new_acc), new_ld, _stream(stream)),
-               "coli_kv_evict")
+    _kv_check("coli_kv_evict", dev, ("acc", acc, f32, (B, H, ld)), ("new_table", new_table, i32, (B, cols)),
+              ("new_lens", new_lens, i32, (B,)), ("kept", kept, i32, (B, H, k)), ("new_acc", new_acc, f32, (B, H, new_ld)))
+    _kv_call("coli_kv_evict", dev, cs, cc, _ptr(acc), ld, k, tail, _ptr(new_table), cols, _ptr(new_lens), _ptr(kept),
+             _ptr(new_acc), new_ld, stream)
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

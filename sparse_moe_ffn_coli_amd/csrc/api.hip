@@ -166,7 +166,7 @@ coli_status check_kv_shape(const coli_kv_shape *s, bool latent)
     if (cap > (1 << 24)) return COLI_E_SHAPE;
     // pool rows, and the attention's work in steps, fit in int32
     if ((int64_t)s->n_pages * s->Hkv * s->page > INT32_MAX) return COLI_E_SHAPE;
-    if ((int64_t)s->B * s->Hq * (cap / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if ((int64_t)s->B * s->Hq * (cap / 32 + 8) > INT32_MAX / 2) return COLI_E_SHAPE;
     return COLI_OK;
 }
 
@@ -674,7 +674,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     const double sc = (double)scale * 1.4426950408889634074;     // exponents are taken to base 2
     if (!(sc >= -3e38 && sc <= 3e38)) return COLI_E_SHAPE;
     if (idx ? (idx_k < 1 || idx_k > (1 << 24) || acc_out) : idx_k != 0) return COLI_E_SHAPE;
-    if (idx && (int64_t)s->B * s->Hq * (idx_k / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if (idx && (int64_t)s->B * s->Hq * (idx_k / 32 + 8) > INT32_MAX / 2) return COLI_E_SHAPE;
     if (acc_in && !acc_out) return COLI_E_NULL;
     if (acc_out && (ld < cap || ld % 4)) return COLI_E_SHAPE;
     if (s->B == 0) return check_device();

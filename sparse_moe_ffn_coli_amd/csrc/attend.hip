@@ -31,92 +31,100 @@ constexpr int KV_NT = 256;                    // threads per workgroup (4 waves)
 constexpr int KV_WAVES = KV_NT / 64;
 constexpr int KV_STEP = 32;                   // positions per step of a wave
 constexpr int KV_QT = 16;                     // query heads per matrix tile
+constexpr int KV_MAX_WG = 1024;               // most ranges
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short bf16x8s __attribute__((ext_vector_type(8)));
 
-// Steps of sequence b (per cache head and query tile).
+// Entries of sequence b: positions, or listed ones.
 __device__ __forceinline__ int kv_len(const AttnLaunch &a, int b)
 {
     return a.idx ? a.idx_k : min(max(a.lens[b], 0), a.cap);
 }
 __device__ __forceinline__ int kv_steps(int n) { return (n + KV_STEP - 1) / KV_STEP; }
 
-__device__ __forceinline__ int block_sum(int v, int32_t *red)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-    __syncthreads();
-    if (lane == 0) red[wave] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < KV_WAVES; ++w) s += red[w];
-    return s;
-}
+// Work is counted in units: the steps of a row (a cache head's query tile of
+// one sequence), but no less than KV_MIN_UNITS for a row that has any, since
+// a short row costs its latencies and not its steps (a range of eight
+// one-step rows took 40 us).
+constexpr int KV_MIN_UNITS = 8;
+__device__ __forceinline__ int kv_units(int n) { return n > 0 ? max(kv_steps(n), KV_MIN_UNITS) : 0; }
 
-// Steps of all sequences before b, and of all sequences (per unit of
-// Hkv * query tiles).
-__device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int32_t *red, int *before, int *total)
+// Units of all sequences before b, and of all (per row of a sequence).  Every
+// wave computes it by itself: no barriers, and one load for up to 64
+// sequences.
+__device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int *before, int *total)
 {
+    if (a.idx) {
+        const int per = kv_units(a.idx_k);
+        *before = b * per;
+        *total = a.B * per;
+        return;
+    }
+    const int lane = threadIdx.x & 63;
     int lo = 0, all = 0;
-    for (int i = threadIdx.x; i < a.B; i += KV_NT) {
-        const int st = kv_steps(kv_len(a, i));
+    for (int i = lane; i < a.B; i += 64) {
+        const int st = kv_units(kv_len(a, i));
         all += st;
         lo += (i < b) ? st : 0;
     }
-    *before = block_sum(lo, red);
-    *total = block_sum(all, red);
+    *before = __builtin_amdgcn_readlane(wave_scan_incl(lo), 63);
+    *total = __builtin_amdgcn_readlane(wave_scan_incl(all), 63);
 }
 
-// Units (steps) of one workgroup's range.
+// Units of one workgroup's range.
 __device__ __forceinline__ int kv_range(const AttnLaunch &a, int units)
 {
     return max((units + a.n_wg - 1) / a.n_wg, a.min_units);
 }
 
-// A workgroup's range: units u .. u_end - 1, beginning at step s0 of row `row`
-// (cache head and query tile) of sequence b.
+// A workgroup's range: units u .. u_end - 1, beginning with unit s0 (a step,
+// or past the last one) of row `row` of sequence b.
 struct KvRange {
     int u, u_end, b, n, steps, row, s0;
 };
 
-// False: the range is empty (the same for every thread).  R rows a sequence.
-__device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, int32_t *scan, int32_t *found, KvRange &rg)
+// False: the range is empty.  R rows a sequence.  The same for every wave.
+__device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg)
 {
-    const int tid = threadIdx.x;
-    int sum = 0;
-    for (int i = tid; i < a.B; i += KV_NT) sum += kv_steps(kv_len(a, i));
-    const int total = block_sum(sum, scan) * R;
+    int before, total;
+    kv_prefix(a, 0, &before, &total);
+    total *= R;
     const int range = kv_range(a, total);
     const int u = blockIdx.x * range;         // at most total + n_wg * min_units: below 2^31 by the host's check
     if (u >= total) return false;
     int base = 0;
-    if (tid == 0) found[0] = -1;
-    for (int c = 0; c < a.B; c += KV_NT) {
-        const int st = (c + tid < a.B) ? kv_steps(kv_len(a, c + tid)) : 0;
-        __syncthreads();
-        const int incl = block_scan_incl<KV_WAVES>(st, scan) + base;
-        if (u >= (incl - st) * R && u < incl * R) {
-            found[0] = c + tid;
-            found[1] = (incl - st) * R;
+    if (a.idx) {
+        const int per = kv_units(a.idx_k) * R;
+        rg.b = u / per;
+        base = rg.b * per;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int sum = 0;                          // units (per row) before this chunk of sequences
+        for (int c = 0;; c += 64) {
+            const int st = (c + lane < a.B) ? kv_units(kv_len(a, c + lane)) : 0;
+            const int incl = wave_scan_incl(st) + sum;
+            const uint64_t here = __ballot(u < incl * R);
+            if (here) {                       // the first lane that ends behind u (u < total: there is one)
+                const int x = __ffsll((unsigned long long)here) - 1;
+                rg.b = c + x;
+                base = __builtin_amdgcn_readlane(incl - st, x) * R;
+                break;
+            }
+            sum = __builtin_amdgcn_readlane(incl, 63);
         }
-        __syncthreads();
-        base += scan[KV_WAVES - 1];
-        if (found[0] >= 0) break;
     }
     rg.u = u;
     rg.u_end = min(u + range, total);
-    rg.b = found[0];
     rg.n = kv_len(a, rg.b);
     rg.steps = kv_steps(rg.n);
-    rg.row = (u - found[1]) / rg.steps;
-    rg.s0 = (u - found[1]) % rg.steps;
+    const int per = kv_units(rg.n);
+    rg.row = (u - base) / per;
+    rg.s0 = (u - base) - rg.row * per;
     return true;
 }
 
-// The next row of a range (past the last sequence: one step, never taken).
+// The next row of a range (past the last sequence: one that is never taken).
 __device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, int &n, int &steps, int &row)
 {
     if (++row < R) return;
@@ -124,8 +132,8 @@ __device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, 
     do {
         ++b;
         n = b < a.B ? kv_len(a, b) : 1;
-        steps = kv_steps(n);
-    } while (steps == 0);
+    } while (n == 0);
+    steps = kv_steps(n);
 }
 
 __device__ __forceinline__ int kv_pool_row(const AttnLaunch &a, int pg, int h, int p)
@@ -219,8 +227,6 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
     constexpr int RS = DV + 4;                // padded row of the join buffer
     __shared__ __attribute__((aligned(16))) float red[2][KV_QT][RS];
     __shared__ float red_m[KV_WAVES][KV_QT], red_l[KV_WAVES][KV_QT];
-    __shared__ int32_t scan[KV_WAVES];
-    __shared__ int32_t found[2];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, g = lane >> 4;
@@ -228,7 +234,7 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
     const int R = a.Hkv * a.q_tiles;
 
     KvRange rg;
-    if (!kv_first(a, R, scan, found, rg)) return;
+    if (!kv_first(a, R, rg)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
 
@@ -236,8 +242,9 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
     const T *vpool = (const T *)(a.v ? a.v : a.k);
     const int vstride = a.v ? a.Dv : a.Dk;
 
-    while (u < u_end) {
+    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
+        if (s0 >= steps) continue;            // a short row's units past its steps
         const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * KV_QT;
         const int nq = min(KV_QT, G - q0);    // query heads of this tile
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
@@ -468,10 +475,6 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
             }
         }
         __syncthreads();                      // the join buffer is free again
-
-        u += s1 - s0;
-        s0 = 0;
-        kv_next_row(a, R, b, n, steps, row);
     }
 }
 
@@ -480,14 +483,14 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
 // summed in the order of the positions.
 __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
 {
-    __shared__ int32_t scan[KV_WAVES];
     __shared__ __attribute__((aligned(16))) float red[KV_NT * 4];
+    __shared__ float factor[KV_MAX_WG];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
     const int G = a.Hq / a.Hkv, R = a.Hkv * a.q_tiles;
     int before, total;
-    kv_prefix(a, b, scan, &before, &total);
-    const int steps = kv_steps(kv_len(a, b));
+    kv_prefix(a, b, &before, &total);
+    const int n = kv_len(a, b), steps = kv_steps(n);
     const int qi = hq % G, row = hq / G * a.q_tiles + qi / KV_QT, q = qi % KV_QT;
     if (steps == 0) {
         for (int d = tid; d < a.Dv; d += KV_NT) {
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
         return;
     }
     const int range = kv_range(a, total * R);
-    const int u0 = before * R + row * steps, u1 = u0 + steps;
+    const int u0 = before * R + row * kv_units(n), u1 = u0 + steps;
     const int w0 = u0 / range, w1 = (u1 - 1) / range;
     if (w0 == w1) return;                     // one range holds all of it
     const int first_slot = 2 * w0 + (u0 == w0 * range ? 0 : 1);
@@ -510,20 +513,22 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
     for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float l = 0.f;
-    for (int w = w0 + (tid & 63); w <= w1; w += 64)
-        l += a.part_ml[slot_of(w) * 2 + 1] * __builtin_amdgcn_exp2f(a.part_ml[slot_of(w) * 2] - ref);
+    for (int w = w0 + (tid & 63); w <= w1; w += 64) {
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[slot_of(w) * 2] - ref);
+        l += a.part_ml[slot_of(w) * 2 + 1] * f;
+        if (tid < 64) factor[w - w0] = f;
+    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
+    __syncthreads();
 
     // groups of threads take every ng-th part, 4 columns a thread
     const int cols = a.Dv / 4, ng = KV_NT / cols, grp = tid / cols, col = tid % cols;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     if (grp < ng) {
-        for (int w = w0 + grp; w <= w1; w += ng) {
-            const size_t sl = slot_of(w);
-            acc += *reinterpret_cast<const f32x4 *>(a.part_o + sl * a.Dv + 4 * col) *
-                   __builtin_amdgcn_exp2f(a.part_ml[sl * 2] - ref);
-        }
+#pragma unroll 4
+        for (int w = w0 + grp; w <= w1; w += ng)
+            acc += *reinterpret_cast<const f32x4 *>(a.part_o + slot_of(w) * a.Dv + 4 * col) * factor[w - w0];
         *reinterpret_cast<f32x4 *>(red + 4 * tid) = acc;
     }
     __syncthreads();
@@ -613,8 +618,6 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     __shared__ int32_t rows_s[KW_BLOCK * KW_ROWS];
     __shared__ uint32_t hidden_s[KW_RING];
     __shared__ float red_m[KV_WAVES][32], red_l[KV_WAVES][32];
-    __shared__ int32_t scan[KV_WAVES];
-    __shared__ int32_t found[2];
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);    // uniform: the copies' LDS addresses are
@@ -622,13 +625,15 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     const int G = a.Hq / a.Hkv;
     const int R = a.Hkv * a.q_tiles;
     KvRange rg;
-    if (!kv_first(a, R, scan, found, rg)) return;
+    if (!kv_first(a, R, rg)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const char *pool = (const char *)a.k;
     const int row_bytes = a.Dk * 2, chunks = a.Dk / 8;
 
-    while (u < u_end) {
+    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
+        const int s1 = min(steps, s0 + (u_end - u));
+        if (s0 >= steps) continue;            // a short row's units past its steps
         // The lane number is made opaque here (and in issue): the offsets that
         // follow from it are cheap to form again, and kept over the whole row
         // loop they would push the operands out of the registers.
@@ -652,7 +657,6 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                     voff[half][odd] = r * (RS * 16) + c * 16 + (lane & 1) * 8;
                 }
         }
-        const int s1 = min(steps, s0 + (u_end - u));
         const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
         const int nq = G - q0;                // query heads of this wave's tile (may be none)
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
@@ -953,10 +957,6 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             }
         }
         kw_barrier();                                       // red_m, red_l and the ring are free again
-
-        u += s1 - s0;
-        s0 = 0;
-        kv_next_row(a, R, b, n, steps, row);
     }
 }
 
@@ -969,7 +969,6 @@ template <int DV, int WQ>
 __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
 {
     constexpr int SPLIT = DV / 32 / KJ_COLS;
-    __shared__ int32_t scan[KV_WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int ql = lane & 31, hi = lane >> 5;
     int at = blockIdx.x;
@@ -982,8 +981,8 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
     const int nq = G - q0;
     if (nq <= 0) return;
     int before, total;
-    kv_prefix(a, b, scan, &before, &total);
-    const int steps = kv_steps(kv_len(a, b));
+    kv_prefix(a, b, &before, &total);
+    const int n = kv_len(a, b), steps = kv_steps(n);
     const size_t q = (size_t)b * a.Hq + h * G + q0 + ql;
     uint16_t *out = (uint16_t *)a.out + q * a.Dv;
     // wave i of the workgroup holds the i-th 8 columns of each tile: its lanes' are 8 i + 4 hi + 0..3
@@ -993,7 +992,7 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
     float mx = -INFINITY, l = 0.f;
     if (steps > 0) {
         const int range = kv_range(a, total * R);
-        const int u0 = before * R + row * steps, u1 = u0 + steps;
+        const int u0 = before * R + row * kv_units(n), u1 = u0 + steps;
         const int w0 = u0 / range, w1 = (u1 - 1) / range;
         if (w0 == w1) return;                               // one range holds all of it
         const int first = 2 * w0 + (u0 == w0 * range ? 0 : 1);
@@ -1060,13 +1059,13 @@ AttnPlan attn_plan(int Hq, int Hkv, int Dk, int Dv, bool bf16)
         p.wq = G <= 32 ? 1 : G <= 64 ? 2 : 4;
         p.tile_rows = 32 * p.wq;
         p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
-        p.n_wg = 256;
+        p.n_wg = 256;                     // one workgroup per CU: the ring fills its LDS
     } else {
         p.tile_rows = KV_QT;
         p.out_cols = Dv;
-        p.n_wg = 1024;
+        p.n_wg = KV_MAX_WG;
     }
-    p.min_units = 8;
+    p.min_units = KV_MIN_UNITS;
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
     return p;
 }

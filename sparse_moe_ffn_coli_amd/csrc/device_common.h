@@ -76,6 +76,21 @@ __device__ __forceinline__ uint32_t wave_reduce_u32(uint32_t v, Op op)
 struct MaxU32 { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; } };
 struct MinU32 { __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; } };
 
+// Inclusive prefix sum over the 64 lanes of a wave on DPP lane moves: shifts
+// by 1, 2, 4 and 8 inside each row of 16 lanes, then each row's total is
+// added to the rows above it (row broadcasts of lanes 15 and 31).  Lanes
+// whose source is outside the pattern add 0.
+__device__ __forceinline__ int wave_scan_incl(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2, 3
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // Inclusive prefix sum over the NW waves of a workgroup (thread order):
 // a shuffle scan inside each wave, then one wave scans the NW wave totals.

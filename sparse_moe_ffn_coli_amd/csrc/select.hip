@@ -42,21 +42,6 @@ constexpr int SEL_CAP = 32768;           // positions whose keys a workgroup kee
 constexpr int SEL_PER = SEL_CAP / (4 * SEL_NT);   // 16-byte loads per thread for a cached row
 constexpr int SEL_MAX_K = 4096;          // largest k
 
-// Inclusive prefix sum over the 64 lanes of a wave on DPP lane moves: shifts
-// by 1, 2, 4 and 8 inside each row of 16 lanes, then each row's total is
-// added to the rows above it (row broadcasts of lanes 15 and 31).  Lanes
-// whose source is outside the pattern add 0.
-__device__ __forceinline__ int wave_scan_incl(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1, 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2, 3
-    return v;
-}
-
 // Barrier for LDS traffic only: every wave's LDS operations have completed
 // (global loads in flight, such as the next row's prefetch, are not waited for).
 __device__ __forceinline__ void lds_barrier()
