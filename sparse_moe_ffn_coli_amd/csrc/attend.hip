@@ -564,22 +564,30 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
 // Waves that share a stage: WQ = 4, 2, 1 query tiles for up to 128, 64, 32
 // heads; with WQ < 4 the waves also split the positions (WK = 4 / WQ stages
 // at a time), and the parts are joined in LDS at the end of a row.
-// LDS layout: chunk c (16 bytes) of row r sits at c with its low three bits
-// XORed by bits 1, 2, 3 of r reversed.  The row stride is half a bank round
-// more than whole rounds, so 16 rows of one chunk (scores) and 4 rows of 4
-// chunks (output) both fall in distinct banks.
+// LDS layout of a stage: the columns that are values too (DV of them) first,
+// row after row, then the keys' last 64.  A row of the first part is whole
+// bank rounds, so chunk c (16 bytes) of row r sits at c with its low four
+// bits XORed by r's low bits (1, 0, 3, 2): 16 rows of one chunk (scores) and
+// 4 rows of 4 chunks (output) both fall in distinct banks.  A copy
+// instruction brings one row (or two of 256 columns), so its address is
+// uniform: a few scalar instructions, which go between the products.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int KW_ROWS = 32;                   // positions of a stage
 constexpr int KW_RING = 4;                    // stages in LDS
-constexpr int KW_BLOCK = 64;                  // stages whose pool rows are looked up at a time
+constexpr int KW_BLOCK = 32;                  // stages whose rows are looked up at a time
+
+template <int N>
+struct KwInt {
+    static constexpr int value = N;
+};
 
 // what hidden positions read: they must count as zeros, whatever their memory holds
-static __device__ const u32x4 kw_zeros = {0, 0, 0, 0};
+static __device__ const u32x4 kw_zeros[72] = {};
 
-__device__ __forceinline__ int kw_swz(int row) { return ((row >> 1) & 1) * 4 + ((row >> 2) & 1) * 2 + ((row >> 3) & 1); }
+__device__ __forceinline__ int kw_swz(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
 
 template <int N>
 __device__ __forceinline__ void kw_wait_copies()
@@ -589,6 +597,32 @@ __device__ __forceinline__ void kw_wait_copies()
 }
 
 __device__ __forceinline__ void kw_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// 16 bytes of each lane's address to LDS, lane after lane from byte `dst`
+// (uniform): the address uniform with an offset for each lane, or the lane's
+// own.  In assembler, and counted by hand (kw_wait_copies), because the
+// compiler lets every transposing read wait for all copies in flight where it
+// knows of them.  There is no register output, and the compiler has no use of
+// its own for m0 here; the barriers order what is written.
+__device__ __forceinline__ void kw_copy(uint64_t base, uint32_t off, uint32_t dst)
+{
+    // five wait states between the lane read that formed the base and its use as an address
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(off),
+                 "s"(__builtin_amdgcn_readfirstlane(dst)));
+}
+__device__ __forceinline__ void kw_copy(uint64_t src, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(dst)));
+}
+
+// lane i's value (i uniform)
+__device__ __forceinline__ uint64_t kw_lane(uint64_t v, int i)
+{
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, i);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), i);
+    return (uint64_t)hi << 32 | lo;
+}
 
 // d += a b on vector registers.  The compiler gives every product of a kernel
 // its accumulator in the 256 accumulation registers; with the output's 256
@@ -603,20 +637,21 @@ template <int DK, int DV, int WQ>
 __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_kernel(AttnLaunch a)
 {
     constexpr int WK = KV_WAVES / WQ;
-    constexpr int RS = DK / 8;                // chunks of a row
-    static_assert(RS % 16 == 8, "row stride: half a bank round past whole ones");
-    constexpr int STAGE = KW_ROWS * RS * 16;  // bytes
-    constexpr int CPS = RS / 2;               // copy instructions of a stage
-    constexpr int CPW = WQ == 1 ? CPS : CPS / KV_WAVES;   // of them, this wave's (WQ = 1: a stage of its own)
-    static_assert(WQ == 1 || CPS % KV_WAVES == 0, "copies split evenly");
+    constexpr int RA = DV / 8;                // chunks of a row's first part
+    static_assert((RA == 64 || RA == 32) && DK == DV + 64, "row parts");
+    constexpr int RPC = 64 / RA;              // rows of a copy instruction
+    constexpr int FIRST = KW_ROWS * RA * 16;  // bytes of a stage's first part
+    constexpr int STAGE = FIRST + KW_ROWS * 128;
+    constexpr int CA = KW_ROWS / RPC, CB = 4; // copy instructions of a stage's parts
+    constexpr int SHARE = WQ == 1 ? 1 : KV_WAVES;         // waves that bring a stage (WQ = 1: each its own)
+    constexpr int CPW = (CA + CB) / SHARE;    // copies of a wave
     constexpr int AHEAD = KW_RING / WK - 1;   // rounds in flight beside the one computed
     constexpr int KS = DK / 16, DT = DV / 32;
     static_assert(KS % 4 == 0, "fragments in fours");
     constexpr int OUT = 32 * DV;              // floats of a query tile's output
     static_assert(2 * OUT * 4 <= KW_RING * STAGE, "two outputs fit the ring");
-    __shared__ __attribute__((aligned(16))) char ring[KW_RING * STAGE];
-    __shared__ int32_t rows_s[KW_BLOCK * KW_ROWS];
-    __shared__ uint32_t hidden_s[KW_RING];
+    __shared__ __attribute__((aligned(256))) char ring[KW_RING * STAGE];
+    __shared__ uint64_t rows_s[KW_BLOCK * KW_ROWS];         // addresses of the stages' rows
     __shared__ float red_m[KV_WAVES][32], red_l[KV_WAVES][32];
 
     const int tid = threadIdx.x;
@@ -630,6 +665,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     const int u_begin = u, u_end = rg.u_end;
     const char *pool = (const char *)a.k;
     const int row_bytes = a.Dk * 2, chunks = a.Dk / 8;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
 
     for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
@@ -640,47 +676,26 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         int lane = tid & 63;
         asm volatile("" : "+v"(lane));
         const int ql = lane & 31, hi = lane >> 5;
-        // this lane's offsets inside a stage: key fragments (by chunk pair) ...
-        int koff[4];
-    #pragma unroll
-        for (int x = 0; x < 4; ++x) koff[x] = ql * (RS * 16) + (((2 * x + hi) ^ kw_swz(ql)) * 16);
-        // ... and the transposing value reads (by half of 8 rows and parity of the column tile)
-        int voff[2][2];
-        {
-            const int rr = (lane & 15) >> 2, g1 = (lane >> 4) & 1;
-    #pragma unroll
-            for (int half = 0; half < 2; ++half)
-    #pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    const int r = 8 * half + 4 * hi + rr;
-                    const int c = (4 * odd + 2 * g1 + ((lane >> 1) & 1)) ^ kw_swz(r);
-                    voff[half][odd] = r * (RS * 16) + c * 16 + (lane & 1) * 8;
-                }
-        }
+        // This lane's places inside a stage, as bytes: key row ql, chunks hi and
+        // RA + hi (chunk c of the row: XOR by 16 times c's even part, low four or
+        // three bits), and the transposing reads' (below).
+        const int key_at = ql * (RA * 16) + ((hi ^ kw_swz(ql)) << 4);
+        const int tail_at = FIRST + ql * 128 + ((hi ^ ((ql >> 1) & 7)) << 4);
+        // A transposing read takes rows 16 ks + 8 half + 4 hi + 0..3 (16 lanes: 4 rows of 32 bytes): this is for
+        // ks = half = 0 and column 16 * (bit 4 of the lane).
+        const int rr = (lane & 15) >> 2;
+        const int val_at = (4 * hi + rr) * (RA * 16) + (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ (rr << 2) ^ hi) << 4) +
+                           (lane & 1) * 8;
         const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
         const int nq = G - q0;                // query heads of this wave's tile (may be none)
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
         const int len = min(max(a.lens[b], 0), a.cap);
         const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
 
-        bf16x8 qf[KS];
-        {
-            // no branches: lanes without a query, and columns past its width, load something valid and take zeros
-            const char *qp = (const char *)a.q + ((size_t)b * a.Hq + h * G + min(q0 + ql, G - 1)) * row_bytes;
-#pragma unroll
-            for (int c = 0; c < KS; ++c) {
-                const int ch = 2 * c + hi;
-                u32x4 v = *reinterpret_cast<const u32x4 *>(qp + (ch < chunks ? ch * 16 : 0));
-                const uint32_t keep = (ql < nq && ch < chunks) ? ~0u : 0u;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] &= keep;
-                qf[c] = as_bf16(v);
-            }
-        }
         f32x16 o[DT];
         float m = -INFINITY, l, top;          // m: the reference; top: the largest score
 
-        // pool rows of the block of stages that holds stage t0 (a multiple of KW_BLOCK)
+        // row addresses of the block of stages that holds stage t0 (a multiple of KW_BLOCK)
         auto look_up = [&](int t0) {
             constexpr int PER = KW_BLOCK * KW_ROWS / KV_NT;
             const int first = (s0 + t0) * KV_STEP + tid, end = min(n, s1 * KV_STEP);
@@ -696,30 +711,81 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             for (int x = 0; x < PER; ++x) pg[x] = a.table[(size_t)b * a.max_pages + (max(p[x], 0) >> a.page_shift)];
 #pragma unroll
             for (int x = 0; x < PER; ++x)
-                rows_s[tid + x * KV_NT] = (p[x] >= 0 && pg[x] >= 0 && pg[x] < a.n_pages) ? kv_pool_row(a, pg[x], h, p[x]) : -1;
+                rows_s[tid + x * KV_NT] =
+                    (p[x] >= 0 && pg[x] >= 0 && pg[x] < a.n_pages)
+                        ? (uint64_t)pool + (uint64_t)(uint32_t)kv_pool_row(a, pg[x], h, p[x]) * (uint32_t)row_bytes
+                        : (uint64_t)kw_zeros;
         };
-        // copies of stage t: this wave's share (WQ = 1: all of them)
-        auto issue = [&](int t) {
-            char *dst = ring + (t % KW_RING) * STAGE;
-            const int32_t *rows = rows_s + (t % KW_BLOCK) * KW_ROWS;
-            const uint32_t hid = (uint32_t)__ballot(rows[ql] < 0);
-            if (lane == 0) hidden_s[t % KW_RING] = hid;
-            int first = (WQ == 1 ? 0 : wave * 64) + lane;
-            asm volatile("" : "+v"(first));
-#pragma unroll
-            for (int i = 0; i < CPW; ++i) {
-                constexpr int NEXT = WQ == 1 ? 64 : KV_NT;
-                const int slot = first + i * NEXT, r = slot / RS, pos = slot % RS;
-                const int c = pos ^ kw_swz(r);              // kw_swz < 8: stays in its group of eight
-                const int pr = rows[r];
-                uint64_t src = (uint64_t)pool + (uint64_t)(uint32_t)max(pr, 0) * (uint32_t)row_bytes + c * 16;
-                asm volatile("" : "+v"(src));               // formed for every lane: a select, not a branch
-                src = (pr >= 0 && c < chunks) ? src : (uint64_t)&kw_zeros;
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                                 (__attribute__((address_space(3))) void *)(dst + ((WQ == 1 ? 0 : wave) + i * (NEXT / 64)) * 1024),
-                                                 16, 0, 0);
+        // Copy instructions of 32 rows' two parts into the stage at byte dst; rows: lane i holds row i's address.
+        // Columns past the row's width repeat its last chunk: zeros of the query and output columns that are not
+        // written meet them.
+        const uint32_t last = (chunks - 1) * 16;
+        auto copy_first = [&](uint64_t rows, int i, uint32_t dst) {
+            uint32_t lane_at = (lane & (RA - 1)) << 4;
+            if constexpr (RPC == 2) lane_at ^= (lane >> 5) << 6;
+            const uint32_t off = min(lane_at ^ (kw_swz(i * RPC) << 4), last);
+            const uint64_t src = kw_lane(rows, i * RPC);
+            if constexpr (RPC == 1) {
+                kw_copy(src, off, dst + i * 1024);
+            } else {
+                const uint64_t other = kw_lane(rows, i * RPC + 1);
+                kw_copy((lane < 32 ? src : other) + off, dst + i * 1024);
             }
         };
+        auto copy_tail = [&](uint64_t rows, int i, uint32_t dst) {
+            const uint32_t off = min((uint32_t)(RA + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))) << 4, last);
+            kw_copy((uint64_t)__shfl((unsigned long long)rows, 8 * i + (lane >> 3)) + off, dst + FIRST + i * 1024);
+        };
+        // copy number i of the wave's share of stage t
+        auto copy = [&](int t, uint64_t rows, int i) {
+            const uint32_t dst = ring_at + (t % KW_RING) * STAGE;
+            const int me = SHARE == 1 ? 0 : wave;
+            if (i < CA / SHARE) copy_first(rows, i * SHARE + me, dst);
+            else copy_tail(rows, (i - CA / SHARE) * SHARE + me, dst);
+        };
+        // lane i's: address of row i (lane 32 + i: the same) of stage t, and which rows are hidden
+        auto stage_rows = [&](int t) { return rows_s[(t % KW_BLOCK) * KW_ROWS + ql]; };
+        auto hidden = [&](uint64_t rows) { return (uint32_t)__ballot(rows == (uint64_t)kw_zeros); };
+        auto issue = [&](int t) {
+            const uint64_t rows = stage_rows(t);
+#pragma unroll
+            for (int i = 0; i < CPW; ++i) copy(t, rows, i);
+            return hidden(rows);
+        };
+
+        // Query fragments and key fragments are the same places of a stage: group grp of four, number x of it, is
+        // columns 16 frag(grp, x) + 8 hi + 0..7; the last group is the tail.
+        constexpr int GRP = KS / 4;
+        auto frag = [](int grp, int x) {
+            return grp == GRP - 1 ? RA / 2 + x : RA == 64 ? grp + 8 * x : 2 * grp + (x >> 1) + 8 * (x & 1);
+        };
+        auto frag_at = [&](const char *st, int grp, int x) {
+            const int c = frag(grp, x);
+            const int at = grp == GRP - 1 ? tail_at ^ (32 * x) : (key_at ^ (32 * (c & 7))) + (c >> 3) * 256;
+            return *reinterpret_cast<const bf16x8 *>(st + at);
+        };
+
+        // the queries come in like a stage, each tile by its waves, and stay in registers as the score operand
+        bf16x8 qf[KS];
+        {
+            const uint64_t rows = ql < nq ? (uint64_t)a.q + (qrow + ql) * row_bytes : (uint64_t)kw_zeros;
+#pragma unroll
+            for (int i = 0; i < CA / WK; ++i) copy_first(rows, i * WK + kb, ring_at + qt * STAGE);
+#pragma unroll
+            for (int i = 0; i < CB / WK; ++i) copy_tail(rows, i * WK + kb, ring_at + qt * STAGE);
+            look_up(0);
+            kw_wait_copies<0>();
+            kw_barrier();
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {                  // zeros past the width
+                u32x4 v = __builtin_bit_cast(u32x4, frag_at(ring + qt * STAGE, c / 4, c % 4));
+                const uint32_t keep = 16 * frag(c / 4, c % 4) + 8 * hi < a.Dk ? ~0u : 0u;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] &= keep;
+                qf[c] = as_bf16(v);
+            }
+            kw_barrier();
+        }
 
         // The reference is the largest score of the wave's first stage and stays:
         // weights are numbers of fp32's and bf16's whole range, so a later score
@@ -735,30 +801,23 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
                 asm volatile("" : "+a"(o[t]));    // at home in the accumulation registers
             }
-            look_up(0);
-            __syncthreads();
+            uint32_t hids[AHEAD + 1];                       // hidden rows of the wave's stages in flight, next one first
             if constexpr (AHEAD > 0) {
 #pragma unroll
-                for (int r = 0; r < AHEAD; ++r)
-                    if (r < rounds) {
-#pragma unroll
-                        for (int x = 0; x < WK; ++x) issue(r * WK + x);
-                    }
+                for (int t = 0; t < AHEAD * WK; ++t) {
+                    const uint32_t mask = issue(t);
+                    if (t % WK == kb) hids[t / WK] = mask;
+                }
             }
             for (int r = 0; r < rounds; ++r) {
+                const int ahead = (r + AHEAD) * WK;         // first stage of the round to be copied in this one
                 if constexpr (AHEAD > 0) {
                     // this wave's copies of round r have landed, then everyone's; round r - 1 is done with its stages
-                    if (r + AHEAD <= rounds) kw_wait_copies<(AHEAD - 1) * WK * CPW>();
-                    else kw_wait_copies<0>();
+                    kw_wait_copies<(AHEAD - 1) * WK * CPW>();
                     kw_barrier();
-                    if (r + AHEAD < rounds) {
-                        const int t = (r + AHEAD) * WK;
-                        if (t % KW_BLOCK == 0) {
-                            look_up(t);
-                            kw_barrier();
-                        }
-#pragma unroll
-                        for (int x = 0; x < WK; ++x) issue(t + x);
+                    if (ahead % KW_BLOCK == 0) {
+                        look_up(ahead);
+                        kw_barrier();
                     }
                 } else {
                     // a stage of the wave's own: the other three waves' work covers its copies
@@ -767,41 +826,54 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                         look_up(r * WK);
                         kw_barrier();
                     }
-                    issue(r * WK + kb);
+                    hids[0] = issue(r * WK + kb);
                     kw_wait_copies<0>();
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 }
                 const int t = r * WK + kb;
-                if (t >= seg || nq <= 0) continue;              // the same for the whole wave
+                // A wave without positions (t >= seg: all of them hidden) or queries (nq <= 0: zeros) computes all the
+                // same: a second way through the loop would cost the accumulators their registers.
                 const char *st = ring + (t % KW_RING) * STAGE;
+                const uint32_t hid = hids[0] >> (4 * hi);
 
-                // ---- scores ----
+                // ---- scores, with the copies of a later round between the products (a wave that issues them in one
+                // go multiplies nothing meanwhile: 2000 cycles of 7200) ----
                 f32x16 sc;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sc[i] = 0.f;
                 {
-                    // fragments four at a time, read one group ahead (the order is fixed: left to itself the compiler
-                    // reads all 36 ahead and spills)
-                    bf16x8 kf[2][4];
-                    auto frags = [&](int grp) {
+                    // Eight fragments in a ring: the one just used makes room for the one eight products on (the order is
+                    // fixed: left to itself the compiler reads all 36 ahead and spills).
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            kf[grp & 1][x] = *reinterpret_cast<const bf16x8 *>(st + koff[x] + grp * 128);
-                    };
-                    frags(0);
+                    for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+                    static_assert(AHEAD == 0 || CPW == GRP, "a copy of each stage to a group");
+                    bf16x8 kf[8];
+                    uint64_t rows[WK];
 #pragma unroll
-                    for (int grp = 0; grp < KS / 4; ++grp) {
-                        if (grp + 1 < KS / 4) frags(grp + 1);
+                    for (int x = 0; x < 8; ++x) kf[x] = frag_at(st, x / 4, x % 4);
+                    if constexpr (AHEAD > 0) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            kw_mfma_v(sc, kf[grp & 1][x], qf[4 * grp + x]);
-                        __builtin_amdgcn_sched_barrier(0);
+                        for (int y = 0; y < WK; ++y) rows[y] = stage_rows(ahead + y);
+#pragma unroll
+                        for (int y = 0; y < AHEAD; ++y) hids[y] = hids[y + 1];
+#pragma unroll
+                        for (int y = 0; y < WK; ++y)
+                            if (y == kb) hids[AHEAD - 1] = hidden(rows[y]);
+                    }
+#pragma unroll
+                    for (int grp = 0; grp < GRP; ++grp) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {       // a read after each product: the four waves share the LDS port
+                            kw_mfma_v(sc, kf[(4 * grp + x) % 8], qf[4 * grp + x]);
+                            if (grp + 2 < GRP) kf[(4 * grp + x) % 8] = frag_at(st, grp + 2, x);
+                            if constexpr (AHEAD > 0) {
+                                if (x % 2 == 1 && x / 2 < WK) copy(ahead + x / 2, rows[x / 2], grp);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
                     // the last product's result: 18 cycles of wait states before a vector instruction may read it
                     asm volatile("s_nop 15\n\ts_nop 7" : "+v"(sc));
                 }
                 // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
-                const uint32_t hid = __builtin_amdgcn_readfirstlane(hidden_s[t % KW_RING]) >> (4 * hi);
                 float w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = fmaf(sc[i], a.scale_hi, sc[i] * a.scale_lo);
@@ -810,7 +882,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                     for (int i = 0; i < 16; ++i)
                         if (hid >> (8 * (i >> 2) + (i & 3)) & 1) w[i] = -INFINITY;
                 }
-                if (a.scores && ql < nq) {
+                if (a.scores && ql < nq && t < seg) {
                     float *dst = a.scores + (qrow + ql) * a.s_ld + (s0 + t) * KV_STEP + 4 * hi;
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -841,35 +913,39 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                                                a1 - __uint_as_float(whi[ks][x] & 0xffff0000u));
                     }
                 // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further ----
-                s16x4 vf[2][2][2];
-                auto columns = [&](int x) {
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            vf[x & 1][ks][half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) s16x4 *)(st + voff[half][x & 1] + ks * (16 * RS * 16) +
-                                                                            (x >> 1) * 128));
+                // two column tiles at a time, read one pair ahead, their products taken in turn
+                s16x4 vf[2][2][2][2];
+                auto column = [&](int x, int y) {           // read number y of eight: columns 64 x .. + 63
+                    const int odd = y & 1, half = (y >> 1) & 1, ks = y >> 2;
+                    const int at = (val_at ^ ((x & 1) * 128 + odd * 64 + half * 32)) + (x >> 1) * 256 +
+                                   (16 * ks + 8 * half) * (RA * 16);
+                    vf[x & 1][odd][ks][half] =
+                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
                 };
-                columns(0);
 #pragma unroll
-                for (int x = 0; x < DT; ++x) {
-                    if (x + 1 < DT) columns(x + 1);
+                for (int y = 0; y < 8; ++y) column(0, y);
 #pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) {
-                        const s16x8 v = __builtin_shufflevector(vf[x & 1][ks][0], vf[x & 1][ks][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                        const bf16x8 vb = __builtin_bit_cast(bf16x8, v);
-                        o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(whi[ks]), o[x], 0, 0, 0);
-                        o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(wlo[ks]), o[x], 0, 0, 0);
+                for (int x = 0; x < DT / 2; ++x) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int odd = y & 1, ks = y >> 2;
+                        const bf16x8 vb = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(
+                            vf[x & 1][odd][ks][0], vf[x & 1][odd][ks][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                        o[2 * x + odd] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16((y & 2) ? wlo[ks] : whi[ks]),
+                                                                                o[2 * x + odd], 0, 0, 0);
+                        if (x + 1 < DT / 2) column(x + 1, y);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    asm volatile("" : "+a"(o[x]));
-                    __builtin_amdgcn_sched_barrier(0);
+                    asm volatile("" : "+a"(o[2 * x]), "+a"(o[2 * x + 1]));
                 }
             }
+            kw_wait_copies<0>();                            // stages past the row's end are copied too, as zeros
             top = fmaxf(top, __shfl_xor(top, 32));
             const bool past = top > m + 60.f;
             if (!__syncthreads_or(past)) break;
             m = top;
+            look_up(0);
+            kw_barrier();
         }
 
         // ---- the waves of a query tile become one (the ring is free: its copies have landed and been read) ----
@@ -890,46 +966,18 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 const float mw = red_m[w * WQ + qt][ql];
                 la += mw == -INFINITY ? 0.f : red_l[w * WQ + qt][ql] * __builtin_amdgcn_exp2f(mw - ma);
             }
-            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - ma);
-#pragma unroll
-            for (int x = 0; x < DT; ++x) o[x] *= f;
-            // two outputs at a time go through LDS: WK = 2: one from each tile's second wave; WK = 4: waves 1, 2, then 3
-            f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
-            constexpr int TURNS = WK == 2 ? 1 : 2;
-#pragma unroll
-            for (int turn = 0; turn < TURNS; ++turn) {
-                const int mine = WK == 2 ? (kb == 1 ? qt : -1) : (turn == 0 ? (kb == 1 || kb == 2 ? kb - 1 : -1) : (kb == 3 ? 0 : -1));
-                if (mine >= 0) {
-#pragma unroll
-                    for (int x = 0; x < DT; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            buf[mine * (OUT / 4) + (x * 4 + i) * 64 + lane] =
-                                f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
-                }
-                kw_barrier();
-                if (kb == 0) {
-                    const int first = WK == 2 ? qt : 0, last = WK == 2 ? qt : (turn == 0 ? 1 : 0);
-                    for (int from = first; from <= last; ++from)
-#pragma unroll
-                        for (int x = 0; x < DT; ++x)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const f32x4 v = buf[from * (OUT / 4) + (x * 4 + i) * 64 + lane];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) o[x][4 * i + e] += v[e];
-                            }
-                }
-                kw_barrier();
-            }
         }
-        if (kb == 0 && nq > 0) {
+        // Each wave ends with a share of the tile's columns summed over the waves: with each partner it gives away the
+        // half of its columns that the other one keeps.
+        auto tiles = [&](auto first, auto count) {          // what the wave holds at the end goes out
+            constexpr int X0 = decltype(first)::value, N = decltype(count)::value;
+            if (nq <= 0) return;
             if (s0 == 0 && s1 == steps) {
                 if (ql < nq) {
                     const float inv = la > 0.f ? 1.f / la : 0.f;
                     uint16_t *dst = (uint16_t *)a.out + (qrow + ql) * a.Dv;
 #pragma unroll
-                    for (int x = 0; x < DT; ++x)
+                    for (int x = X0; x < X0 + N; ++x)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int d = 32 * x + 8 * i + 4 * hi;
@@ -939,21 +987,60 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                                           pack_bf16(o[x][4 * i + 2] * inv, o[x][4 * i + 3] * inv)};
                             __builtin_amdgcn_sched_barrier(0);
                         }
-                    if (hi == 0) kv_write_stats(a, qrow + ql, ma, la);
+                    if (X0 == 0 && hi == 0) kv_write_stats(a, qrow + ql, ma, la);
                 }
             } else {
                 // a part: lanes side by side (attn_wide_join_kernel reads it the same way)
                 const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
                 f32x4 *dst = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
 #pragma unroll
-                for (int x = 0; x < DT; ++x)
+                for (int x = X0; x < X0 + N; ++x)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         dst[(x * 4 + i) * 64] = f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
-                if (hi == 0) {
+                if (X0 == 0 && hi == 0) {
                     a.part_ml[(slot * 32 + ql) * 2] = ma;
                     a.part_ml[(slot * 32 + ql) * 2 + 1] = la;
                 }
+            }
+        };
+        auto give_and_take = [&](auto keep, auto give, auto count, int partner) {
+            constexpr int K0 = decltype(keep)::value, G0 = decltype(give)::value, N = decltype(count)::value;
+            f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    buf[wave * (OUT / 8) + (x * 4 + i) * 64 + lane] =
+                        f32x4{o[G0 + x][4 * i], o[G0 + x][4 * i + 1], o[G0 + x][4 * i + 2], o[G0 + x][4 * i + 3]};
+            kw_barrier();
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 v = buf[partner * (OUT / 8) + (x * 4 + i) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[K0 + x][4 * i + e] += v[e];
+                }
+            kw_barrier();
+        };
+        if constexpr (WK == 1) {
+            tiles(KwInt<0>{}, KwInt<DT>{});
+        } else {
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - ma);
+#pragma unroll
+            for (int x = 0; x < DT; ++x) o[x] *= f;
+            constexpr int H = DT / 2, Q = DT / 4;
+            if (kb & 1) give_and_take(KwInt<H>{}, KwInt<0>{}, KwInt<H>{}, wave ^ WQ);
+            else give_and_take(KwInt<0>{}, KwInt<H>{}, KwInt<H>{}, wave ^ WQ);
+            if constexpr (WK == 2) {
+                if (kb) tiles(KwInt<H>{}, KwInt<H>{});
+                else tiles(KwInt<0>{}, KwInt<H>{});
+            } else {
+                if (kb == 0) give_and_take(KwInt<0>{}, KwInt<Q>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<0>{}, KwInt<Q>{});
+                else if (kb == 1) give_and_take(KwInt<H>{}, KwInt<H + Q>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<H>{}, KwInt<Q>{});
+                else if (kb == 2) give_and_take(KwInt<Q>{}, KwInt<0>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<Q>{}, KwInt<Q>{});
+                else give_and_take(KwInt<H + Q>{}, KwInt<H>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<H + Q>{}, KwInt<Q>{});
             }
         }
         kw_barrier();                                       // red_m, red_l and the ring are free again
