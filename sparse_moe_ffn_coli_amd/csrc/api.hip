@@ -197,14 +197,14 @@ struct AttnWs {
     long s_ld;
 };
 
-AttnWs attn_ws(const coli_kv_shape *s, bool acc)
+AttnWs attn_ws(const coli_kv_shape *s, int32_t idx_k, bool acc)
 {
     AttnWs w{};
     const size_t heads = (size_t)s->B * s->Hq, cap = (size_t)s->max_pages * s->page;
-    w.plan = coli::attn_plan(s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16);
+    w.plan = coli::attn_plan(s->B, s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16, idx_k ? idx_k : (int)cap);
     w.s_ld = (long)((cap + 31) / 32 * 32);
     // a range leaves at most two parts: of the row it begins in and of the one it ends in
-    const size_t part_rows = (size_t)2 * w.plan.n_wg * w.plan.tile_rows;
+    const size_t part_rows = w.plan.direct ? 0 : (size_t)2 * w.plan.n_wg * w.plan.tile_rows;
     w.part_o = 0;
     w.part_ml = align_up(w.part_o + part_rows * w.plan.out_cols * 4);
     w.stats = align_up(w.part_ml + part_rows * 8);
@@ -660,7 +660,7 @@ size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32
     // a shape that either kind of cache allows
     if (check_kv_shape(s, false) != COLI_OK && check_kv_shape(s, true) != COLI_OK) return 0;
     if (idx_k < 0 || idx_k > (1 << 24) || (idx_k && acc)) return 0;
-    const size_t n = attn_ws(s, acc != 0).total;
+    const size_t n = attn_ws(s, idx_k, acc != 0).total;
     return n > 256 ? n : 256;
 }
 
@@ -682,7 +682,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || !aligned16(idx) || !aligned16(acc_in) ||
         !aligned16(acc_out) || !aligned16(lse))
         return COLI_E_ALIGN;
-    const AttnWs L = attn_ws(s, acc_out != nullptr);
+    const AttnWs L = attn_ws(s, idx_k, acc_out != nullptr);
     if (ws_bytes < L.total) return COLI_E_WORKSPACE;
     const size_t elt = kv_elt(s), pool = kv_pool_rows(s), heads = (size_t)s->B * s->Hq;
     const size_t accb = acc_out ? (size_t)s->B * s->Hkv * ld * 4 : 0;
@@ -705,14 +705,14 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     a.scale_hi = (float)sc;
     a.scale_lo = (float)(sc - (double)a.scale_hi);
     a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
-    a.q_tiles = L.plan.q_tiles; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
+    a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
     char *base = (char *)ws;
     a.part_o = (float *)(base + L.part_o);
     a.part_ml = (float *)(base + L.part_ml);
     a.stats = acc_out ? (float *)(base + L.stats) : nullptr;
     a.scores = acc_out ? (float *)(base + L.scores) : nullptr;
     a.s_ld = L.s_ld;
-    return coli::launch_attn(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+    return coli::launch_attn(a, L.plan, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
 }
 
 coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const float *acc, int64_t ld,

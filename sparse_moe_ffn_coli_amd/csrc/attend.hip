@@ -31,7 +31,8 @@ constexpr int KV_NT = 256;                    // threads per workgroup (4 waves)
 constexpr int KV_WAVES = KV_NT / 64;
 constexpr int KV_STEP = 32;                   // positions per step of a wave
 constexpr int KV_QT = 16;                     // query heads per matrix tile
-constexpr int KV_MAX_WG = 1024;               // most ranges
+constexpr int KV_MAX_WG = 768;                // most ranges
+constexpr int KV_DIRECT_STEPS = 32;           // longest rows that run whole, a workgroup each
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short bf16x8s __attribute__((ext_vector_type(8)));
@@ -44,11 +45,12 @@ __device__ __forceinline__ int kv_len(const AttnLaunch &a, int b)
 __device__ __forceinline__ int kv_steps(int n) { return (n + KV_STEP - 1) / KV_STEP; }
 
 // Work is counted in units: the steps of a row (a cache head's query tile of
-// one sequence), but no less than KV_MIN_UNITS for a row that has any, since
-// a short row costs its latencies and not its steps (a range of eight
-// one-step rows took 40 us).
-constexpr int KV_MIN_UNITS = 8;
-__device__ __forceinline__ int kv_units(int n) { return n > 0 ? max(kv_steps(n), KV_MIN_UNITS) : 0; }
+// one sequence), rounded up to whole KV_ROW_UNITS.  A short row costs its
+// latencies and not its steps (a range of eight one-step rows took 40 us),
+// and a border just before a row's end would give one workgroup two rows'
+// latencies (25 against 16 thousand cycles).
+constexpr int KV_ROW_UNITS = 8;
+__device__ __forceinline__ int kv_units(int n) { return (kv_steps(n) + KV_ROW_UNITS - 1) / KV_ROW_UNITS * KV_ROW_UNITS; }
 
 // Units of all sequences before b, and of all (per row of a sequence).  Every
 // wave computes it by itself: no barriers, and one load for up to 64
@@ -142,18 +144,17 @@ __device__ __forceinline__ int kv_pool_row(const AttnLaunch &a, int pg, int h, i
                  (uint32_t)(p & ((1 << a.page_shift) - 1)));
 }
 
-// Pool row of entry p of sequence b's positions (of its list, where there is
-// one) for cache head h; -1: hidden.
-__device__ __forceinline__ int kv_row(const AttnLaunch &a, int b, int h, int n, int len, int p)
+// Pool row of entry e < end of sequence b's positions (of its list, where
+// there is one) for cache head h; -1: hidden.  No branches, and the table is
+// read before the length is known: its loads wait for nothing.
+__device__ __forceinline__ int kv_row(const AttnLaunch &a, int b, int h, int end, int len, int e)
 {
-    bool ok = p < n;
-    if (a.idx) {
-        p = ok ? a.idx[(size_t)b * a.idx_k + p] : -1;
-        ok = p >= 0 && p < len;
-    }
-    if (!ok) return -1;
-    const int pg = a.table[(size_t)b * a.max_pages + (p >> a.page_shift)];
-    return (pg >= 0 && pg < a.n_pages) ? kv_pool_row(a, pg, h, p) : -1;
+    int p = e;
+    if (a.idx) p = a.idx[(size_t)b * a.idx_k + min(e, a.idx_k - 1)];
+    const int at = min(max(p, 0), a.cap - 1);
+    const int pg = a.table[(size_t)b * a.max_pages + (at >> a.page_shift)];
+    const bool ok = e < end && p >= 0 && p < len && pg >= 0 && pg < a.n_pages;
+    return ok ? kv_pool_row(a, pg, h, at) : -1;
 }
 
 // ---- operands -----------------------------------------------------------------
@@ -218,15 +219,26 @@ __device__ __forceinline__ float quad_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-template <bool BF16, int DK, int DV>
-__global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
+// Zeros for the rows of an empty sequence, by the whole workgroup.
+__device__ __forceinline__ void kv_write_empty(const AttnLaunch &a, size_t qrow, int nq)
+{
+    for (size_t i = threadIdx.x; i < (size_t)nq * a.Dv; i += blockDim.x) {
+        if (a.bf16) ((uint16_t *)a.out)[qrow * a.Dv + i] = 0;
+        else ((float *)a.out)[qrow * a.Dv + i] = 0.f;
+    }
+    if ((int)threadIdx.x < nq) kv_write_stats(a, qrow + threadIdx.x, -INFINITY, 0.f);
+}
+
+// NW waves; `a.direct`: a workgroup per row, none of them cut.
+template <bool BF16, int DK, int DV, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
 {
     using KT = KvTile<BF16, DK, DV>;
     using T = typename KT::T;
     constexpr int EPL = KT::EPL, KC = KT::KC, VE = KT::VE, VC = KT::VC, VW = KT::VW;
     constexpr int RS = DV + 4;                // padded row of the join buffer
-    __shared__ __attribute__((aligned(16))) float red[2][KV_QT][RS];
-    __shared__ float red_m[KV_WAVES][KV_QT], red_l[KV_WAVES][KV_QT];
+    __shared__ __attribute__((aligned(16))) float red[NW][KV_QT][RS];
+    __shared__ float red_m[NW][KV_QT], red_l[NW][KV_QT];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, g = lane >> 4;
@@ -234,20 +246,33 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
     const int R = a.Hkv * a.q_tiles;
 
     KvRange rg;
-    if (!kv_first(a, R, rg)) return;
+    if (a.direct) {
+        rg.b = blockIdx.x / R;
+        rg.row = blockIdx.x - rg.b * R;
+        rg.n = kv_len(a, rg.b);
+        rg.steps = kv_steps(rg.n);
+        rg.u = rg.s0 = 0;
+        rg.u_end = max(rg.steps, 1);
+    } else if (!kv_first(a, R, rg)) {
+        return;
+    }
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
 
     const T *kpool = (const T *)a.k;
     const T *vpool = (const T *)(a.v ? a.v : a.k);
     const int vstride = a.v ? a.Dv : a.Dk;
+    const int key_chunks = (a.Dk + 4 * EPL - 1) / (4 * EPL);
 
     for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
-        if (s0 >= steps) continue;            // a short row's units past its steps
-        const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * KV_QT;
+        const int h = a.q_tiles == 1 ? row : row / a.q_tiles, q0 = (row - h * a.q_tiles) * KV_QT;
         const int nq = min(KV_QT, G - q0);    // query heads of this tile
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
+        if (s0 >= steps) {                    // a row's units past its steps, or (direct) an empty row
+            if (a.direct) return kv_write_empty(a, qrow, nq);
+            continue;
+        }
         const int len = min(max(a.lens[b], 0), a.cap);
 
         // the query tile: lane (j, g) holds query j's elements as a key's
@@ -267,7 +292,8 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
         float m = -INFINITY, l = 0.f;
 
         // pool row of position `lane & 31` of step s (-1: hidden)
-        auto rows_of = [&](int s) { return s < s1 ? kv_row(a, b, h, n, len, s * KV_STEP + (lane & 31)) : -1; };
+        const int end = min(n, s1 * KV_STEP);
+        auto rows_of = [&](int s) { return kv_row(a, b, h, end, len, s * KV_STEP + (lane & 31)); };
         u32x4 kf[2][KC];
         auto load_keys = [&](int rows) {
 #pragma unroll
@@ -277,7 +303,7 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
                     const int d = (4 * c + g) * EPL;      // past the key's width: a zero of the query meets it
-                    kf[t][c] = *reinterpret_cast<const u32x4 *>(p + (d < a.Dk ? d : 0));
+                    if (c < key_chunks) kf[t][c] = *reinterpret_cast<const u32x4 *>(p + (d < a.Dk ? d : 0));
                 }
             }
         };
@@ -305,34 +331,36 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
         };
 
         int s = s0 + wave;
-        int rows = rows_of(s), rows_next = rows_of(s + KV_WAVES);
+        int rows = rows_of(s), rows_next = rows_of(s + NW);
         if (s < s1) {
             load_keys(rows);
             load_values(rows);
         }
-        for (; s < s1; s += KV_WAVES) {
-            const bool more = s + KV_WAVES < s1;
+        for (; s < s1; s += NW) {
+            const bool more = s + NW < s1;
             // ---- scores: D[key][query] = K Q^T, two tiles of 16 keys ----
             f32x4 sc[2];
+            sc[0] = sc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < KC; ++c) {
+                if (c >= key_chunks) break;
+                if constexpr (BF16) {
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    if constexpr (BF16) {
+                    for (int t = 0; t < 2; ++t)
                         sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[t][c]), as_bf16(qf[c]), sc[t], 0, 0, 0);
-                    } else {
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
                             sc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kf[t][c][e]),
                                                                         __uint_as_float(qf[c][e]), sc[t], 0, 0, 0);
-                    }
                 }
             }
             const int rows_now = rows;
             rows = rows_next;
             if (more) load_keys(rows);
-            rows_next = rows_of(s + 2 * KV_WAVES);
+            rows_next = rows_of(s + 2 * NW);
 
             // ---- weights: lane (j, g) holds query j, positions 16 t + 4 g + r ----
             float t2[8];
@@ -421,59 +449,54 @@ __global__ __launch_bounds__(KV_NT) void attn_kernel(AttnLaunch a)
             if (more) load_values(rows);
         }
 
-        // ---- the four waves' parts become one ----
+        // ---- the waves' parts become one ----
         l = quad_sum(l);
         if (g == 0) {
             red_m[wave][j] = m;
             red_l[wave][j] = l;
         }
-        __syncthreads();
-        float ma = red_m[0][j];
+        if (j < nq) {
 #pragma unroll
-        for (int w = 1; w < KV_WAVES; ++w) ma = fmaxf(ma, red_m[w][j]);
-        const float f = (m == -INFINITY) ? 0.f : __builtin_amdgcn_exp2f(m - ma);
+            for (int c = 0; c < VC; ++c)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if ((wave >> 1) == half && j < nq) {
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int c = 0; c < VC; ++c)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float *dst = &red[wave & 1][j][(16 * c + 4 * g + r) * VE];
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            const float v = o[c][e][r] * f;
-                            dst[e] = half ? dst[e] + v : v;
-                        }
-                    }
-            }
-            __syncthreads();
+                    for (int e = 0; e < VE; ++e) red[wave][j][(16 * c + 4 * g + r) * VE + e] = o[c][e][r];
         }
+        __syncthreads();
         const bool whole = s0 == 0 && s1 == steps;
         const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
-        for (int i = tid; i < nq * DV; i += KV_NT) {
-            const int q = i / DV, d = i % DV;
+        // four columns of a query a thread
+        for (int i = tid; i < nq * (DV / 4); i += 64 * NW) {
+            const int q = i / (DV / 4), d = i % (DV / 4) * 4;
             if (d >= a.Dv) continue;
-            const float v = red[0][q][d] + red[1][q][d];
             float mq = red_m[0][q], lq = 0.f;
 #pragma unroll
-            for (int w = 1; w < KV_WAVES; ++w) mq = fmaxf(mq, red_m[w][q]);
+            for (int w = 1; w < NW; ++w) mq = fmaxf(mq, red_m[w][q]);
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < KV_WAVES; ++w)
-                lq += (red_m[w][q] == -INFINITY) ? 0.f : red_l[w][q] * __builtin_amdgcn_exp2f(red_m[w][q] - mq);
+            for (int w = 0; w < NW; ++w) {
+                const float f = red_m[w][q] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(red_m[w][q] - mq);
+                lq += red_l[w][q] * f;
+                v += *reinterpret_cast<const f32x4 *>(&red[w][q][d]) * f;
+            }
             if (whole) {
-                const float y = lq > 0.f ? v / lq : 0.f;
-                if constexpr (BF16) ((uint16_t *)a.out)[(qrow + q) * a.Dv + d] = f32_to_bf16_bits(y);
-                else ((float *)a.out)[(qrow + q) * a.Dv + d] = y;
+                const float inv = lq > 0.f ? 1.f / lq : 0.f;
+                const size_t at = (qrow + q) * a.Dv + d;
+                if constexpr (BF16)
+                    *reinterpret_cast<u32x2 *>((uint16_t *)a.out + at) =
+                        u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
+                else *reinterpret_cast<f32x4 *>((float *)a.out + at) = v * inv;
                 if (d == 0) kv_write_stats(a, qrow + q, mq, lq);
             } else {
-                a.part_o[((size_t)slot * KV_QT + q) * a.Dv + d] = v;
+                *reinterpret_cast<f32x4 *>(a.part_o + ((size_t)slot * KV_QT + q) * a.Dv + d) = v;
                 if (d == 0) {
                     a.part_ml[((size_t)slot * KV_QT + q) * 2] = mq;
                     a.part_ml[((size_t)slot * KV_QT + q) * 2 + 1] = lq;
                 }
             }
         }
+        if (a.direct) return;
         __syncthreads();                      // the join buffer is free again
     }
 }
@@ -492,14 +515,7 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
     kv_prefix(a, b, &before, &total);
     const int n = kv_len(a, b), steps = kv_steps(n);
     const int qi = hq % G, row = hq / G * a.q_tiles + qi / KV_QT, q = qi % KV_QT;
-    if (steps == 0) {
-        for (int d = tid; d < a.Dv; d += KV_NT) {
-            if (a.bf16) ((uint16_t *)a.out)[(size_t)blockIdx.x * a.Dv + d] = 0;
-            else ((float *)a.out)[(size_t)blockIdx.x * a.Dv + d] = 0.f;
-        }
-        if (tid == 0) kv_write_stats(a, blockIdx.x, -INFINITY, 0.f);
-        return;
-    }
+    if (steps == 0) return kv_write_empty(a, blockIdx.x, 1);
     const int range = kv_range(a, total * R);
     const int u0 = before * R + row * kv_units(n), u1 = u0 + steps;
     const int w0 = u0 / range, w1 = (u1 - 1) / range;
@@ -1135,37 +1151,58 @@ __global__ __launch_bounds__(KV_NT) void attn_weights_kernel(AttnLaunch a)
     }
 }
 
-// How a shape runs.  Rows past 256 elements are latent caches (host check);
-// in bf16 they take the LDS kernel.
-AttnPlan attn_plan(int Hq, int Hkv, int Dk, int Dv, bool bf16)
+// How a call runs.  entries: the longest row (the cache's capacity, or the
+// listed positions).
+AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entries)
 {
     AttnPlan p{};
-    const int G = Hq / Hkv;
+    const int G = Hq / Hkv, d = Dk > Dv ? Dk : Dv;
+    const int steps = (entries + KV_STEP - 1) / KV_STEP;
+    // Rows past 256 elements are latent caches (host check); in bf16 they take
+    // the LDS kernel.
     p.wide = bf16 && Dk > 256;
     if (p.wide) {
         p.wq = G <= 32 ? 1 : G <= 64 ? 2 : 4;
         p.tile_rows = 32 * p.wq;
         p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
-        p.n_wg = 256;                     // one workgroup per CU: the ring fills its LDS
+        p.n_wg = 256;                         // one workgroup per CU: the ring fills its LDS
     } else {
         p.tile_rows = KV_QT;
         p.out_cols = Dv;
-        p.n_wg = KV_MAX_WG;
+        // as many as the registers let run at once
+        p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 256 ? 256 : 512;
+        p.n_wg = 256 * (bf16 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1));
     }
-    p.min_units = KV_MIN_UNITS;
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
+    p.min_units = p.wide ? KV_ROW_UNITS : 4;
+    // Short rows: a workgroup each, and no join.
+    const long rows = (long)B * Hkv * p.q_tiles;
+    p.direct = !p.wide && steps <= KV_DIRECT_STEPS;
+    p.waves = p.direct && (bf16 ? d <= 128 : d <= 64) && steps > KV_WAVES ? 8 : KV_WAVES;
+    if (p.direct) p.n_wg = (int)rows;
     return p;
 }
 
-template <bool BF16>
-static void launch_main(const AttnLaunch &a, hipStream_t st)
+template <bool BF16, int DK, int DV>
+static void launch_tier(const AttnLaunch &a, int waves, hipStream_t st)
 {
-    const int d = max(a.Dk, a.Dv);
-    if (d <= 64) attn_kernel<BF16, 64, 64><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if (d <= 128) attn_kernel<BF16, 128, 128><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if (d <= 256) attn_kernel<BF16, 256, 256><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if constexpr (!BF16) attn_kernel<BF16, 576, 512><<<a.n_wg, KV_NT, 0, st>>>(a);
-    attn_join_kernel<<<a.B * a.Hq, KV_NT, 0, st>>>(a);
+    if constexpr (DV <= (BF16 ? 128 : 64)) {
+        if (waves == 8) {
+            attn_kernel<BF16, DK, DV, 8><<<a.n_wg, 512, 0, st>>>(a);
+            return;
+        }
+    }
+    attn_kernel<BF16, DK, DV, KV_WAVES><<<a.n_wg, KV_NT, 0, st>>>(a);
+}
+
+template <bool BF16>
+static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
+{
+    if (p.tier == 64) launch_tier<BF16, 64, 64>(a, p.waves, st);
+    else if (p.tier == 128) launch_tier<BF16, 128, 128>(a, p.waves, st);
+    else if (p.tier == 256) launch_tier<BF16, 256, 256>(a, p.waves, st);
+    else if constexpr (!BF16) launch_tier<BF16, 576, 512>(a, p.waves, st);
+    if (!a.direct) attn_join_kernel<<<a.B * a.Hq, KV_NT, 0, st>>>(a);
 }
 
 template <int DK, int DV, int WQ>
@@ -1183,13 +1220,12 @@ static void launch_wide(const AttnLaunch &a, int wq, hipStream_t st)
     else launch_wide<DK, DV, 4>(a, st);
 }
 
-hipError_t launch_attn(const AttnLaunch &a, hipStream_t st)
+hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 {
-    const AttnPlan p = attn_plan(a.Hq, a.Hkv, a.Dk, a.Dv, a.bf16);
     if (p.wide && p.out_cols == 256) launch_wide<320, 256>(a, p.wq, st);
     else if (p.wide) launch_wide<576, 512>(a, p.wq, st);
-    else if (a.bf16) launch_main<true>(a, st);
-    else launch_main<false>(a, st);
+    else if (a.bf16) launch_main<true>(a, p, st);
+    else launch_main<false>(a, p, st);
     if (a.acc_out) {
         const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
         attn_weights_kernel<<<a.B * a.Hkv * chunks, KV_NT, 0, st>>>(a);

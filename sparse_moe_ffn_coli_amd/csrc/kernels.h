@@ -76,7 +76,8 @@ struct AttnLaunch {
     float *acc_out;        // nullable
     long ld;
     int q_tiles;           // query tiles per cache head
-    int n_wg, min_units;   // ranges of the main kernel; fewest steps in one
+    bool direct;           // a workgroup per row
+    int n_wg, min_units;   // ranges of the main kernel (direct: rows); fewest steps in one
     float *part_o;         // workspace [2 n_wg][tile rows][Dv]: unnormalised parts
     float *part_ml;        // workspace [2 n_wg][tile rows][2]: their references and sums
     float *stats;          // workspace [B][Hq][2]: reference and 1 / sum (running weights only)
@@ -90,6 +91,8 @@ struct AttnPlan {
     int wq;                // its query tiles per workgroup
     int tile_rows, q_tiles;     // query heads a workgroup takes at a time, and how often per cache head
     int out_cols;          // columns of a part's rows
+    int tier, waves;       // the other kernels' width and waves per workgroup
+    bool direct;           // a workgroup per row, no parts
     int n_wg, min_units;
 };
 
@@ -115,10 +118,10 @@ struct EvictLaunch {
     long new_ld;
 };
 
-hipError_t launch_attn(const AttnLaunch &a, hipStream_t st);
+hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st);
 hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
-AttnPlan attn_plan(int Hq, int Hkv, int Dk, int Dv, bool bf16);
+AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entries);
 
 hipError_t launch_route(const RouteLaunch &a, hipStream_t st);
 // rows_per_len consecutive rows share an entry of lens
