@@ -74,10 +74,12 @@ __device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int *befor
     *total = __builtin_amdgcn_readlane(wave_scan_incl(all), 63);
 }
 
-// Units of one workgroup's range.
+// Units of one workgroup's range: half of KV_ROW_UNITS, or whole ones, so that
+// borders and rows' ends meet where the work is small.
 __device__ __forceinline__ int kv_range(const AttnLaunch &a, int units)
 {
-    return max((units + a.n_wg - 1) / a.n_wg, a.min_units);
+    const int even = (units + a.n_wg - 1) / a.n_wg;
+    return even <= a.min_units ? a.min_units : (even + KV_ROW_UNITS - 1) / KV_ROW_UNITS * KV_ROW_UNITS;
 }
 
 // A workgroup's range: units u .. u_end - 1, beginning with unit s0 (a step,
@@ -198,9 +200,13 @@ struct KvTile {
 };
 
 // lse of a query row, and its reference and 1 / sum for the running weights.
-__device__ __forceinline__ void kv_write_stats(const AttnLaunch &a, size_t q, float m, float l)
+__device__ __forceinline__ void kv_write_lse(const AttnLaunch &a, size_t q, float m, float l)
 {
     if (a.lse) a.lse[q] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+__device__ __forceinline__ void kv_write_stats(const AttnLaunch &a, size_t q, float m, float l)
+{
+    kv_write_lse(a, q, m, l);
     if (a.stats) {
         a.stats[2 * q] = m == -INFINITY ? 0.f : m;
         a.stats[2 * q + 1] = l > 0.f ? 1.f / l : 0.f;
@@ -501,38 +507,53 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     }
 }
 
-// One workgroup per (sequence, query head): joins the parts that the ranges'
-// borders left of it, or writes an empty sequence's zeros.  The parts are
-// summed in the order of the positions.
-__global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
+// Where the parts of a row are: ranges w0 .. w1 hold some of it (w0 = w1: one
+// holds all, and has written the row's results); the first part's slot, the
+// later ranges' being their first ones.
+struct KvParts {
+    int steps, w0, w1, first;
+    __device__ __forceinline__ int slot(int w) const { return w == w0 ? first : 2 * w; }
+};
+__device__ __forceinline__ KvParts kv_parts(const AttnLaunch &a, int b, int row, int before, int total)
+{
+    const int R = a.Hkv * a.q_tiles, n = kv_len(a, b);
+    KvParts p{kv_steps(n), 0, 0, 0};
+    if (p.steps == 0) return p;
+    const int range = kv_range(a, total * R);
+    const int u0 = before * R + row * kv_units(n);
+    p.w0 = u0 / range;
+    p.w1 = (u0 + p.steps - 1) / range;
+    p.first = 2 * p.w0 + (u0 == p.w0 * range ? 0 : 1);
+    return p;
+}
+
+// One (sequence, query head): joins the parts that the ranges' borders left of
+// it, or writes an empty sequence's zeros.  The parts are summed in the order
+// of the positions.
+__device__ __forceinline__ void attn_join(const AttnLaunch &a, int bq)
 {
     __shared__ __attribute__((aligned(16))) float red[KV_NT * 4];
     __shared__ float factor[KV_MAX_WG];
     const int tid = threadIdx.x;
-    const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-    const int G = a.Hq / a.Hkv, R = a.Hkv * a.q_tiles;
+    const int b = bq / a.Hq, hq = bq - b * a.Hq;
+    const int G = a.Hq / a.Hkv, h = hq / G, qi = hq - h * G, q = qi % KV_QT;
     int before, total;
     kv_prefix(a, b, &before, &total);
-    const int n = kv_len(a, b), steps = kv_steps(n);
-    const int qi = hq % G, row = hq / G * a.q_tiles + qi / KV_QT, q = qi % KV_QT;
-    if (steps == 0) return kv_write_empty(a, blockIdx.x, 1);
-    const int range = kv_range(a, total * R);
-    const int u0 = before * R + row * kv_units(n), u1 = u0 + steps;
-    const int w0 = u0 / range, w1 = (u1 - 1) / range;
-    if (w0 == w1) return;                     // one range holds all of it
-    const int first_slot = 2 * w0 + (u0 == w0 * range ? 0 : 1);
-    auto slot_of = [&](int w) { return (size_t)(w == w0 ? first_slot : 2 * w) * KV_QT + q; };
+    const KvParts p = kv_parts(a, b, h * a.q_tiles + qi / KV_QT, before, total);
+    if (p.steps == 0) return kv_write_empty(a, bq, 1);
+    if (p.w0 == p.w1) return;
+    auto slot_of = [&](int w) { return (size_t)p.slot(w) * KV_QT + q; };
 
     float mx = -INFINITY;
-    for (int w = w0 + (tid & 63); w <= w1; w += 64) mx = fmaxf(mx, a.part_ml[slot_of(w) * 2]);
+    for (int w = p.w0 + (tid & 63); w <= p.w1; w += 64) mx = fmaxf(mx, a.part_ml[slot_of(w) * 2]);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float l = 0.f;
-    for (int w = w0 + (tid & 63); w <= w1; w += 64) {
+    for (int w = p.w0 + (tid & 63); w <= p.w1; w += 64) {
         const float f = __builtin_amdgcn_exp2f(a.part_ml[slot_of(w) * 2] - ref);
         l += a.part_ml[slot_of(w) * 2 + 1] * f;
-        if (tid < 64) factor[w - w0] = f;
+        if (tid < 64) factor[w - p.w0] = f;
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
@@ -543,22 +564,106 @@ __global__ __launch_bounds__(KV_NT) void attn_join_kernel(AttnLaunch a)
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     if (grp < ng) {
 #pragma unroll 4
-        for (int w = w0 + grp; w <= w1; w += ng)
-            acc += *reinterpret_cast<const f32x4 *>(a.part_o + slot_of(w) * a.Dv + 4 * col) * factor[w - w0];
+        for (int w = p.w0 + grp; w <= p.w1; w += ng)
+            acc += *reinterpret_cast<const f32x4 *>(a.part_o + slot_of(w) * a.Dv + 4 * col) * factor[w - p.w0];
         *reinterpret_cast<f32x4 *>(red + 4 * tid) = acc;
     }
     __syncthreads();
     if (tid < cols) {
         for (int x = 1; x < ng; ++x) acc += *reinterpret_cast<const f32x4 *>(red + 4 * (x * cols + col));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float y = l > 0.f ? acc[x] / l : 0.f;
-            const size_t at = (size_t)blockIdx.x * a.Dv + 4 * col + x;
-            if (a.bf16) ((uint16_t *)a.out)[at] = f32_to_bf16_bits(y);
-            else ((float *)a.out)[at] = y;
-        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t at = (size_t)bq * a.Dv + 4 * col;
+        if (a.bf16)
+            *reinterpret_cast<u32x2 *>((uint16_t *)a.out + at) =
+                u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+        else *reinterpret_cast<f32x4 *>((float *)a.out + at) = acc * inv;
     }
-    if (tid == 0) kv_write_stats(a, blockIdx.x, mx, l);
+    if (tid == 0) kv_write_lse(a, bq, mx, l);
+}
+
+// Running weights of 4 KV_NT positions of a (sequence, cache head):
+// acc_out = acc_in + sum over its query heads of e^(t - m) / l, four positions
+// a thread.  The references m and sums l come from the row's writer or, where
+// it was cut, from its parts (the wide kernel's join, which runs before,
+// leaves them like a writer).
+__device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool joined)
+{
+    __shared__ float stat[KV_NT][2];
+    const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
+    const int tid = threadIdx.x;
+    const int bh = at / chunks, b = bh / a.Hkv, h = bh - b * a.Hkv, G = a.Hq / a.Hkv;
+    const int n = min(max(a.lens[b], 0), a.cap);
+    const int p0 = (at - bh * chunks) * KV_NT * 4;
+    if (p0 >= n) return;
+    int before = 0, total = 0;
+    if (!joined && !a.direct) kv_prefix(a, b, &before, &total);
+    const int p = p0 + tid * 4;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < G; i0 += KV_NT) {
+        if (i0 + tid < G) {
+            const int i = i0 + tid;
+            const size_t q = (size_t)b * a.Hq + h * G + i;
+            float m, inv;
+            KvParts parts{};
+            if (!joined && !a.direct) parts = kv_parts(a, b, h * a.q_tiles + i / KV_QT, before, total);
+            if (parts.w0 == parts.w1) {
+                m = a.stats[2 * q];
+                inv = a.stats[2 * q + 1];
+            } else {
+                // one pass, eight parts' loads in flight
+                m = 0.f;
+                float mx = -INFINITY, l = 0.f;
+                for (int w = parts.w0; w <= parts.w1; w += 8) {
+                    float mw[8], lw[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float *ml = a.part_ml + ((size_t)parts.slot(min(w + x, parts.w1)) * KV_QT + i % KV_QT) * 2;
+                        mw[x] = w + x <= parts.w1 ? ml[0] : -INFINITY;
+                        lw[x] = ml[1];
+                    }
+                    float mn = mx;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) mn = fmaxf(mn, mw[x]);
+                    m = mn == -INFINITY ? 0.f : mn;
+                    l *= __builtin_amdgcn_exp2f(mx - m);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) l += mw[x] == -INFINITY ? 0.f : lw[x] * __builtin_amdgcn_exp2f(mw[x] - m);
+                    mx = mn;
+                }
+                inv = l > 0.f ? 1.f / l : 0.f;
+            }
+            stat[tid][0] = m;
+            stat[tid][1] = inv;
+        }
+        __syncthreads();
+        if (p < n)
+            for (int i = i0; i < min(G, i0 + KV_NT); ++i) {
+                const f32x4 t =
+                    *reinterpret_cast<const f32x4 *>(a.scores + ((size_t)b * a.Hq + h * G + i) * a.s_ld + p);
+                const float m = stat[i - i0][0], inv = stat[i - i0][1];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sum[x] += __builtin_amdgcn_exp2f(t[x] - m) * inv;
+            }
+        __syncthreads();
+    }
+    if (p >= n) return;
+    const size_t to = (size_t)bh * a.ld + p;
+    if (p + 4 <= n) {
+        if (a.acc_in) sum += *reinterpret_cast<const f32x4 *>(a.acc_in + to);
+        *reinterpret_cast<f32x4 *>(a.acc_out + to) = sum;
+    } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (p + x < n) a.acc_out[to + x] = sum[x] + (a.acc_in ? a.acc_in[to + x] : 0.f);
+    }
+}
+
+// What follows the main kernel, in one launch: n_join workgroups join, the
+// others keep the running weights.
+__global__ __launch_bounds__(KV_NT) void attn_finish_kernel(AttnLaunch a, int n_join, bool joined)
+{
+    if ((int)blockIdx.x < n_join) attn_join(a, blockIdx.x);
+    else attn_weights(a, blockIdx.x - n_join, joined);
 }
 
 // ---- wide latent caches -------------------------------------------------------
@@ -1085,7 +1190,7 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
     if (nq <= 0) return;
     int before, total;
     kv_prefix(a, b, &before, &total);
-    const int n = kv_len(a, b), steps = kv_steps(n);
+    const KvParts p = kv_parts(a, b, row, before, total);
     const size_t q = (size_t)b * a.Hq + h * G + q0 + ql;
     uint16_t *out = (uint16_t *)a.out + q * a.Dv;
     // wave i of the workgroup holds the i-th 8 columns of each tile: its lanes' are 8 i + 4 hi + 0..3
@@ -1093,16 +1198,12 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
 #pragma unroll
     for (int x = 0; x < KJ_COLS; ++x) sum[x] = f32x4{0.f, 0.f, 0.f, 0.f};
     float mx = -INFINITY, l = 0.f;
-    if (steps > 0) {
-        const int range = kv_range(a, total * R);
-        const int u0 = before * R + row * kv_units(n), u1 = u0 + steps;
-        const int w0 = u0 / range, w1 = (u1 - 1) / range;
-        if (w0 == w1) return;                               // one range holds all of it
-        const int first = 2 * w0 + (u0 == w0 * range ? 0 : 1);
-        auto slot_of = [&](int w) { return (size_t)(w == w0 ? first : 2 * w) * WQ + qt; };
-        for (int w = w0; w <= w1; ++w) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
+    if (p.steps > 0) {
+        if (p.w0 == p.w1) return;                           // one range holds all of it
+        auto slot_of = [&](int w) { return (size_t)p.slot(w) * WQ + qt; };
+        for (int w = p.w0; w <= p.w1; ++w) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
         const float ref = mx == -INFINITY ? 0.f : mx;
-        for (int w = w0; w <= w1; ++w) {
+        for (int w = p.w0; w <= p.w1; ++w) {
             const size_t sl = slot_of(w);
             const float f = __builtin_amdgcn_exp2f(a.part_ml[(sl * 32 + ql) * 2] - ref);
             l += a.part_ml[(sl * 32 + ql) * 2 + 1] * f;
@@ -1121,34 +1222,6 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
                                                         pack_bf16(sum[x][2] * inv, sum[x][3] * inv)};
     }
     if (part == 0 && wave == 0 && hi == 0) kv_write_stats(a, q, mx, l);
-}
-
-// Running weights: acc_out = acc_in + sum over the cache head's query heads
-// of e^(t - m) / l, four positions a thread.
-__global__ __launch_bounds__(KV_NT) void attn_weights_kernel(AttnLaunch a)
-{
-    const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
-    const int bh = blockIdx.x / chunks, b = bh / a.Hkv, h = bh % a.Hkv, G = a.Hq / a.Hkv;
-    const int n = min(max(a.lens[b], 0), a.cap);
-    const int p = ((int)blockIdx.x % chunks * KV_NT + (int)threadIdx.x) * 4;
-    if (p >= n) return;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < G; ++i) {
-        const size_t qrow = (size_t)b * a.Hq + h * G + i;
-        const f32x4 t = *reinterpret_cast<const f32x4 *>(a.scores + qrow * a.s_ld + p);
-        const float m = a.stats[2 * qrow], inv = a.stats[2 * qrow + 1];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] += __builtin_amdgcn_exp2f(t[x] - m) * inv;
-    }
-    const size_t at = (size_t)bh * a.ld + p;
-    if (p + 4 <= n) {
-        if (a.acc_in) sum += *reinterpret_cast<const f32x4 *>(a.acc_in + at);
-        *reinterpret_cast<f32x4 *>(a.acc_out + at) = sum;
-    } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (p + x < n) a.acc_out[at + x] = sum[x] + (a.acc_in ? a.acc_in[at + x] : 0.f);
-    }
 }
 
 // How a call runs.  entries: the longest row (the cache's capacity, or the
@@ -1202,7 +1275,6 @@ static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
     else if (p.tier == 128) launch_tier<BF16, 128, 128>(a, p.waves, st);
     else if (p.tier == 256) launch_tier<BF16, 256, 256>(a, p.waves, st);
     else if constexpr (!BF16) launch_tier<BF16, 576, 512>(a, p.waves, st);
-    if (!a.direct) attn_join_kernel<<<a.B * a.Hq, KV_NT, 0, st>>>(a);
 }
 
 template <int DK, int DV, int WQ>
@@ -1226,10 +1298,9 @@ hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
     else if (p.wide) launch_wide<576, 512>(a, p.wq, st);
     else if (a.bf16) launch_main<true>(a, p, st);
     else launch_main<false>(a, p, st);
-    if (a.acc_out) {
-        const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
-        attn_weights_kernel<<<a.B * a.Hkv * chunks, KV_NT, 0, st>>>(a);
-    }
+    const int n_join = p.wide || p.direct ? 0 : a.B * a.Hq;
+    const int n_weights = a.acc_out ? a.B * a.Hkv * ((a.cap + 4 * KV_NT - 1) / (4 * KV_NT)) : 0;
+    if (n_join + n_weights > 0) attn_finish_kernel<<<n_join + n_weights, KV_NT, 0, st>>>(a, n_join, p.wide);
     return hipGetLastError();
 }
 

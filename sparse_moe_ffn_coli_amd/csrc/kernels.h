@@ -124,7 +124,8 @@ hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
 AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entries);
 
 hipError_t launch_route(const RouteLaunch &a, hipStream_t st);
-// rows_per_len consecutive rows share an entry of lens
+// rows_per_len consecutive rows share an entry of lens; k may pass the 4096 of
+// the public selection
 hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, const int32_t *lens, int rows_per_len,
                              int k, int tail, int32_t *idx, hipStream_t st);
 hipError_t launch_ffn(const FfnLaunch &a, hipStream_t st);

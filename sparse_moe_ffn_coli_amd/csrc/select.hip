@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t score_key(float f)
 
 constexpr int SEL_CAP = 32768;           // positions whose keys a workgroup keeps in LDS (128 KB)
 constexpr int SEL_PER = SEL_CAP / (4 * SEL_NT);   // 16-byte loads per thread for a cached row
-constexpr int SEL_MAX_K = 4096;          // largest k
+constexpr int SEL_MAX_K = 4096;          // longest output row that is put together in LDS
 
 // Barrier for LDS traffic only: every wave's LDS operations have completed
 // (global loads in flight, such as the next row's prefetch, are not waited for).
@@ -294,6 +294,10 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
 // Persistent workgroups: workgroup b takes rows b, b + G, b + 2G, ...  While
 // a cached row is being selected, the next row's scores are already loading
 // into registers, so the row reads overlap the selection work.
+// LONG_K: output rows past SEL_MAX_K go to memory as they are found, rows past
+// SEL_CAP are its own too, and the next row is loaded in its turn (the
+// registers are needed).
+template <bool LONG_K>
 __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restrict__ scores, int rows, int L,
                                                             long ld, const int32_t *__restrict__ lens,
                                                             int rows_per_len, int k, int tail,
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
     __shared__ int32_t ws[SEL_WAVES];
     __shared__ int32_t sel_s[2];
     __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
-    __shared__ __attribute__((aligned(16))) int32_t staged[SEL_MAX_K];   // the output row
+    __shared__ __attribute__((aligned(16))) int32_t staged[LONG_K ? 4 : SEL_MAX_K];   // the output row
     const int tid = threadIdx.x;
     auto row_len = [&](int r) { return lens ? min(max(lens[r / rows_per_len], 0), L) : L; };
     for (int b = tid; b < 2048; b += SEL_NT) hist[b] = 0;
@@ -317,17 +321,21 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
             for (int j = tid; j < k; j += SEL_NT) out[j] = j < n ? j : -1;
             continue;
         }
-        if (n > SEL_CAP) continue;                // index_topk_long_kernel's row
+        if (!LONG_K && n > SEL_CAP) continue;     // index_topk_long_kernel's row
         const float *__restrict__ row = scores + (size_t)r * ld;
         const int tail0 = n - min(tail, k);       // positions >= tail0 are always kept
         __syncthreads();                          // the previous row is done with keys / hist
+        if (LONG_K && n > SEL_CAP) {              // (it leaves the histogram clear, as it found it)
+            select_uncached(row, n, tail0, k, hist, ws, sel_s, wave_gt, wave_eq, out);
+            continue;
+        }
         if (have != r) load_row(row, n, v);
         store_keys(row, n, tail0, v, keys, hist);
         lds_barrier();
         // the next row of this workgroup starts loading now
         have = -1;
         const int rn = r + gridDim.x;
-        if (rn < rows) {
+        if (!LONG_K && rn < rows) {
             const int nn = row_len(rn);
             if (nn > k && nn <= SEL_CAP) {
                 load_row(scores + (size_t)rn * ld, nn, v);
@@ -364,6 +372,10 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
             prefix |= (uint32_t)pick_bin(hist, nb, need, ws, sel_s, &above) << shift;
             need -= above;
         }
+        if constexpr (LONG_K) {
+            compact_cached(keys, n, k, prefix, need, wave_gt, wave_eq, out);
+            continue;
+        }
         compact_cached(keys, n, k, prefix, need, wave_gt, wave_eq, staged);
         lds_barrier();
         if ((k & 3) == 0) {
@@ -375,13 +387,11 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
     }
 }
 
-// Rows longer than `skip` positions: one workgroup per row, every pass
-// re-reading the scores; the other rows are left to index_topk_kernel (skip =
-// SEL_CAP), or there are none (skip = -1: k past SEL_MAX_K, whose output row
-// the other kernels cannot stage).
+// Rows longer than SEL_CAP, where the other kernels leave them: one workgroup
+// per row, every pass re-reading the scores.
 __global__ __launch_bounds__(SEL_NT) void index_topk_long_kernel(const float *__restrict__ scores, int L, long ld,
                                                                  const int32_t *__restrict__ lens,
-                                                                 int rows_per_len, int skip, int k, int tail,
+                                                                 int rows_per_len, int k, int tail,
                                                                  int32_t *__restrict__ idx)
 {
     __shared__ int32_t hist[2048];
@@ -390,11 +400,7 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_long_kernel(const float *__
     __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
     const int r = blockIdx.x;
     const int n = lens ? min(max(lens[r / rows_per_len], 0), L) : L;
-    if (n <= skip) return;
-    if (n <= k) {                                 // the whole row, then -1
-        for (int j = threadIdx.x; j < k; j += SEL_NT) idx[(size_t)r * k + j] = j < n ? j : -1;
-        return;
-    }
+    if (n <= SEL_CAP || n <= k) return;
     for (int b = threadIdx.x; b < 2048; b += SEL_NT) hist[b] = 0;
     __syncthreads();
     select_uncached(scores + (size_t)r * ld, n, n - min(tail, k), k, hist, ws, sel_s, wave_gt, wave_eq,
@@ -615,8 +621,9 @@ hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, cons
                              int k, int tail, int32_t *idx, hipStream_t st)
 {
     if (rows == 0) return hipSuccess;
+    const int grid = min(rows, 256);
     if (k > SEL_MAX_K) {
-        index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, -1, k, tail, idx);
+        index_topk_kernel<true><<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
         return hipGetLastError();
     }
     // more rows than CUs: the register-key kernel; otherwise one workgroup
@@ -627,11 +634,10 @@ hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, cons
         // for one cached-row workgroup per CU, each row's latency deciding)
         index_topk_reg_kernel<<<rows, SR_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, k, tail, idx);
     } else {
-        const int grid = min(rows, 256);
-        index_topk_kernel<<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
+        index_topk_kernel<false><<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
     }
     if (L > SEL_CAP && L > k)
-        index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, SEL_CAP, k, tail, idx);
+        index_topk_long_kernel<<<rows, SEL_NT, 0, st>>>(scores, L, ld, lens, rows_per_len, k, tail, idx);
     return hipGetLastError();
 }
 
