@@ -242,6 +242,11 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     using KT = KvTile<BF16, DK, DV>;
     using T = typename KT::T;
     constexpr int EPL = KT::EPL, KC = KT::KC, VE = KT::VE, VC = KT::VC, VW = KT::VW;
+    // BIG: too wide for a step's rows in registers; keys are taken KP chunks at
+    // a time, values chunk by chunk, each read one ahead of its products.
+    constexpr bool BIG = DK > 256;
+    constexpr int KP = BIG ? (KC % 6 == 0 ? 6 : 5) : KC;
+    static_assert(!BIG || (KC % KP == 0 && !BF16), "whole groups; bf16 takes the LDS kernel");
     constexpr int RS = DV + 4;                // padded row of the join buffer
     __shared__ __attribute__((aligned(16))) float red[NW][KV_QT][RS];
     __shared__ float red_m[NW][KV_QT], red_l[NW][KV_QT];
@@ -300,45 +305,57 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
         // pool row of position `lane & 31` of step s (-1: hidden)
         const int end = min(n, s1 * KV_STEP);
         auto rows_of = [&](int s) { return kv_row(a, b, h, end, len, s * KV_STEP + (lane & 31)); };
-        u32x4 kf[2][KC];
-        auto load_keys = [&](int rows) {
+        u32x4 kf[2][BIG ? 2 * KP : KC];
+        auto load_keys = [&](int rows, int c0 = 0) {      // (BIG: KP chunks from c0 on, into their half of the buffer)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int r = max(__shfl(rows, 16 * t + j), 0);
                 const T *p = kpool + (size_t)r * a.Dk;
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const int d = (4 * c + g) * EPL;      // past the key's width: a zero of the query meets it
-                    if (c < key_chunks) kf[t][c] = *reinterpret_cast<const u32x4 *>(p + (d < a.Dk ? d : 0));
+                for (int x = 0; x < KP; ++x) {
+                    const int c = c0 + x, d = (4 * c + g) * EPL;      // past the key's width: a zero of the query meets it
+                    if (BIG || c < key_chunks) kf[t][BIG ? c % (2 * KP) : c] = *reinterpret_cast<const u32x4 *>(p + (d < a.Dk ? d : 0));
                 }
             }
         };
-        uint32_t vf[VC][8][VW];
-        auto load_values = [&](int rows) {
+        uint32_t vf[BIG ? 2 : VC][8][VW];
+        auto load_values = [&](int rows, int c0 = 0) {    // (BIG: chunk c0)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = max(__shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3)), 0);
                 const T *p = vpool + (size_t)r * vstride;
 #pragma unroll
-                for (int c = 0; c < VC; ++c) {
+                for (int x = 0; x < (BIG ? 1 : VC); ++x) {
+                    const int c = BIG ? c0 : x, to = BIG ? c0 & 1 : x;
                     const int d = (16 * c + j) * VE;      // past the value's width: columns that are not written
                     const T *src = p + (d < a.Dv ? d : 0);
                     if constexpr (VW == 4) {
-                        const u32x4 x = *reinterpret_cast<const u32x4 *>(src);
+                        const u32x4 v = *reinterpret_cast<const u32x4 *>(src);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) vf[c][i][w] = x[w];
+                        for (int w = 0; w < 4; ++w) vf[to][i][w] = v[w];
                     } else {
-                        const u32x2 x = *reinterpret_cast<const u32x2 *>(src);
-                        vf[c][i][0] = x[0];
-                        vf[c][i][1] = x[1];
+                        const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
+                        vf[to][i][0] = v[0];
+                        vf[to][i][1] = v[1];
                     }
                 }
             }
         };
+        // what stands in hidden rows (NaN, infinities) must not count
+        auto clear_hidden = [&](int rows, int first, int last) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (__shfl(rows, 16 * (i >> 2) + 4 * g + (i & 3)) < 0) {
+#pragma unroll
+                    for (int c = first; c < last; ++c)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) vf[c][i][x] = 0u;
+                }
+        };
 
         int s = s0 + wave;
         int rows = rows_of(s), rows_next = rows_of(s + NW);
-        if (s < s1) {
+        if (!BIG && s < s1) {
             load_keys(rows);
             load_values(rows);
         }
@@ -347,25 +364,35 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
             // ---- scores: D[key][query] = K Q^T, two tiles of 16 keys ----
             f32x4 sc[2];
             sc[0] = sc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                if (c >= key_chunks) break;
+            auto product = [&](const u32x4 &k0, const u32x4 &k1, int c) {
                 if constexpr (BF16) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[t][c]), as_bf16(qf[c]), sc[t], 0, 0, 0);
+                    sc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k0), as_bf16(qf[c]), sc[0], 0, 0, 0);
+                    sc[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k1), as_bf16(qf[c]), sc[1], 0, 0, 0);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            sc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kf[t][c][e]),
-                                                                        __uint_as_float(qf[c][e]), sc[t], 0, 0, 0);
+                    for (int e = 0; e < 4; ++e) {
+                        sc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k0[e]), __uint_as_float(qf[c][e]), sc[0], 0, 0, 0);
+                        sc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k1[e]), __uint_as_float(qf[c][e]), sc[1], 0, 0, 0);
+                    }
                 }
+            };
+            if constexpr (BIG) {
+                load_keys(rows, 0);
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    if (c % KP == 0 && c + KP < KC) load_keys(rows, c + KP);
+                    product(kf[0][c % (2 * KP)], kf[1][c % (2 * KP)], c);
+                    if (c % KP == KP - 1) __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+                    if (c < key_chunks) product(kf[0][c], kf[1][c], c);
             }
             const int rows_now = rows;
             rows = rows_next;
-            if (more) load_keys(rows);
+            if (!BIG && more) load_keys(rows);
+            if constexpr (BIG) load_values(rows_now);
             rows_next = rows_of(s + 2 * NW);
 
             // ---- weights: lane (j, g) holds query j, positions 16 t + 4 g + r ----
@@ -410,16 +437,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
                 l += w[i];
             }
             // ---- output: O^T[value column][query] += V^T w ----
-            if (hidden) {                     // what stands in hidden rows (NaN, infinities) must not count
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (__shfl(rows_now, 16 * (i >> 2) + 4 * g + (i & 3)) < 0) {
-#pragma unroll
-                        for (int c = 0; c < VC; ++c)
-#pragma unroll
-                            for (int x = 0; x < VW; ++x) vf[c][i][x] = 0u;
-                    }
-            }
+            if (!BIG && hidden) clear_hidden(rows_now, 0, BIG ? 0 : VC);
             if constexpr (BF16) {
                 // each weight as two bf16 parts: 16 bits of it enter the products
                 u32x4 hi, lo;
@@ -444,15 +462,21 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
                     }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int c = 0; c < VC; ++c) {
+                    if constexpr (BIG) {
+                        if (c + 1 < VC) load_values(rows_now, c + 1);
+                        if (hidden) clear_hidden(rows_now, c & 1, (c & 1) + 1);
+                    }
 #pragma unroll
-                    for (int c = 0; c < VC; ++c)
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
                         for (int e = 0; e < VE; ++e)
-                            o[c][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vf[c][i][e]), w[i], o[c][e],
-                                                                          0, 0, 0);
+                            o[c][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vf[BIG ? c & 1 : c][i][e]), w[i],
+                                                                          o[c][e], 0, 0, 0);
+                    if constexpr (BIG) __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            if (more) load_values(rows);
+            if (!BIG && more) load_values(rows);
         }
 
         // ---- the waves' parts become one ----
@@ -1243,7 +1267,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entrie
         p.tile_rows = KV_QT;
         p.out_cols = Dv;
         // as many as the registers let run at once
-        p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 256 ? 256 : 512;
+        p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 256 ? 256 : (d <= 320 && Dv <= 256) ? 320 : 512;
         p.n_wg = 256 * (bf16 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1));
     }
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
@@ -1274,7 +1298,10 @@ static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
     if (p.tier == 64) launch_tier<BF16, 64, 64>(a, p.waves, st);
     else if (p.tier == 128) launch_tier<BF16, 128, 128>(a, p.waves, st);
     else if (p.tier == 256) launch_tier<BF16, 256, 256>(a, p.waves, st);
-    else if constexpr (!BF16) launch_tier<BF16, 576, 512>(a, p.waves, st);
+    else if constexpr (!BF16) {
+        if (p.tier == 320) launch_tier<BF16, 320, 256>(a, p.waves, st);
+        else launch_tier<BF16, 576, 512>(a, p.waves, st);
+    }
 }
 
 template <int DK, int DV, int WQ>

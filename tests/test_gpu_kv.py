@@ -592,3 +592,24 @@ def test_attn_latent_long_ranges(Hq):
     few = dict(c, table=c["table"][pick], lens=c["lens"][pick])
     r = ref.attn(few, q[pick], 0.1)
     within(out[pick].double().cpu().numpy(), r["out"], r["tol_out"], "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,Dk,Dv,page,latent", [
+    (8, 2, 64, 64, 16, False), (3, 3, 8, 8, 1, False), (12, 12, 80, 80, 2, False), (14, 2, 128, 128, 64, False),
+    (5, 1, 96, 40, 4, False), (34, 2, 192, 128, 32, False), (16, 1, 256, 256, 128, False), (32, 1, 128, 64, 16, True),
+    (16, 1, 576, 512, 64, True), (100, 1, 320, 256, 32, True), (8, 4, 296, 264, 8, True), (3, 1, 264, 8, 16, True),
+    (64, 1, 512, 512, 64, True), (40, 1, 400, 384, 16, True)])
+def test_attn_rows_cut_into_ranges(dtype, Hq, Hkv, Dk, Dv, page, latent):
+    # a table long enough that rows are not taken whole: ranges begin and end inside them
+    c = ref.make_cache(BORDERS + [1100, 0, 4000], Hkv, Dk, Dv, page, dtype, latent, seed=Hq * 1000 + Dk + 1)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk))
+    acc = np.random.default_rng(2).random((16, Hkv, c["max_pages"] * page // 4 * 4 + 4)).astype(np.float32)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), acc_in=acc)
+
+
+@pytest.mark.parametrize("dtype,Hq,Dk,Dv,latent", [("bf16", 4, 128, 128, False), ("f32", 2, 576, 512, True)])
+def test_attn_more_heads_than_a_workgroups_threads(dtype, Hq, Dk, Dv, latent):
+    c = ref.make_cache([40, 3], 1, Dk, Dv, 16, dtype, latent, seed=71)
+    acc = np.random.default_rng(2).random((2, 1, c["max_pages"] * 16)).astype(np.float32)
+    run_attn(c, 260 * Hq // 2, 0.1, acc_in=acc)
