@@ -128,6 +128,19 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
     return true;
 }
 
+// A workgroup's range, or (direct) its row, which may be empty.
+__device__ __forceinline__ bool kv_begin(const AttnLaunch &a, int R, KvRange &rg)
+{
+    if (!a.direct) return kv_first(a, R, rg);
+    rg.b = blockIdx.x / R;
+    rg.row = blockIdx.x - rg.b * R;
+    rg.n = kv_len(a, rg.b);
+    rg.steps = kv_steps(rg.n);
+    rg.u = rg.s0 = 0;
+    rg.u_end = max(rg.steps, 1);
+    return true;
+}
+
 // The next row of a range (past the last sequence: one that is never taken).
 __device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, int &n, int &steps, int &row)
 {
@@ -257,16 +270,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     const int R = a.Hkv * a.q_tiles;
 
     KvRange rg;
-    if (a.direct) {
-        rg.b = blockIdx.x / R;
-        rg.row = blockIdx.x - rg.b * R;
-        rg.n = kv_len(a, rg.b);
-        rg.steps = kv_steps(rg.n);
-        rg.u = rg.s0 = 0;
-        rg.u_end = max(rg.steps, 1);
-    } else if (!kv_first(a, R, rg)) {
-        return;
-    }
+    if (!kv_begin(a, R, rg)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
 
@@ -660,7 +664,8 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
             stat[tid][1] = inv;
         }
         __syncthreads();
-        if (p < n)
+        if (p < n) {
+#pragma unroll 8
             for (int i = i0; i < min(G, i0 + KV_NT); ++i) {
                 const f32x4 t =
                     *reinterpret_cast<const f32x4 *>(a.scores + ((size_t)b * a.Hq + h * G + i) * a.s_ld + p);
@@ -668,6 +673,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sum[x] += __builtin_amdgcn_exp2f(t[x] - m) * inv;
             }
+        }
         __syncthreads();
     }
     if (p >= n) return;
@@ -721,6 +727,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int KW_ROWS = 32;                   // positions of a stage
+constexpr int KW_MAX_WG = 256;                // ranges: one workgroup per CU, the ring fills its LDS
 constexpr int KW_RING = 4;                    // stages in LDS
 constexpr int KW_BLOCK = 32;                  // stages whose rows are looked up at a time
 
@@ -814,7 +821,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
 
     for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
-        if (s0 >= steps) continue;            // a short row's units past its steps
+        if (s0 >= steps) continue;            // a row's units past its steps
         // The lane number is made opaque here (and in issue): the offsets that
         // follow from it are cheap to form again, and kept over the whole row
         // loop they would push the operands out of the registers.
@@ -1201,6 +1208,7 @@ template <int DV, int WQ>
 __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
 {
     constexpr int SPLIT = DV / 32 / KJ_COLS;
+    __shared__ float factor[KW_MAX_WG][32], red[KV_NT / 32][32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int ql = lane & 31, hi = lane >> 5;
     int at = blockIdx.x;
@@ -1225,13 +1233,29 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
     if (p.steps > 0) {
         if (p.w0 == p.w1) return;                           // one range holds all of it
         auto slot_of = [&](int w) { return (size_t)p.slot(w) * WQ + qt; };
-        for (int w = p.w0; w <= p.w1; ++w) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
+        // the parts' factors for the 32 queries: the workgroup's eight groups of 32 threads take every eighth part
+        const int grp = tid >> 5;
+        for (int w = p.w0 + grp; w <= p.w1; w += KV_NT / 32) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
+        red[grp][ql] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < KV_NT / 32; ++x) mx = fmaxf(mx, red[x][ql]);
         const float ref = mx == -INFINITY ? 0.f : mx;
+        for (int w = p.w0 + grp; w <= p.w1; w += KV_NT / 32) {
+            const float f = __builtin_amdgcn_exp2f(a.part_ml[(slot_of(w) * 32 + ql) * 2] - ref);
+            l += a.part_ml[(slot_of(w) * 32 + ql) * 2 + 1] * f;
+            factor[w - p.w0][ql] = f;
+        }
+        __syncthreads();
+        red[grp][ql] = l;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int x = 0; x < KV_NT / 32; ++x) l += red[x][ql];
+#pragma unroll 4
         for (int w = p.w0; w <= p.w1; ++w) {
-            const size_t sl = slot_of(w);
-            const float f = __builtin_amdgcn_exp2f(a.part_ml[(sl * 32 + ql) * 2] - ref);
-            l += a.part_ml[(sl * 32 + ql) * 2 + 1] * f;
-            const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + sl * (32 * DV)) + lane;
+            const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + slot_of(w) * (32 * DV)) + lane;
+            const float f = factor[w - p.w0][ql];
 #pragma unroll
             for (int x = 0; x < KJ_COLS; ++x) sum[x] += src[((part * KJ_COLS + x) * 4 + wave) * 64] * f;
         }
@@ -1262,7 +1286,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entrie
         p.wq = G <= 32 ? 1 : G <= 64 ? 2 : 4;
         p.tile_rows = 32 * p.wq;
         p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
-        p.n_wg = 256;                         // one workgroup per CU: the ring fills its LDS
+        p.n_wg = KW_MAX_WG;
     } else {
         p.tile_rows = KV_QT;
         p.out_cols = Dv;

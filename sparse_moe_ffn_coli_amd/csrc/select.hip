@@ -130,6 +130,49 @@ __device__ __forceinline__ int pick_bin(int32_t *hist, int nb, int need, int32_t
     return bin;
 }
 
+// One 256-position step of an ordered compaction: the lane's four keys are of
+// positions p0 .. p0 + 3; gt_b, eq_b: keys above and equal to tau before the
+// step (moved on here).  A lane's count of earlier selected positions in the
+// wave comes from ballots of the four position slots and bit counts below the
+// lane.  A slot is written only inside the row's k outputs.
+__device__ __forceinline__ void place_group(const uint32_t (&q)[4], int p0, int seg1, int k, uint32_t tau, int need,
+                                            int &gt_b, int &eq_b, int32_t *staged)
+{
+    bool g[4], e[4];
+    uint64_t mg[4], me[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const bool in = p0 + c < seg1;
+        g[c] = in && q[c] > tau;
+        e[c] = in && q[c] == tau;
+        mg[c] = __ballot(g[c]);
+        me[c] = __ballot(e[c]);
+    }
+    // selected positions of this step before this lane's first
+    int my_gt = gt_b, my_eq = eq_b;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        my_gt += __builtin_amdgcn_mbcnt_hi((uint32_t)(mg[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mg[c], 0));
+        my_eq += __builtin_amdgcn_mbcnt_hi((uint32_t)(me[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)me[c], 0));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (g[c]) {
+            const int slot = my_gt + min(my_eq, need);
+            if (slot < k) staged[slot] = p0 + c;
+            ++my_gt;
+        } else if (e[c]) {
+            if (my_eq < need) staged[my_gt + my_eq] = p0 + c;
+            ++my_eq;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        gt_b += __popcll(mg[c]);
+        eq_b += __popcll(me[c]);
+    }
+}
+
 // Ordered compaction of a cached row: wave w owns positions [seg0, seg1)
 // (whole groups of 256: four consecutive positions per lane), counts its keys
 // above and equal to tau, takes its starting counts from the waves before it,
@@ -184,39 +227,8 @@ __device__ __forceinline__ void compact_cached(const uint32_t *keys, int n, int 
         const int p0 = seg0 + 256 * it + 4 * lane;
         if (seg0 + 256 * it >= seg1) break;       // uniform over the wave
         const u32x4 q = group(it);
-        bool g[4], e[4];
-        uint64_t mg[4], me[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const bool in = p0 + c < seg1;
-            g[c] = in && q[c] > tau;
-            e[c] = in && q[c] == tau;
-            mg[c] = __ballot(g[c]);
-            me[c] = __ballot(e[c]);
-        }
-        // selected positions of this step before this lane's first
-        int my_gt = gt_b, my_eq = eq_b;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            my_gt += __builtin_amdgcn_mbcnt_hi((uint32_t)(mg[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mg[c], 0));
-            my_eq += __builtin_amdgcn_mbcnt_hi((uint32_t)(me[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)me[c], 0));
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (g[c]) {
-                const int slot = my_gt + min(my_eq, need);
-                if (slot < k) staged[slot] = p0 + c;
-                ++my_gt;
-            } else if (e[c]) {
-                if (my_eq < need) staged[my_gt + my_eq] = p0 + c;
-                ++my_eq;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            gt_b += __popcll(mg[c]);
-            eq_b += __popcll(me[c]);
-        }
+        const uint32_t keys4[4] = {q[0], q[1], q[2], q[3]};
+        place_group(keys4, p0, seg1, k, tau, need, gt_b, eq_b, staged);
     }
 }
 
@@ -226,18 +238,17 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
                                                 int32_t *__restrict__ out)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto key_at = [&](int i) { return i >= tail0 ? 0xffffffffu : score_key(row[i]); };
-    // f(i, key) for every position, SEL_BATCH per thread with their loads in flight together
-    auto for_each_key = [&](auto &&f) {
-        for (int b0 = 0; b0 < n; b0 += SEL_BATCH * SEL_NT) {
-            uint32_t q[SEL_BATCH];
+    auto key_of = [&](float f, int i) { return i >= n ? 0u : i >= tail0 ? 0xffffffffu : score_key(f); };
+    // the scores of positions i .. i + 3 (i a multiple of four): one load inside the row, none past its end
+    auto scores4 = [&](int i) {
+        if (i + 4 <= n) return *reinterpret_cast<const f32x4 *>(row + i);
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < SEL_BATCH; ++j) q[j] = key_at(min(b0 + j * SEL_NT + tid, n - 1));
-#pragma unroll
-            for (int j = 0; j < SEL_BATCH; ++j)
-                if (b0 + j * SEL_NT + tid < n) f(q[j]);
-        }
+        for (int c = 0; c < 3; ++c)
+            if (i + c < n) v[c] = row[i + c];
+        return v;
     };
+    constexpr int GRP = SEL_BATCH / 2;            // groups of four positions a thread has in flight
     uint32_t prefix = 0;
     int need = k;
 #pragma unroll 1
@@ -245,22 +256,42 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int nb = pass == 2 ? 1024 : 2048;
         const uint32_t hi = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 2 ? 10 : 11));
-        for_each_key([&](uint32_t q) {
-            if ((q & hi) == prefix) atomicAdd(&hist[(q >> shift) & (nb - 1)], 1);
-        });
+        for (int b0 = 4 * tid; b0 < n; b0 += 4 * GRP * SEL_NT) {
+            f32x4 v[GRP];
+#pragma unroll
+            for (int j = 0; j < GRP; ++j) v[j] = scores4(b0 + 4 * j * SEL_NT);
+#pragma unroll
+            for (int j = 0; j < GRP; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int i = b0 + 4 * j * SEL_NT + c;
+                    const uint32_t q = key_of(v[j][c], i);
+                    if (i < n && (q & hi) == prefix) atomicAdd(&hist[(q >> shift) & (nb - 1)], 1);
+                }
+        }
         __syncthreads();
         int above;
         prefix |= (uint32_t)pick_bin(hist, nb, need, ws, sel_s, &above) << shift;
         need -= above;
     }
     const uint32_t tau = prefix;
-    const int seg = ((n + SEL_WAVES - 1) / SEL_WAVES + 63) & ~63;
+    // each wave a contiguous segment, GRP groups of 256 positions at a time
+    const int seg = ((n + SEL_WAVES - 1) / SEL_WAVES + 255) & ~255;
     const int seg0 = min(wave * seg, n), seg1 = min(seg0 + seg, n);
     int gt = 0, eq = 0;
-    for (int i = seg0 + lane; i < seg1; i += 64) {
-        const uint32_t q = key_at(i);
-        gt += q > tau;
-        eq += q == tau;
+    for (int i0 = seg0; i0 < seg1; i0 += 256 * GRP) {
+        f32x4 v[GRP];
+#pragma unroll
+        for (int j = 0; j < GRP; ++j) v[j] = scores4(i0 + 256 * j + 4 * lane);
+#pragma unroll
+        for (int j = 0; j < GRP; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int i = i0 + 256 * j + 4 * lane + c;
+                const uint32_t q = key_of(v[j][c], i);
+                gt += i < seg1 && q > tau;
+                eq += i < seg1 && q == tau;
+            }
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
@@ -277,17 +308,18 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
         gt_b += wave_gt[w2];
         eq_b += wave_eq[w2];
     }
-    const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
-    for (int i0 = seg0; i0 < seg1; i0 += 64) {
-        const int i = i0 + lane;
-        const uint32_t q = (i < seg1) ? key_at(i) : 0u;
-        const bool g = (i < seg1) && q > tau, e = (i < seg1) && q == tau;
-        const uint64_t mg = __ballot(g), me = __ballot(e);
-        const int my_gt = gt_b + __popcll(mg & below), my_eq = eq_b + __popcll(me & below);
-        if (g) out[my_gt + min(my_eq, need)] = i;
-        else if (e && my_eq < need) out[my_gt + my_eq] = i;
-        gt_b += __popcll(mg);
-        eq_b += __popcll(me);
+    for (int i0 = seg0; i0 < seg1; i0 += 256 * GRP) {
+        f32x4 v[GRP];
+#pragma unroll
+        for (int j = 0; j < GRP; ++j) v[j] = scores4(i0 + 256 * j + 4 * lane);
+#pragma unroll
+        for (int j = 0; j < GRP; ++j) {
+            const int p0 = i0 + 256 * j + 4 * lane;
+            uint32_t q[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) q[c] = key_of(v[j][c], p0 + c);
+            place_group(q, p0, seg1, k, tau, need, gt_b, eq_b, out);
+        }
     }
 }
 
