@@ -13,11 +13,10 @@
 // workgroup suffix scan over the bins to find the digit holding the k-th key.
 // Every position whose key is above tau is selected, and of those equal to
 // tau the lowest positions until k are reached.  The selected positions are
-// written in ascending order by an ordered compaction: each wave owns a
-// contiguous segment of the row, counts its keys above and equal to tau,
-// takes its starting counts from a scan over the waves, and then walks its
-// segment 64 positions at a time placing each selected position by ballot
-// popcounts.  Integer work only: the result is unique and reproducible.
+// written in ascending order by an ordered compaction: each thread marks its
+// neighbouring positions above and equal to tau in bit masks, and one scan of
+// their counts over the workgroup gives it its first slot.  Integer work only:
+// the result is unique and reproducible.
 // Rows of up to SEL_CAP positions keep their keys in LDS after one read of
 // the scores; longer rows re-read the scores (from L2) in each pass.  Each
 // workgroup walks several rows and loads the next row's scores into
@@ -101,6 +100,9 @@ __device__ __forceinline__ void store_keys(const float *__restrict__ row, int n,
         keys[i] = q;
         atomicAdd(&hist[q >> 21], 1);
     }
+    // up to the next whole 4 * SEL_NT positions: keys that are never selected (compact_cached)
+    const int whole = (n + 4 * SEL_NT - 1) / (4 * SEL_NT) * (4 * SEL_NT);
+    for (int i = n + (int)threadIdx.x; i < whole; i += SEL_NT) keys[i] = 0u;
 }
 
 // The digit holding the need-th largest key: thread t holds bins nb-1-2t and
@@ -130,114 +132,72 @@ __device__ __forceinline__ int pick_bin(int32_t *hist, int nb, int need, int32_t
     return bin;
 }
 
-// One 256-position step of an ordered compaction: the lane's four keys are of
-// positions p0 .. p0 + 3; gt_b, eq_b: keys above and equal to tau before the
-// step (moved on here).  A lane's count of earlier selected positions in the
-// wave comes from ballots of the four position slots and bit counts below the
-// lane.  A slot is written only inside the row's k outputs.
-__device__ __forceinline__ void place_group(const uint32_t (&q)[4], int p0, int seg1, int k, uint32_t tau, int need,
-                                            int &gt_b, int &eq_b, int32_t *staged)
+// Places a thread's selected positions among the workgroup's: bit i of gt, eq:
+// position first + i is above, equal to tau; gt_b, eq_b: such keys before the
+// workgroup's first (moved on past its last).
+__device__ __forceinline__ void place_masks(uint32_t gt, uint32_t eq, int first, int k, int need, int &gt_b, int &eq_b,
+                                            int32_t *ws, int32_t *out)
 {
-    bool g[4], e[4];
-    uint64_t mg[4], me[4];
+    // at most SEL_CAP positions at a time: both counts fit in 16 bits
+    const uint32_t mine = (uint32_t)__popc(gt) | (uint32_t)__popc(eq) << 16;
+    const uint32_t before = (uint32_t)block_scan_incl_dpp((int)mine, ws) - mine;
+    uint32_t all = 0;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const bool in = p0 + c < seg1;
-        g[c] = in && q[c] > tau;
-        e[c] = in && q[c] == tau;
-        mg[c] = __ballot(g[c]);
-        me[c] = __ballot(e[c]);
-    }
-    // selected positions of this step before this lane's first
-    int my_gt = gt_b, my_eq = eq_b;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        my_gt += __builtin_amdgcn_mbcnt_hi((uint32_t)(mg[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mg[c], 0));
-        my_eq += __builtin_amdgcn_mbcnt_hi((uint32_t)(me[c] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)me[c], 0));
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (g[c]) {
-            const int slot = my_gt + min(my_eq, need);
-            if (slot < k) staged[slot] = p0 + c;
-            ++my_gt;
-        } else if (e[c]) {
-            if (my_eq < need) staged[my_gt + my_eq] = p0 + c;
-            ++my_eq;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        gt_b += __popcll(mg[c]);
-        eq_b += __popcll(me[c]);
-    }
+    for (int w = 0; w < SEL_WAVES; ++w) all += (uint32_t)ws[w];
+    const int my_gt = gt_b + (int)(before & 0xffffu), my_eq = eq_b + (int)(before >> 16);
+    gt_b += (int)(all & 0xffffu);
+    eq_b += (int)(all >> 16);
+    int slot = my_gt + min(my_eq, need);
+    const int keep = min(max(need - my_eq, 0), __popc(eq));
+    if (keep == 0) eq = 0u;
+    for (int drop = __popc(eq) - keep; drop > 0; --drop)      // of equal keys the lowest positions stay
+        eq &= ~(0x80000000u >> __clz((int)eq));
+    for (uint32_t sel = gt | eq; sel; sel &= sel - 1, ++slot)
+        if (slot < k) out[slot] = first + __ffs((int)sel) - 1;
 }
 
-// Ordered compaction of a cached row: wave w owns positions [seg0, seg1)
-// (whole groups of 256: four consecutive positions per lane), counts its keys
-// above and equal to tau, takes its starting counts from the waves before it,
-// and walks its segment 256 positions at a time: a lane's count of earlier
-// selected positions in the wave comes from ballots of the four position
-// slots and bit counts below the lane.  A slot is written only inside the
-// row's k outputs.
-__device__ __forceinline__ void compact_cached(const uint32_t *keys, int n, int k, uint32_t tau, int need,
-                                               int32_t *wave_gt, int32_t *wave_eq, int32_t *staged)
+// Ordered compaction of a cached row: thread t owns the `per` positions from
+// t * per on (a multiple of four, at most 32) and marks those above and equal
+// to tau in two bit masks; one scan over the workgroup of both counts gives it
+// the slot of its first selected position, and the set bits go out in order.
+// A thread reads its groups of four in an order that begins at a place of its
+// own (whole rows of 128 bytes apart, all threads would meet in one bank).
+// (Ballots over 256-position steps of a wave took 21 thousand cycles of the 47
+// thousand of a 32768-position row, this 9.)  Places past the row hold key 0:
+// above no tau, and equal to it only behind all the row's own keys that are,
+// of which there are enough.  A slot is written only inside the row's k
+// outputs.
+__device__ __forceinline__ void compact_cached(const uint32_t *keys, int n, int k, uint32_t tau, int need, int32_t *ws,
+                                               int32_t *staged)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int seg = ((n + SEL_WAVES - 1) / SEL_WAVES + 255) & ~255;
-    const int seg0 = min(wave * seg, n), seg1 = min(seg0 + seg, n);
-    constexpr int MAXIT = SEL_CAP / SEL_WAVES / 256;  // 256-position steps of the longest segment
-    // keys of the segment's step `it` for this lane (past seg1: masked by the caller)
-    auto group = [&](int it) {
-        return *reinterpret_cast<const u32x4 *>(keys + min(seg0 + 256 * it + 4 * lane, SEL_CAP - 4));
-    };
-    int gt = 0, eq = 0;
+    constexpr int MOST = SEL_CAP / SEL_NT / 4;    // groups of a thread
+    const int groups = (n + 4 * SEL_NT - 1) / (4 * SEL_NT), per = 4 * groups;
+    const int first = (int)threadIdx.x * per, turn = (int)threadIdx.x % groups;
+    uint32_t gt = 0, eq = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {                 // half the steps' keys loaded at a time
-        u32x4 q[MAXIT / 2];
+    for (int i = 0; i < MOST; ++i) {
+        if (i >= groups) break;                   // uniform
+        int g = i + turn;
+        g = g >= groups ? g - groups : g;
+        const u32x4 q = *reinterpret_cast<const u32x4 *>(keys + first + 4 * g);
+        uint32_t gt4 = 0, eq4 = 0;
 #pragma unroll
-        for (int j = 0; j < MAXIT / 2; ++j) q[j] = group(h * (MAXIT / 2) + j);
-#pragma unroll
-        for (int j = 0; j < MAXIT / 2; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool in = seg0 + 256 * (h * (MAXIT / 2) + j) + 4 * lane + c < seg1;
-                gt += in && q[j][c] > tau;
-                eq += in && q[j][c] == tau;
-            }
+        for (int c = 0; c < 4; ++c) {
+            gt4 |= q[c] > tau ? 1u << c : 0u;
+            eq4 |= q[c] == tau ? 1u << c : 0u;
+        }
+        gt |= gt4 << (4 * g);
+        eq |= eq4 << (4 * g);
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        gt += __shfl_xor(gt, off);
-        eq += __shfl_xor(eq, off);
-    }
-    if (lane == 0) {
-        wave_gt[wave] = gt;
-        wave_eq[wave] = eq;
-    }
-    lds_barrier();
-    int gt_b = 0, eq_b = 0;                       // keys above / equal to tau before this segment
-#pragma unroll
-    for (int w2 = 0; w2 < SEL_WAVES; ++w2) {
-        gt_b += (w2 < wave) ? wave_gt[w2] : 0;
-        eq_b += (w2 < wave) ? wave_eq[w2] : 0;
-    }
-#pragma unroll
-    for (int it = 0; it < MAXIT; ++it) {
-        const int p0 = seg0 + 256 * it + 4 * lane;
-        if (seg0 + 256 * it >= seg1) break;       // uniform over the wave
-        const u32x4 q = group(it);
-        const uint32_t keys4[4] = {q[0], q[1], q[2], q[3]};
-        place_group(keys4, p0, seg1, k, tau, need, gt_b, eq_b, staged);
-    }
+    int gt_b = 0, eq_b = 0;
+    place_masks(gt, eq, first, k, need, gt_b, eq_b, ws, staged);
 }
 
 // ---- a row too long for LDS: every pass re-reads the scores -----------------
 __device__ __forceinline__ void select_uncached(const float *__restrict__ row, int n, int tail0, int k, int32_t *hist,
-                                                int32_t *ws, int32_t *sel_s, int32_t *wave_gt, int32_t *wave_eq,
-                                                int32_t *__restrict__ out)
+                                                int32_t *ws, int32_t *sel_s, int32_t *__restrict__ out)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x;
     auto key_of = [&](float f, int i) { return i >= n ? 0u : i >= tail0 ? 0xffffffffu : score_key(f); };
     // the scores of positions i .. i + 3 (i a multiple of four): one load inside the row, none past its end
     auto scores4 = [&](int i) {
@@ -274,52 +234,29 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
         prefix |= (uint32_t)pick_bin(hist, nb, need, ws, sel_s, &above) << shift;
         need -= above;
     }
+    // SEL_CAP positions at a time, 32 neighbours a thread (see compact_cached)
     const uint32_t tau = prefix;
-    // each wave a contiguous segment, GRP groups of 256 positions at a time
-    const int seg = ((n + SEL_WAVES - 1) / SEL_WAVES + 255) & ~255;
-    const int seg0 = min(wave * seg, n), seg1 = min(seg0 + seg, n);
-    int gt = 0, eq = 0;
-    for (int i0 = seg0; i0 < seg1; i0 += 256 * GRP) {
-        f32x4 v[GRP];
-#pragma unroll
-        for (int j = 0; j < GRP; ++j) v[j] = scores4(i0 + 256 * j + 4 * lane);
-#pragma unroll
-        for (int j = 0; j < GRP; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int i = i0 + 256 * j + 4 * lane + c;
-                const uint32_t q = key_of(v[j][c], i);
-                gt += i < seg1 && q > tau;
-                eq += i < seg1 && q == tau;
-            }
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        gt += __shfl_xor(gt, off);
-        eq += __shfl_xor(eq, off);
-    }
-    if (lane == 0) {
-        wave_gt[wave] = gt;
-        wave_eq[wave] = eq;
-    }
-    __syncthreads();
     int gt_b = 0, eq_b = 0;
-    for (int w2 = 0; w2 < wave; ++w2) {
-        gt_b += wave_gt[w2];
-        eq_b += wave_eq[w2];
-    }
-    for (int i0 = seg0; i0 < seg1; i0 += 256 * GRP) {
-        f32x4 v[GRP];
+    for (int c0 = 0; c0 < n; c0 += SEL_CAP) {
+        const int first = c0 + 32 * tid;
+        uint32_t gt = 0, eq = 0;
 #pragma unroll
-        for (int j = 0; j < GRP; ++j) v[j] = scores4(i0 + 256 * j + 4 * lane);
+        for (int h = 0; h < 2; ++h) {
+            f32x4 v[4];
 #pragma unroll
-        for (int j = 0; j < GRP; ++j) {
-            const int p0 = i0 + 256 * j + 4 * lane;
-            uint32_t q[4];
+            for (int j = 0; j < 4; ++j) v[j] = scores4(first + 16 * h + 4 * j);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) q[c] = key_of(v[j][c], p0 + c);
-            place_group(q, p0, seg1, k, tau, need, gt_b, eq_b, out);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int x = 16 * h + 4 * j + c;
+                    const uint32_t q = key_of(v[j][c], first + x);    // 0 past the row
+                    gt |= q > tau ? 1u << x : 0u;
+                    eq |= q == tau ? 1u << x : 0u;
+                }
         }
+        place_masks(gt, eq, first, k, need, gt_b, eq_b, ws, out);
+        __syncthreads();                          // ws is free again
     }
 }
 
@@ -339,7 +276,6 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
     __shared__ int32_t hist[2048];
     __shared__ int32_t ws[SEL_WAVES];
     __shared__ int32_t sel_s[2];
-    __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
     __shared__ __attribute__((aligned(16))) int32_t staged[LONG_K ? 4 : SEL_MAX_K];   // the output row
     const int tid = threadIdx.x;
     auto row_len = [&](int r) { return lens ? min(max(lens[r / rows_per_len], 0), L) : L; };
@@ -358,11 +294,17 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
         const int tail0 = n - min(tail, k);       // positions >= tail0 are always kept
         __syncthreads();                          // the previous row is done with keys / hist
         if (LONG_K && n > SEL_CAP) {              // (it leaves the histogram clear, as it found it)
-            select_uncached(row, n, tail0, k, hist, ws, sel_s, wave_gt, wave_eq, out);
+            select_uncached(row, n, tail0, k, hist, ws, sel_s, out);
             continue;
         }
-        if (have != r) load_row(row, n, v);
-        store_keys(row, n, tail0, v, keys, hist);
+        if constexpr (LONG_K) {
+            f32x4 own[SEL_PER];
+            load_row(row, n, own);
+            store_keys(row, n, tail0, own, keys, hist);
+        } else {
+            if (have != r) load_row(row, n, v);
+            store_keys(row, n, tail0, v, keys, hist);
+        }
         lds_barrier();
         // the next row of this workgroup starts loading now
         have = -1;
@@ -395,6 +337,7 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
 #pragma unroll
                 for (int j = 0; j < HALF; ++j) {
                     const int i = 4 * ((h * HALF + j) * SEL_NT + tid);
+                    if (4 * (h * HALF + j) * SEL_NT >= n) break;       // uniform: short rows have fewer groups
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (i + c < n && (g[j][c] & hi) == prefix) atomicAdd(&hist[(g[j][c] >> shift) & (nb - 1)], 1);
@@ -405,10 +348,10 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_kernel(const float *__restr
             need -= above;
         }
         if constexpr (LONG_K) {
-            compact_cached(keys, n, k, prefix, need, wave_gt, wave_eq, out);
+            compact_cached(keys, n, k, prefix, need, ws, out);
             continue;
         }
-        compact_cached(keys, n, k, prefix, need, wave_gt, wave_eq, staged);
+        compact_cached(keys, n, k, prefix, need, ws, staged);
         lds_barrier();
         if ((k & 3) == 0) {
             for (int j = 4 * tid; j < k; j += 4 * SEL_NT)
@@ -429,14 +372,12 @@ __global__ __launch_bounds__(SEL_NT) void index_topk_long_kernel(const float *__
     __shared__ int32_t hist[2048];
     __shared__ int32_t ws[SEL_WAVES];
     __shared__ int32_t sel_s[2];
-    __shared__ int32_t wave_gt[SEL_WAVES], wave_eq[SEL_WAVES];
     const int r = blockIdx.x;
     const int n = lens ? min(max(lens[r / rows_per_len], 0), L) : L;
     if (n <= SEL_CAP || n <= k) return;
     for (int b = threadIdx.x; b < 2048; b += SEL_NT) hist[b] = 0;
     __syncthreads();
-    select_uncached(scores + (size_t)r * ld, n, n - min(tail, k), k, hist, ws, sel_s, wave_gt, wave_eq,
-                    idx + (size_t)r * k);
+    select_uncached(scores + (size_t)r * ld, n, n - min(tail, k), k, hist, ws, sel_s, idx + (size_t)r * k);
 }
 
 // ---- rows of up to SEL_CAP positions, keys held in registers ---------------
@@ -654,7 +595,9 @@ hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, cons
 {
     if (rows == 0) return hipSuccess;
     const int grid = min(rows, 256);
-    if (k > SEL_MAX_K) {
+    // long output rows; and one launch for rows of any length (a second one,
+    // for the long rows alone, costs 4 us where there are none)
+    if (k > SEL_MAX_K || (rows <= SEL_REG_MIN_ROWS && L > SEL_CAP && L > k)) {
         index_topk_kernel<true><<<grid, SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
         return hipGetLastError();
     }

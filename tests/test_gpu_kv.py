@@ -613,3 +613,22 @@ def test_attn_more_heads_than_a_workgroups_threads(dtype, Hq, Dk, Dv, latent):
     c = ref.make_cache([40, 3], 1, Dk, Dv, 16, dtype, latent, seed=71)
     acc = np.random.default_rng(2).random((2, 1, c["max_pages"] * 16)).astype(np.float32)
     run_attn(c, 260 * Hq // 2, 0.1, acc_in=acc)
+
+
+@pytest.mark.parametrize("k,ties", [(300, False), (5000, True), (40000, False)])
+def test_evict_rows_past_the_key_cache(k, ties):
+    # rows of more than 32768 positions beside shorter ones, budgets that are staged and ones that are not
+    run_evict([70001, 32769, 32768, 4096, 12], 1, 8, 8, 64, k, 5, ties=ties, dtype="f32")
+
+
+def test_evict_weights_of_every_kind():
+    # infinities, zeros of both signs, subnormals, one value everywhere: the last positions and the lowest stay
+    def edit(c, acc, new_table):
+        acc[0, 0, :400] = 0.0
+        acc[0, 0, 1:400:2] = -0.0
+        acc[0, 1, :400] = np.inf
+        acc[1, 0, :300] = 1e-45
+        acc[1, 0, 7] = -1e-45
+        acc[1, 1, :300] = -np.inf
+        acc[1, 1, 250:260] = 3.0
+    run_evict([400, 300], 2, 8, 8, 16, 100, 4, edit=edit, dtype="f32")

@@ -116,3 +116,22 @@ def test_index_topk_many_rows_special_values():
     s[2::3, :] = np.float32(1e-45)
     s[2::3, 50:60] = -np.float32(1e-45)
     _check(s, 37, 0, label="many rows: signed zeros / infinities / subnormals")
+
+
+# Lengths around the places where a thread's share of the row changes, and
+# rows past the key cache beside shorter ones in one launch.
+@pytest.mark.parametrize("L,k,tail,ties", [
+    (4095, 64, 4, True), (4096, 2048, 0, True), (4097, 2048, 4, False), (8193, 1, 0, True), (28671, 4096, 4, True),
+    (32767, 2048, 4, False), (32769, 2048, 4, True), (65536, 4096, 0, True), (65537, 33, 4, False),
+])
+def test_index_topk_share_borders(L, k, tail, ties):
+    rng = np.random.default_rng(L)
+    s = (rng.integers(0, 5, size=(3, L)) if ties else rng.standard_normal((3, L))).astype(np.float32)
+    lens = np.array([L, min(L, 32768), max(L - 4097, 0)], np.int32)
+    _check(s, k, tail, lens, label=f"L={L} k={k}")
+
+
+def test_index_topk_one_value():
+    # nothing but ties: the lowest positions, whole threads' shares of them
+    s = np.full((2, 50000), 1.5, np.float32)
+    _check(s, 3000, 4, np.array([50000, 30000], np.int32), label="one value")
