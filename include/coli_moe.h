@@ -317,8 +317,8 @@ coli_status coli_index_topk(const float *scores, int32_t rows, int32_t L, int64_
  * Supported: B >= 0, 1 <= Hkv <= Hq <= 1024 with Hq % Hkv = 0, page a power
  * of two <= 4096, n_pages and max_pages >= 1, Dk and Dv multiples of 8, both
  * <= 256 (a latent cache: Dv <= Dk, Dk <= 576, Dv <= 512),
- * n_pages * Hkv * page and B * Hq * (max_pages * page / 32 + 8) below 2^30,
- * max_pages * page <= 2^24. */
+ * max_pages * page <= 2^24, n_pages * Hkv * page < 2^31, B * Hq <= 2^20,
+ * B * Hq * (max_pages * page / 32 + 8) <= 2^28. */
 typedef struct {
     int32_t B;         /* sequences of the call */
     int32_t Hq, Hkv;   /* query heads; heads of the cache */
@@ -343,7 +343,7 @@ typedef struct {
  * last positions; rows behind start[B] and rows that would come before
  * position 0 are not written anywhere.  start = NULL: one new token per
  * sequence (rows = B), a sequence of length 0 taking none.  A page shared by
- * sequences must not be written through two of them.  Hq is ignored. */
+ * sequences must not be written through two of them.  rows <= 2^25. */
 coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void *v_new, int32_t rows,
                            const int32_t *start, const coli_kv_cache *c, void *stream);
 
@@ -358,6 +358,7 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
  *   idx (nullable, int32 [B][idx_k], as coli_index_topk writes it): only the
  *     listed positions take part; entries outside [0, lens[b]) are skipped
  *     (the -1 padding among them), a position listed twice counts twice.
+ *     1 <= idx_k <= 2^24, B * Hq * (idx_k / 32 + 8) <= 2^28.
  *   acc_out (nullable, fp32 [B][Hkv][ld], ld a multiple of 4, at least
  *     max_pages * page): the running attention weight of each position for
  *     the eviction below,
@@ -390,7 +391,9 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
  *     acc, and 0 from there to new_ld (the next tokens count from 0)
  * Each cache head keeps its own positions; a position listed by `idx` above
  * means the same token for all heads only while Hkv = 1 or nothing was
- * evicted.  1 <= k <= 1 << 24, tail >= 0.  Hq is ignored.  No workspace. */
+ * evicted.  A kept position of a page outside the pool leaves its new row as
+ * it was.  1 <= k <= 2^24, tail >= 0, B * Hkv * (max(k, new_ld) / 64 + 1) <=
+ * 2^23.  No workspace. */
 coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const float *acc, int64_t ld,
                           int32_t k, int32_t tail, const int32_t *new_table, int32_t new_max_pages,
                           int32_t *new_lens, int32_t *kept, float *new_acc, int64_t new_ld,

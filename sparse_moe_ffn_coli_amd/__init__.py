@@ -454,6 +454,10 @@ class KvCache:
     table: object
     lens: object
 
+    def __getstate__(self):
+        # a copy holds the tensors and not what calls have formed from them
+        return {n: v for n, v in self.__dict__.items() if n != "_handles"}
+
     def c(self) -> CKvCache:
         return CKvCache(_ptr(self.k), _ptr(self.v), _ptr(self.table), _ptr(self.lens))
 
@@ -528,6 +532,9 @@ def coli_kv_attn(shape: KvShape, q, cache: KvCache, out, scale: float, idx=None,
     _kv_check("coli_kv_attn", dev, ("q", q, dt, (B, Hq, shape.Dk)), ("out", out, dt, (B, Hq, shape.Dv)),
               ("lse", lse, f32, (B, Hq)), ("idx", idx, torch.int32, (B, idx_k)),
               ("acc_in", acc_in, f32, (B, shape.Hkv, ld)), ("acc_out", acc_out, f32, (B, shape.Hkv, ld)))
+    # an empty tensor has no address, and without one the argument would count as absent
+    if (idx is not None and idx_k == 0) or (acc_out is not None and ld == 0):
+        raise ValueError("coli_kv_attn: idx and acc_out must not be empty")
     if ws is not None and ws.device != dev:
         raise ValueError(f"coli_kv_attn: ws is on {ws.device}, the cache on {dev}")
     _kv_call("coli_kv_attn", dev, cs, _ptr(q), cc, scale, _ptr(idx), idx_k, _ptr(acc_in), _ptr(acc_out), ld, _ptr(out),
@@ -545,6 +552,8 @@ def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_le
     new_ld = 0 if new_acc is None else new_acc.shape[-1]
     _kv_check("coli_kv_evict", dev, ("acc", acc, f32, (B, H, ld)), ("new_table", new_table, i32, (B, cols)),
               ("new_lens", new_lens, i32, (B,)), ("kept", kept, i32, (B, H, k)), ("new_acc", new_acc, f32, (B, H, new_ld)))
+    if new_acc is not None and new_ld == 0:
+        raise ValueError("coli_kv_evict: new_acc must not be empty")
     _kv_call("coli_kv_evict", dev, cs, cc, _ptr(acc), ld, k, tail, _ptr(new_table), cols, _ptr(new_lens), _ptr(kept),
              _ptr(new_acc), new_ld, stream)
 

@@ -153,6 +153,8 @@ coli_status check_dense_shape(const coli_moe_shape *s, coli_moe_shape *inner)
 }
 
 // ---- the paged key-value cache ------------------------------------------------
+int64_t kv_work(const coli_kv_shape *s, int64_t entries) { return (int64_t)s->B * s->Hq * (entries / 32 + 8); }
+
 coli_status check_kv_shape(const coli_kv_shape *s, bool latent)
 {
     if (!s) return COLI_E_NULL;
@@ -164,9 +166,9 @@ coli_status check_kv_shape(const coli_kv_shape *s, bool latent)
     if (s->n_pages < 1 || s->max_pages < 1) return COLI_E_SHAPE;
     const int64_t cap = (int64_t)s->max_pages * s->page;
     if (cap > (1 << 24)) return COLI_E_SHAPE;
-    // pool rows, and the attention's work in steps, fit in int32
+    // pool rows, and the attention's work in steps, fit in int32, and the threads of every launch in 32 bits
     if ((int64_t)s->n_pages * s->Hkv * s->page > INT32_MAX) return COLI_E_SHAPE;
-    if ((int64_t)s->B * s->Hq * (cap / 32 + 8) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if ((int64_t)s->B * s->Hq > (1 << 20) || kv_work(s, cap) > (1 << 28)) return COLI_E_SHAPE;
     return COLI_OK;
 }
 
@@ -210,6 +212,7 @@ AttnWs attn_ws(const coli_kv_shape *s, int32_t idx_k, bool acc)
     w.stats = align_up(w.part_ml + part_rows * 8);
     w.scores = align_up(w.stats + (acc ? heads * 8 : 0));
     w.total = align_up(w.scores + (acc ? heads * (size_t)w.s_ld * 4 : 0));
+    if (w.total < 256) w.total = 256;          // never none: 0 is an invalid shape's answer
     return w;
 }
 
@@ -632,7 +635,7 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
 {
     coli_status st = check_kv_cache(s, c);
     if (st != COLI_OK) return st;
-    if (rows < 0 || (!start && rows != s->B)) return COLI_E_SHAPE;
+    if (rows < 0 || rows > (1 << 25) || (!start && rows != s->B)) return COLI_E_SHAPE;
     if (s->B == 0 || rows == 0) return check_device();
     if (!k_new || !v_new != !c->v) return COLI_E_NULL;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(start)) return COLI_E_ALIGN;
@@ -659,9 +662,8 @@ size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32
 {
     // a shape that either kind of cache allows
     if (check_kv_shape(s, false) != COLI_OK && check_kv_shape(s, true) != COLI_OK) return 0;
-    if (idx_k < 0 || idx_k > (1 << 24) || (idx_k && acc)) return 0;
-    const size_t n = attn_ws(s, idx_k, acc != 0).total;
-    return n > 256 ? n : 256;
+    if (idx_k < 0 || idx_k > (1 << 24) || (idx_k && acc) || kv_work(s, idx_k) > (1 << 28)) return 0;
+    return attn_ws(s, idx_k, acc != 0).total;
 }
 
 coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
@@ -674,7 +676,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     const double sc = (double)scale * 1.4426950408889634074;     // exponents are taken to base 2
     if (!(sc >= -3e38 && sc <= 3e38)) return COLI_E_SHAPE;
     if (idx ? (idx_k < 1 || idx_k > (1 << 24) || acc_out) : idx_k != 0) return COLI_E_SHAPE;
-    if (idx && (int64_t)s->B * s->Hq * (idx_k / 32 + 8) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if (kv_work(s, idx_k) > (1 << 28)) return COLI_E_SHAPE;
     if (acc_in && !acc_out) return COLI_E_NULL;
     if (acc_out && (ld < cap || ld % 4)) return COLI_E_SHAPE;
     if (s->B == 0) return check_device();
@@ -727,7 +729,7 @@ coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const 
     if (new_max_pages < 1 || (int64_t)new_max_pages * s->page < k) return COLI_E_SHAPE;
     if (new_acc && (new_ld < k || new_ld > (1 << 25))) return COLI_E_SHAPE;
     const int64_t span = new_acc && new_ld > k ? new_ld : k;
-    if ((int64_t)s->B * s->Hkv * (span / 32 + 1) > INT32_MAX / 2) return COLI_E_SHAPE;
+    if ((int64_t)s->B * s->Hkv * (span / 64 + 1) > (1 << 23)) return COLI_E_SHAPE;     // threads of the copy: 2^31
     if (s->B == 0) return check_device();
     if (!acc || !new_table || !new_lens || !kept) return COLI_E_NULL;
     if (!aligned16(acc) || !aligned16(new_table) || !aligned16(new_lens) || !aligned16(kept) || !aligned16(new_acc))

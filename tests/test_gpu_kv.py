@@ -632,3 +632,18 @@ def test_evict_weights_of_every_kind():
         acc[1, 1, :300] = -np.inf
         acc[1, 1, 250:260] = 3.0
     run_evict([400, 300], 2, 8, 8, 16, 100, 4, edit=edit, dtype="f32")
+
+
+def test_empty_arguments_do_not_count_as_absent():
+    import torch
+    c = ref.make_cache([40], 2, 64, 64, 16, "bf16", seed=61)
+    s, dev = shape_of(c, 1, 4), cache_of(c)
+    q, out = queries(c, 1, 4).cuda(), torch.empty((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    for bad in (dict(idx=torch.empty((1, 0), dtype=torch.int32, device="cuda")), dict(acc_out=torch.empty((1, 2, 0), device="cuda"))):
+        with pytest.raises(ValueError):
+            coli_kv_attn(s, q, dev, out, 0.1, ws=ws, **bad)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        coli_kv_evict(s, dev, torch.zeros((1, 2, 48), device="cuda"), 8, torch.zeros((1, 1), **i32), torch.zeros(1, **i32),
+                      torch.zeros((1, 2, 8), **i32), new_acc=torch.empty((1, 2, 0), device="cuda"))

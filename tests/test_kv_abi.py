@@ -2,6 +2,7 @@
 addresses that are never dereferenced: every call fails a check before the
 library reaches the device (and the tests run only where there is none).
 Then the plain forms themselves, by hand."""
+import copy
 import ctypes as C
 
 import numpy as np
@@ -56,6 +57,23 @@ def test_shapes_are_refused_everywhere(kw):
     s = shape(**kw)
     rows = max(s.B, 0)
     assert attn(s) == E_SHAPE and append(s, rows=rows) == E_SHAPE and evict(s) == E_SHAPE
+
+
+@no_gpu
+def test_calls_past_the_launches_are_refused():
+    # a launch holds fewer than 2^32 threads
+    for kw in (dict(B=1 << 15, Hq=64), dict(B=1 << 20, Hq=8, max_pages=1), dict(B=1 << 12, max_pages=1 << 13)):
+        s = shape(**kw)
+        assert attn(s) == E_SHAPE and append(s, rows=s.B) == E_SHAPE and evict(s, ld=1 << 17) == E_SHAPE
+        assert pkg.coli_kv_attn_workspace_bytes(s) == 0
+    assert attn(shape(B=1 << 15, max_pages=1)) == E_DEVICE
+    many = shape(B=1 << 15, max_pages=1)
+    assert attn(many, idx=fake(20), idx_k=7904) == E_DEVICE and attn(many, idx=fake(20), idx_k=7936 + 32) == E_SHAPE
+    assert pkg.coli_kv_attn_workspace_bytes(many, idx_k=7936 + 32) == 0
+    assert append(rows=1 << 25, start=fake(20), c=cache()) == E_DEVICE
+    assert append(rows=(1 << 25) + 1, start=fake(20)) == E_SHAPE
+    assert evict(many, ld=16, k=1984 - 64, cols=128) == E_DEVICE and evict(many, ld=16, k=2048, cols=128) == E_SHAPE
+    assert evict(many, ld=16, new_acc=fake(14), new_ld=2048) == E_SHAPE
 
 
 @no_gpu
@@ -182,3 +200,12 @@ def test_plain_eviction_by_hand():
     assert r["kept"].tolist() == [[[0, 2, 3, 5]]] and r["new_lens"].tolist() == [4]      # the newest, then 5 5 5
     assert r["new_acc"].tolist() == [[[5, 5, 5, 2, 0, 0]]]
     assert torch.equal(r["k"][int(new_table[0, 1]), 0, 1], c["k"][int(c["table"][0, 2]), 0, 1])
+
+
+def test_a_copied_cache_forms_its_own_handles():
+    t = torch.zeros(4)
+    c = KvCache(t, None, t.clone(), t.clone())
+    object.__setattr__(c, "_handles", (None, C.byref(C.c_int())))     # as after a call
+    for d in (copy.copy(c), copy.deepcopy(c)):
+        assert "_handles" not in d.__dict__ and torch.equal(d.k, c.k) and d.v is None
+    assert copy.deepcopy(c).k.data_ptr() != c.k.data_ptr() and "_handles" in c.__dict__
