@@ -31,8 +31,7 @@ constexpr int KV_NT = 256;                    // threads per workgroup (4 waves)
 constexpr int KV_WAVES = KV_NT / 64;
 constexpr int KV_STEP = 32;                   // positions per step of a wave
 constexpr int KV_QT = 16;                     // query heads per matrix tile
-constexpr int KV_MAX_WG = 768;                // most ranges
-constexpr int KV_DIRECT_STEPS = 32;           // longest rows that run whole, a workgroup each
+constexpr int KV_MAX_WG = 512;                // most ranges
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short bf16x8s __attribute__((ext_vector_type(8)));
@@ -1283,24 +1282,43 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entrie
     // the LDS kernel.
     p.wide = bf16 && Dk > 256;
     if (p.wide) {
-        p.wq = G <= 32 ? 1 : G <= 64 ? 2 : 4;
+        // Fewer tiles a workgroup: more workgroups for small work, which then
+        // read the cache (out of the caches) more often.  128 heads, us with
+        // 1 / 2 / 4: one row of 512 positions 23.6 / 28.5 / 37.2, 8 of 2048
+        // 32.6 / 35.2 / 44.2, 32 of 1024 51.5 / 46.1 / 51.9, 64 of 2048
+        // 113 / 86 / 93, 64 of 8192 358 / 252 / 241; 64 heads, 1 / 2: one row
+        // of 512 23.8 / 28.7, 8 of 2048 29.3 / 33.3, 64 of 2048 77 / 66.
+        const long work = (long)B * Hkv * steps;
+        p.wq = G <= 32 || work <= 2 * KW_MAX_WG ? 1 : G <= 64 || work <= 32 * KW_MAX_WG ? 2 : 4;
         p.tile_rows = 32 * p.wq;
         p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
         p.n_wg = KW_MAX_WG;
     } else {
         p.tile_rows = KV_QT;
         p.out_cols = Dv;
-        // as many as the registers let run at once
+        // As many as the registers let run at once: with 256 more, 128
+        // sequences of 4096 positions (8 of 32 heads) take 210 -> 272 us at
+        // width 64, 382 -> 446 at 128; 65536 positions alone 95 -> 112 at 256;
+        // with 256 less 62 -> 69 us (width 64, one sequence of 65536).
         p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 256 ? 256 : (d <= 320 && Dv <= 256) ? 320 : 512;
-        p.n_wg = 256 * (bf16 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1));
+        p.n_wg = 256 * (d <= (bf16 ? 128 : 64) ? 2 : 1);
     }
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
     p.min_units = p.wide ? KV_ROW_UNITS : 4;
-    // Short rows: a workgroup each, and no join.
+    // Short rows: a workgroup each, and no join.  Of eight waves where the
+    // registers allow it, one a CU or fewer (us, four against eight, 8 cache
+    // heads of width 128: 8 sequences of 512 positions 13.4 / 11.1, 32 of 1024
+    // 33.1 / 30.0, 40 of 1024 41.9 / 45.7).  How long a row may be goes by the
+    // steps a wave takes one after the other, which many rows cover and few do
+    // not (whole against cut: 1 sequence of 512 positions 9.8 / 10.8, of 1024
+    // 14.1 / 11.7; 8 of 1024 16.0 / 15.7; 24 of 1024 25.0 / 31.5 with eight
+    // waves and 30.2 / 31.5 with four; 32 of 2048 53.6 / 61, but there lengths
+    // that differ would leave most CUs waiting).
     const long rows = (long)B * Hkv * p.q_tiles;
-    p.direct = !p.wide && steps <= KV_DIRECT_STEPS;
-    p.waves = p.direct && (bf16 ? d <= 128 : d <= 64) && steps > KV_WAVES ? 8 : KV_WAVES;
+    p.waves = d <= (bf16 ? 128 : 64) && rows <= 256 && steps > KV_WAVES ? 8 : KV_WAVES;
+    p.direct = !p.wide && steps <= 32 && steps <= p.waves * (rows < 64 ? 2 : rows < 192 ? 4 : 8);
     if (p.direct) p.n_wg = (int)rows;
+    else p.waves = KV_WAVES;
     return p;
 }
 

@@ -8,7 +8,6 @@
 namespace coli {
 
 constexpr int KVC_NT = 256;
-constexpr int KVC_MANY = 2048;           // rows from which a workgroup takes four
 
 // Pool row of position p of cache head h, -1 where the page id is none.
 __device__ __forceinline__ int pool_row(const int32_t *__restrict__ table_row, int p, int h, int Hkv, int page_shift,
@@ -20,61 +19,55 @@ __device__ __forceinline__ int pool_row(const int32_t *__restrict__ table_row, i
                  (uint32_t)(p & ((1 << page_shift) - 1)));
 }
 
-// TOK new tokens a workgroup (several where there are many: their reads are in
-// flight together).  The sequence of row r is the last b with start[b] <= r
-// (found by halving; start ascends), its position lens[b] - (start[b + 1] - r).
-template <int TOK>
+// One new token a workgroup, or several narrow ones (a.tokens), so that its threads have a chunk each: with
+// one, 16384 tokens of two 64-wide heads (32 chunks) took 15.8 us, with
+// eight 6.9.  (With one the place is looked up in scalar registers: 16384
+// tokens of eight 128-wide heads 30 us, 41 without.)  The sequence of row r is the last b with start[b] <= r (found by
+// halving; start ascends), its position lens[b] - (start[b + 1] - r).
+template <bool ONE>
 __global__ __launch_bounds__(KVC_NT) void kv_append_kernel(AppendLaunch a)
 {
-    const int32_t *table[TOK];                        // null: the row has no place
-    int pos[TOK];
-#pragma unroll
-    for (int x = 0; x < TOK; ++x) {
-        const int r = blockIdx.x * TOK + x;
-        int b = r, p = -1;
-        if (a.start) {
-            if (r < a.rows && r >= a.start[0] && r < a.start[a.B]) {
-                int lo = 0, hi = a.B;                 // start[lo] <= r < start[hi]
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.start[mid] <= r) lo = mid;
-                    else hi = mid;
-                }
-                b = lo;
-                p = min(max(a.lens[b], 0), a.cap) - a.start[b + 1] + r;
-            }
-        } else if (r < a.rows) {
-            p = min(max(a.lens[b], 0), a.cap) - 1;
+    const int per = a.k_chunks + a.v_chunks, width = a.Hkv * per;
+    const int x = ONE ? 0 : (int)threadIdx.x / width;
+    const int r = ONE ? blockIdx.x : blockIdx.x * a.tokens + x;
+    if (!ONE && (x >= a.tokens || r >= a.rows)) return;
+    int b = r, p;
+    if (a.start) {
+        if (r < a.start[0] || r >= a.start[a.B]) return;
+        int lo = 0, hi = a.B;                         // start[lo] <= r < start[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.start[mid] <= r) lo = mid;
+            else hi = mid;
         }
-        table[x] = p >= 0 && p < a.cap ? a.table + (size_t)b * a.max_pages : nullptr;
-        pos[x] = p;
+        b = lo;
+        p = min(max(a.lens[b], 0), a.cap) - a.start[b + 1] + r;
+    } else {
+        p = min(max(a.lens[b], 0), a.cap) - 1;
     }
-    const int per = a.k_chunks + a.v_chunks;
-    for (int i = threadIdx.x; i < a.Hkv * per; i += KVC_NT) {
+    if (p < 0 || p >= a.cap) return;
+    const int32_t *table = a.table + (size_t)b * a.max_pages;
+    const int first = pool_row(table, p, 0, a.Hkv, a.page_shift, a.n_pages);
+    if (first < 0) return;
+    const uint32_t page = 1u << a.page_shift;
+    const u32x4 *__restrict__ k_new = (const u32x4 *)a.k_new, *__restrict__ v_new = (const u32x4 *)a.v_new;
+    u32x4 *__restrict__ k = (u32x4 *)a.k, *__restrict__ v = (u32x4 *)a.v;
+    for (int i = threadIdx.x - x * width; i < width; i += KVC_NT) {
         const int h = i / per, c = i - h * per, cv = c - a.k_chunks;
-        u32x4 v[TOK];
-        int to[TOK];
-#pragma unroll
-        for (int x = 0; x < TOK; ++x) {
-            to[x] = table[x] ? pool_row(table[x], pos[x], h, a.Hkv, a.page_shift, a.n_pages) : -1;
-            if (to[x] < 0) continue;
-            const size_t from = (size_t)(blockIdx.x * TOK + x) * a.Hkv + h;
-            v[x] = cv < 0 ? ((const u32x4 *)a.k_new)[from * a.k_chunks + c] : ((const u32x4 *)a.v_new)[from * a.v_chunks + cv];
-        }
-#pragma unroll
-        for (int x = 0; x < TOK; ++x) {
-            if (to[x] < 0) continue;
-            if (cv < 0) ((u32x4 *)a.k)[(size_t)to[x] * a.k_chunks + c] = v[x];
-            else ((u32x4 *)a.v)[(size_t)to[x] * a.v_chunks + cv] = v[x];
-        }
+        const size_t from = (size_t)r * a.Hkv + h, to = (size_t)((uint32_t)first + (uint32_t)h * page);
+        if (cv < 0) k[to * a.k_chunks + c] = k_new[from * a.k_chunks + c];
+        else v[to * a.v_chunks + cv] = v_new[from * a.v_chunks + cv];
     }
 }
 
-hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st)
+hipError_t launch_kv_append(const AppendLaunch &in, hipStream_t st)
 {
-    if (a.rows == 0 || a.B == 0) return hipSuccess;
-    if (a.rows >= KVC_MANY) kv_append_kernel<4><<<(a.rows + 3) / 4, KVC_NT, 0, st>>>(a);
-    else kv_append_kernel<1><<<a.rows, KVC_NT, 0, st>>>(a);
+    if (in.rows == 0 || in.B == 0) return hipSuccess;
+    AppendLaunch a = in;
+    const int width = a.Hkv * (a.k_chunks + a.v_chunks);
+    a.tokens = width < KVC_NT ? KVC_NT / width : 1;
+    if (a.tokens == 1) kv_append_kernel<true><<<a.rows, KVC_NT, 0, st>>>(a);
+    else kv_append_kernel<false><<<(a.rows + a.tokens - 1) / a.tokens, KVC_NT, 0, st>>>(a);
     return hipGetLastError();
 }
 
