@@ -199,11 +199,12 @@ struct AttnWs {
     long s_ld;
 };
 
-AttnWs attn_ws(const coli_kv_shape *s, int32_t idx_k, bool acc)
+AttnWs attn_ws(const coli_kv_shape *s, int32_t idx_k, bool acc, bool latent)
 {
     AttnWs w{};
     const size_t heads = (size_t)s->B * s->Hq, cap = (size_t)s->max_pages * s->page;
-    w.plan = coli::attn_plan(s->B, s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16, idx_k ? idx_k : (int)cap);
+    w.plan = coli::attn_plan(s->B, s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16, latent,
+                             idx_k ? idx_k : (int)cap);
     w.s_ld = (long)((cap + 31) / 32 * 32);
     // a range leaves at most two parts: of the row it begins in and of the one it ends in
     const size_t part_rows = w.plan.direct ? 0 : (size_t)2 * w.plan.n_wg * w.plan.tile_rows;
@@ -660,10 +661,13 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
 
 size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32_t acc)
 {
-    // a shape that either kind of cache allows
-    if (check_kv_shape(s, false) != COLI_OK && check_kv_shape(s, true) != COLI_OK) return 0;
+    // enough for either kind of cache that the shape allows
+    const bool pair = check_kv_shape(s, false) == COLI_OK, latent = check_kv_shape(s, true) == COLI_OK;
+    if (!pair && !latent) return 0;
     if (idx_k < 0 || idx_k > (1 << 24) || (idx_k && acc) || kv_work(s, idx_k) > (1 << 28)) return 0;
-    return attn_ws(s, idx_k, acc != 0).total;
+    const size_t a = pair ? attn_ws(s, idx_k, acc != 0, false).total : 0;
+    const size_t b = latent ? attn_ws(s, idx_k, acc != 0, true).total : 0;
+    return a > b ? a : b;
 }
 
 coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
@@ -684,7 +688,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || !aligned16(idx) || !aligned16(acc_in) ||
         !aligned16(acc_out) || !aligned16(lse))
         return COLI_E_ALIGN;
-    const AttnWs L = attn_ws(s, idx_k, acc_out != nullptr);
+    const AttnWs L = attn_ws(s, idx_k, acc_out != nullptr, !c->v);
     if (ws_bytes < L.total) return COLI_E_WORKSPACE;
     const size_t elt = kv_elt(s), pool = kv_pool_rows(s), heads = (size_t)s->B * s->Hq;
     const size_t accb = acc_out ? (size_t)s->B * s->Hkv * ld * 4 : 0;

@@ -1198,17 +1198,17 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     }
 }
 
-// Joins the parts that attn_wide_kernel left: a workgroup takes KJ_COLS
+// Joins the parts that attn_wide_kernel left: a workgroup takes COLS
 // 32-column tiles of one query tile's output, a thread 4 columns of a query
-// in each, parts in the order of the positions.
-constexpr int KJ_COLS = 4;
-
-template <int DV, int WQ>
-__global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
+// in each.  NG groups of threads take every NG-th part and are summed in their
+// order.
+template <int DV, int WQ, int COLS, int NG>
+__global__ __launch_bounds__(KV_NT * NG) void attn_wide_join_kernel(AttnLaunch a)
 {
-    constexpr int SPLIT = DV / 32 / KJ_COLS;
-    __shared__ float factor[KW_MAX_WG][32], red[KV_NT / 32][32];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int SPLIT = DV / 32 / COLS, NF = KV_NT * NG / 32;
+    __shared__ float factor[KW_MAX_WG][32], red[NF][32];
+    __shared__ f32x4 others[NG > 1 ? NG - 1 : 1][NG > 1 ? COLS : 1][NG > 1 ? KV_NT : 1];
+    const int tid = threadIdx.x % KV_NT, ng = threadIdx.x / KV_NT, lane = tid & 63, wave = tid >> 6;
     const int ql = lane & 31, hi = lane >> 5;
     int at = blockIdx.x;
     const int part = at % SPLIT;
@@ -1225,22 +1225,22 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
     const size_t q = (size_t)b * a.Hq + h * G + q0 + ql;
     uint16_t *out = (uint16_t *)a.out + q * a.Dv;
     // wave i of the workgroup holds the i-th 8 columns of each tile: its lanes' are 8 i + 4 hi + 0..3
-    f32x4 sum[KJ_COLS];
+    f32x4 sum[COLS];
 #pragma unroll
-    for (int x = 0; x < KJ_COLS; ++x) sum[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < COLS; ++x) sum[x] = f32x4{0.f, 0.f, 0.f, 0.f};
     float mx = -INFINITY, l = 0.f;
     if (p.steps > 0) {
         if (p.w0 == p.w1) return;                           // one range holds all of it
         auto slot_of = [&](int w) { return (size_t)p.slot(w) * WQ + qt; };
-        // the parts' factors for the 32 queries: the workgroup's eight groups of 32 threads take every eighth part
-        const int grp = tid >> 5;
-        for (int w = p.w0 + grp; w <= p.w1; w += KV_NT / 32) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
+        // the parts' factors for the 32 queries: the workgroup's NF groups of 32 threads take every NF-th part
+        const int grp = threadIdx.x >> 5;
+        for (int w = p.w0 + grp; w <= p.w1; w += NF) mx = fmaxf(mx, a.part_ml[(slot_of(w) * 32 + ql) * 2]);
         red[grp][ql] = mx;
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < KV_NT / 32; ++x) mx = fmaxf(mx, red[x][ql]);
+        for (int x = 0; x < NF; ++x) mx = fmaxf(mx, red[x][ql]);
         const float ref = mx == -INFINITY ? 0.f : mx;
-        for (int w = p.w0 + grp; w <= p.w1; w += KV_NT / 32) {
+        for (int w = p.w0 + grp; w <= p.w1; w += NF) {
             const float f = __builtin_amdgcn_exp2f(a.part_ml[(slot_of(w) * 32 + ql) * 2] - ref);
             l += a.part_ml[(slot_of(w) * 32 + ql) * 2 + 1] * f;
             factor[w - p.w0][ql] = f;
@@ -1250,20 +1250,33 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
         __syncthreads();
         l = 0.f;
 #pragma unroll
-        for (int x = 0; x < KV_NT / 32; ++x) l += red[x][ql];
-#pragma unroll 4
-        for (int w = p.w0; w <= p.w1; ++w) {
+        for (int x = 0; x < NF; ++x) l += red[x][ql];
+#pragma unroll 16 / COLS
+        for (int w = p.w0 + ng; w <= p.w1; w += NG) {
             const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + slot_of(w) * (32 * DV)) + lane;
             const float f = factor[w - p.w0][ql];
 #pragma unroll
-            for (int x = 0; x < KJ_COLS; ++x) sum[x] += src[((part * KJ_COLS + x) * 4 + wave) * 64] * f;
+            for (int x = 0; x < COLS; ++x) sum[x] += src[((part * COLS + x) * 4 + wave) * 64] * f;
+        }
+        if constexpr (NG > 1) {
+            if (ng > 0) {
+#pragma unroll
+                for (int x = 0; x < COLS; ++x) others[ng - 1][x][tid] = sum[x];
+            }
+            __syncthreads();
+            if (ng == 0) {
+#pragma unroll
+                for (int y = 0; y < NG - 1; ++y)
+#pragma unroll
+                    for (int x = 0; x < COLS; ++x) sum[x] += others[y][x][tid];
+            }
         }
     }
-    if (ql >= nq) return;
+    if (ng > 0 || ql >= nq) return;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int x = 0; x < KJ_COLS; ++x) {
-        const int d = 32 * (part * KJ_COLS + x) + 8 * wave + 4 * hi;
+    for (int x = 0; x < COLS; ++x) {
+        const int d = 32 * (part * COLS + x) + 8 * wave + 4 * hi;
         if (d < a.Dv)
             *reinterpret_cast<u32x2 *>(out + d) = u32x2{pack_bf16(sum[x][0] * inv, sum[x][1] * inv),
                                                         pack_bf16(sum[x][2] * inv, sum[x][3] * inv)};
@@ -1273,14 +1286,19 @@ __global__ __launch_bounds__(KV_NT) void attn_wide_join_kernel(AttnLaunch a)
 
 // How a call runs.  entries: the longest row (the cache's capacity, or the
 // listed positions).
-AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entries)
+AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int entries)
 {
     AttnPlan p{};
     const int G = Hq / Hkv, d = Dk > Dv ? Dk : Dv;
     const int steps = (entries + KV_STEP - 1) / KV_STEP;
-    // Rows past 256 elements are latent caches (host check); in bf16 they take
-    // the LDS kernel.
-    p.wide = bf16 && Dk > 256;
+    // bf16 rows past 256 elements (latent caches by the host's check) take the
+    // LDS kernel, and latent rows past 128 where several query tiles would
+    // read much of them each (256 elements, us there / in the LDS kernel: 32
+    // sequences of 4096 positions with 16 heads 33.6 / 34.5, 32 heads 47 / 35,
+    // 128 heads 134 / 54; of 1024 with 32 heads 23.7 / 20.7; 8 of 512 with 32
+    // heads 16.4 / 17.9, with 128 22.2 / 19.4).
+    const long work = (long)B * Hkv * steps;
+    p.wide = bf16 && (Dk > 256 || (latent && Dk > 128 && G > KV_QT && work * ((G + KV_QT - 1) / KV_QT) >= 8 * KW_MAX_WG));
     if (p.wide) {
         // Fewer tiles a workgroup: more workgroups for small work, which then
         // read the cache (out of the caches) more often.  128 heads, us with
@@ -1288,7 +1306,6 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entrie
         // 32.6 / 35.2 / 44.2, 32 of 1024 51.5 / 46.1 / 51.9, 64 of 2048
         // 113 / 86 / 93, 64 of 8192 358 / 252 / 241; 64 heads, 1 / 2: one row
         // of 512 23.8 / 28.7, 8 of 2048 29.3 / 33.3, 64 of 2048 77 / 66.
-        const long work = (long)B * Hkv * steps;
         p.wq = G <= 32 || work <= 2 * KW_MAX_WG ? 1 : G <= 64 || work <= 32 * KW_MAX_WG ? 2 : 4;
         p.tile_rows = 32 * p.wq;
         p.out_cols = (Dk <= 320 && Dv <= 256) ? 256 : 512;
@@ -1350,7 +1367,12 @@ template <int DK, int DV, int WQ>
 static void launch_wide(const AttnLaunch &a, hipStream_t st)
 {
     attn_wide_kernel<DK, DV, WQ><<<a.n_wg, KV_NT, 0, st>>>(a);
-    attn_wide_join_kernel<DV, WQ><<<a.B * a.Hkv * a.q_tiles * WQ * (DV / 32 / KJ_COLS), KV_NT, 0, st>>>(a);
+    // Of few rows the parts are many and the tiles few: more threads for each
+    // (64 heads, whole calls, us with 256 / 1024 threads: one row of 32768
+    // positions 60 / 44, 4 of 32768 69 / 65, 16 of 2048 38 / 42).
+    const int tiles = a.B * a.Hkv * a.q_tiles * WQ * (DV / 32);
+    if (tiles <= KW_MAX_WG) attn_wide_join_kernel<DV, WQ, 1, 4><<<tiles, 4 * KV_NT, 0, st>>>(a);
+    else attn_wide_join_kernel<DV, WQ, 4, 1><<<tiles / 4, KV_NT, 0, st>>>(a);
 }
 
 template <int DK, int DV>

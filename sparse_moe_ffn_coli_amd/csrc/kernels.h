@@ -87,7 +87,7 @@ struct AttnLaunch {
 
 // Which kernel an attention call takes and how its workspace is laid out.
 struct AttnPlan {
-    bool wide;             // bf16 rows past 256 elements: the LDS kernel
+    bool wide;             // the LDS kernel
     int wq;                // its query tiles per workgroup
     int tile_rows, q_tiles;     // query heads a workgroup takes at a time, and how often per cache head
     int out_cols;          // columns of a part's rows
@@ -122,7 +122,7 @@ struct EvictLaunch {
 hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st);
 hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
-AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, int entries);
+AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int entries);
 
 hipError_t launch_route(const RouteLaunch &a, hipStream_t st);
 // rows_per_len consecutive rows share an entry of lens; k may pass the 4096 of

@@ -647,3 +647,31 @@ def test_empty_arguments_do_not_count_as_absent():
     with pytest.raises(ValueError):
         coli_kv_evict(s, dev, torch.zeros((1, 2, 48), device="cuda"), 8, torch.zeros((1, 1), **i32), torch.zeros(1, **i32),
                       torch.zeros((1, 2, 8), **i32), new_acc=torch.empty((1, 2, 0), device="cuda"))
+
+
+@pytest.mark.parametrize("Hq,Dk,Dv,page", [(100, 576, 512, 64), (128, 320, 256, 32), (70, 264, 8, 64), (40, 256, 256, 64),
+                                           (64, 136, 72, 32), (34, 200, 128, 16), (20, 192, 192, 1)])
+def test_attn_latent_long_tables(Hq, Dk, Dv, page):
+    # room for many more positions than there are: calls are laid out by the room
+    c = ref.make_cache(BORDERS + [1100, 0, 2500], 1, Dk, Dv, page, "bf16", True, seed=Hq + Dk, extra_cols=(1 << 15) // page)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk))
+    acc = np.random.default_rng(2).random((16, 1, c["max_pages"] * page // 4 * 4 + 4)).astype(np.float32)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), acc_in=acc)
+    idx = np.random.default_rng(3).integers(-1, 1200, size=(16, 2100)).astype(np.int32)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), idx=idx)
+
+
+@pytest.mark.parametrize("Hq,Dk,Dv", [(100, 576, 512), (128, 320, 256), (33, 256, 256)])
+def test_attn_latent_scores_far_apart_in_long_tables(Hq, Dk, Dv):
+    c = ref.make_cache([1500, 1, 70, 0], 1, Dk, Dv, 16, "bf16", True, seed=64, extra_cols=1 << 13)
+    for b, n in enumerate(c["lens"].tolist()):
+        for p in range(n):
+            c["k"][c["table"][b, p // 16], :, p % 16] *= 0.05 + 1.5 * p / 1500
+    run_attn(c, Hq, 3.0)
+
+
+@pytest.mark.parametrize("Hq", [16, 100])
+def test_attn_latent_one_row_in_many_parts(Hq):
+    # a row that every workgroup has a part of, alone and beside an empty one
+    for lens in ([70000], [0, 66000, 3]):
+        run_attn(ref.make_cache(lens, 1, 320, 256, 64, "bf16", True, seed=65), Hq, 0.1)
