@@ -71,22 +71,22 @@ hipError_t launch_kv_append(const AppendLaunch &in, hipStream_t st)
     return hipGetLastError();
 }
 
-// The kept rows of one (sequence, cache head), EV_ROWS a workgroup: their old
+// The kept rows of one (sequence, cache head), `each` a workgroup: their old
 // and new pool rows go through LDS once, then the chunks of all of them are
 // copied side by side.  The same workgroups write the kept weights, the zeros
 // behind them and the new length.
-constexpr int EV_ROWS = 64;
+constexpr int EV_ROWS = 64;              // most rows of a workgroup
 
-__global__ __launch_bounds__(KVC_NT) void kv_evict_copy_kernel(EvictLaunch a, int blocks)
+__global__ __launch_bounds__(KVC_NT) void kv_evict_copy_kernel(EvictLaunch a, int blocks, int each)
 {
     __shared__ int32_t from[EV_ROWS], to[EV_ROWS];
     const int tid = threadIdx.x;
     const int bh = blockIdx.x / blocks, blk = blockIdx.x % blocks;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     const int n = min(max(a.lens[b], 0), a.cap), m = min(n, a.keep);
-    const int j0 = blk * EV_ROWS;
+    const int j0 = blk * each;
     if (blk == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
-    if (tid < EV_ROWS && j0 + tid < max((long)m, a.new_acc ? a.new_ld : 0)) {
+    if (tid < each && j0 + tid < max((long)m, a.new_acc ? a.new_ld : 0)) {
         const int j = j0 + tid;
         float w = 0.f;
         if (j < m) {
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(KVC_NT) void kv_evict_copy_kernel(EvictLaunch a, in
     }
     __syncthreads();
     // (eight chunks of a thread read before the first is written: 63 against 61 us for 268 MB)
-    const int rows = min(EV_ROWS, m - j0);
+    const int rows = min(each, m - j0);
     u32x4 *k = (u32x4 *)a.k, *v = (u32x4 *)a.v;
     for (int i = tid; i < rows * a.k_chunks; i += KVC_NT) {
         const int r = i / a.k_chunks, c = i - r * a.k_chunks;
@@ -118,8 +118,12 @@ hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st)
         launch_index_topk(a.acc, a.B * a.Hkv, a.cap, a.ld, a.lens, a.Hkv, a.keep, a.tail, a.kept, st);
     if (e != hipSuccess) return e;
     const long span = a.new_acc && a.new_ld > a.keep ? a.new_ld : a.keep;
-    const int blocks = (int)((span + EV_ROWS - 1) / EV_ROWS);
-    kv_evict_copy_kernel<<<a.B * a.Hkv * blocks, KVC_NT, 0, st>>>(a, blocks);
+    // Few rows go over more workgroups (us with 16 / 64 rows each, selection
+    // included: 2048 rows of 32 chunks in all 10.3 / 12.0, 4001 of 72 chunks
+    // 24.1 / 29.9, 65536 of 32 chunks 26.5 / 25.1, 262144 of them 64.6 / 55.3).
+    const int each = (long)a.B * a.Hkv * span < (1 << 15) ? 16 : EV_ROWS;
+    const int blocks = (int)((span + each - 1) / each);
+    kv_evict_copy_kernel<<<a.B * a.Hkv * blocks, KVC_NT, 0, st>>>(a, blocks, each);
     return hipGetLastError();
 }
 
