@@ -800,7 +800,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     constexpr int KS = DK / 16, DT = DV / 32;
     static_assert(KS % 4 == 0, "fragments in fours");
     constexpr int OUT = 32 * DV;              // floats of a query tile's output
-    static_assert(2 * OUT * 4 <= KW_RING * STAGE, "two outputs fit the ring");
+    static_assert(KV_WAVES * OUT * 2 <= KW_RING * STAGE, "half of each wave's output fits the ring");
     __shared__ __attribute__((aligned(256))) char ring[KW_RING * STAGE];
     __shared__ uint64_t rows_s[KW_BLOCK * KW_ROWS];         // addresses of the stages' rows
     __shared__ float red_m[KV_WAVES][32], red_l[KV_WAVES][32];
@@ -871,10 +871,14 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         // Columns past the row's width repeat its last chunk: zeros of the query and output columns that are not
         // written meet them.
         const uint32_t last = (chunks - 1) * 16;
-        auto copy_first = [&](uint64_t rows, int i, uint32_t dst) {
+        auto first_off = [&](int i) {                       // the lane's place in its row
             uint32_t lane_at = (lane & (RA - 1)) << 4;
             if constexpr (RPC == 2) lane_at ^= (lane >> 5) << 6;
-            const uint32_t off = min(lane_at ^ (kw_swz(i * RPC) << 4), last);
+            return lane_at ^ (kw_swz(i * RPC) << 4);
+        };
+        auto tail_off = [&](int i) { return (uint32_t)(RA + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))) << 4; };
+        auto copy_first = [&](uint64_t rows, int i, uint32_t dst) {
+            const uint32_t off = min(first_off(i), last);
             const uint64_t src = kw_lane(rows, i * RPC);
             if constexpr (RPC == 1) {
                 kw_copy(src, off, dst + i * 1024);
@@ -884,7 +888,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             }
         };
         auto copy_tail = [&](uint64_t rows, int i, uint32_t dst) {
-            const uint32_t off = min((uint32_t)(RA + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))) << 4, last);
+            const uint32_t off = min(tail_off(i), last);
             kw_copy((uint64_t)__shfl((unsigned long long)rows, 8 * i + (lane >> 3)) + off, dst + FIRST + i * 1024);
         };
         // copy number i of the wave's share of stage t
@@ -899,7 +903,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         auto hidden = [&](uint64_t rows) { return (uint32_t)__ballot(rows == (uint64_t)kw_zeros); };
         auto issue = [&](int t) {
             const uint64_t rows = stage_rows(t);
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < CPW; ++i) copy(t, rows, i);
             return hidden(rows);
         };
@@ -916,25 +920,25 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             return *reinterpret_cast<const bf16x8 *>(st + at);
         };
 
-        // the queries come in like a stage, each tile by its waves, and stay in registers as the score operand
+        // The queries come in like a stage, each tile by its waves, zeros past their width, and stay in registers as the
+        // score operand.
         bf16x8 qf[KS];
         {
             const uint64_t rows = ql < nq ? (uint64_t)a.q + (qrow + ql) * row_bytes : (uint64_t)kw_zeros;
-#pragma unroll
-            for (int i = 0; i < CA / WK; ++i) copy_first(rows, i * WK + kb, ring_at + qt * STAGE);
-#pragma unroll
-            for (int i = 0; i < CB / WK; ++i) copy_tail(rows, i * WK + kb, ring_at + qt * STAGE);
+            const uint32_t dst = ring_at + qt * STAGE;
+            auto bring = [&](int r, uint32_t off, uint32_t to) {
+                const uint64_t src = (uint64_t)__shfl((unsigned long long)rows, r);
+                kw_copy((off <= last ? src : (uint64_t)kw_zeros) + off, to);
+            };
+#pragma unroll 1
+            for (int i = kb; i < CA; i += WK) bring(i * RPC + (RPC == 1 ? 0 : lane >> 5), first_off(i), dst + i * 1024);
+#pragma unroll 1
+            for (int i = kb; i < CB; i += WK) bring(8 * i + (lane >> 3), tail_off(i), dst + FIRST + i * 1024);
             look_up(0);
             kw_wait_copies<0>();
             kw_barrier();
 #pragma unroll
-            for (int c = 0; c < KS; ++c) {                  // zeros past the width
-                u32x4 v = __builtin_bit_cast(u32x4, frag_at(ring + qt * STAGE, c / 4, c % 4));
-                const uint32_t keep = 16 * frag(c / 4, c % 4) + 8 * hi < a.Dk ? ~0u : 0u;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] &= keep;
-                qf[c] = as_bf16(v);
-            }
+            for (int c = 0; c < KS; ++c) qf[c] = frag_at(ring + qt * STAGE, c / 4, c % 4);
             kw_barrier();
         }
 
@@ -948,16 +952,18 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             top = -INFINITY;
 #pragma unroll
             for (int t = 0; t < DT; ++t) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+                // zero by a product: one instruction for sixteen registers (256 writes were 2 KB of code)
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16x8{}, bf16x8{}, f32x16{}, 0, 0, 0);
                 asm volatile("" : "+a"(o[t]));    // at home in the accumulation registers
             }
             uint32_t hids[AHEAD + 1];                       // hidden rows of the wave's stages in flight, next one first
             if constexpr (AHEAD > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < AHEAD * WK; ++t) {
                     const uint32_t mask = issue(t);
-                    if (t % WK == kb) hids[t / WK] = mask;
+#pragma unroll
+                    for (int y = 0; y < AHEAD; ++y)
+                        if (t == y * WK + kb) hids[y] = mask;
                 }
             }
             for (int r = 0; r < rounds; ++r) {
@@ -1106,7 +1112,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             red_l[wave][ql] = l;
         }
         kw_barrier();
-        float ma = m, la = l;
+        float ma = m, la = l, f[WK];
         if constexpr (WK > 1) {
             ma = red_m[qt][ql];
 #pragma unroll
@@ -1115,83 +1121,77 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
                 const float mw = red_m[w * WQ + qt][ql];
-                la += mw == -INFINITY ? 0.f : red_l[w * WQ + qt][ql] * __builtin_amdgcn_exp2f(mw - ma);
+                f[w] = mw == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw - ma);
+                la += red_l[w * WQ + qt][ql] * f[w];
             }
         }
-        // Each wave ends with a share of the tile's columns summed over the waves: with each partner it gives away the
-        // half of its columns that the other one keeps.
-        auto tiles = [&](auto first, auto count) {          // what the wave holds at the end goes out
-            constexpr int X0 = decltype(first)::value, N = decltype(count)::value;
-            if (nq <= 0) return;
-            if (s0 == 0 && s1 == steps) {
-                if (ql < nq) {
-                    const float inv = la > 0.f ? 1.f / la : 0.f;
-                    uint16_t *dst = (uint16_t *)a.out + (qrow + ql) * a.Dv;
-#pragma unroll
-                    for (int x = X0; x < X0 + N; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int d = 32 * x + 8 * i + 4 * hi;
-                            if (d < a.Dv)                   // Dv is a multiple of 8: all four columns or none
-                                *reinterpret_cast<u32x2 *>(dst + d) =
-                                    u32x2{pack_bf16(o[x][4 * i] * inv, o[x][4 * i + 1] * inv),
-                                          pack_bf16(o[x][4 * i + 2] * inv, o[x][4 * i + 3] * inv)};
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    if (X0 == 0 && hi == 0) kv_write_stats(a, qrow + ql, ma, la);
-                }
-            } else {
-                // a part: lanes side by side (attn_wide_join_kernel reads it the same way)
-                const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
-                f32x4 *dst = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
-#pragma unroll
-                for (int x = X0; x < X0 + N; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[(x * 4 + i) * 64] = f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
-                if (X0 == 0 && hi == 0) {
-                    a.part_ml[(slot * 32 + ql) * 2] = ma;
-                    a.part_ml[(slot * 32 + ql) * 2 + 1] = la;
-                }
+        // columns 32 x + 8 i + 4 hi .. + 3 of query ql go out
+        const bool whole = s0 == 0 && s1 == steps;
+        const float inv = la > 0.f ? 1.f / la : 0.f;
+        const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
+        f32x4 *part = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
+        uint16_t *out = (uint16_t *)a.out + (qrow + ql) * a.Dv;
+        auto put = [&](int x, int i, f32x4 v) {
+            if (!whole) {                     // a part: lanes side by side (attn_wide_join_kernel reads it the same way)
+                part[(x * 4 + i) * 64] = v;
+            } else if (ql < nq && 32 * x + 8 * i + 4 * hi < a.Dv) {  // Dv is a multiple of 8: all four columns or none
+                *reinterpret_cast<u32x2 *>(out + 32 * x + 8 * i + 4 * hi) =
+                    u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
             }
         };
-        auto give_and_take = [&](auto keep, auto give, auto count, int partner) {
-            constexpr int K0 = decltype(keep)::value, G0 = decltype(give)::value, N = decltype(count)::value;
-            f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
-#pragma unroll
-            for (int x = 0; x < N; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    buf[wave * (OUT / 8) + (x * 4 + i) * 64 + lane] =
-                        f32x4{o[G0 + x][4 * i], o[G0 + x][4 * i + 1], o[G0 + x][4 * i + 2], o[G0 + x][4 * i + 3]};
-            kw_barrier();
-#pragma unroll
-            for (int x = 0; x < N; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 v = buf[partner * (OUT / 8) + (x * 4 + i) * 64 + lane];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[K0 + x][4 * i + e] += v[e];
-                }
-            kw_barrier();
-        };
         if constexpr (WK == 1) {
-            tiles(KwInt<0>{}, KwInt<DT>{});
-        } else {
-            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - ma);
+            if (nq > 0) {
 #pragma unroll
-            for (int x = 0; x < DT; ++x) o[x] *= f;
-            constexpr int H = DT / 2, Q = DT / 4;
-            if (kb & 1) give_and_take(KwInt<H>{}, KwInt<0>{}, KwInt<H>{}, wave ^ WQ);
-            else give_and_take(KwInt<0>{}, KwInt<H>{}, KwInt<H>{}, wave ^ WQ);
-            if constexpr (WK == 2) {
-                if (kb) tiles(KwInt<H>{}, KwInt<H>{});
-                else tiles(KwInt<0>{}, KwInt<H>{});
-            } else {
-                if (kb == 0) give_and_take(KwInt<0>{}, KwInt<Q>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<0>{}, KwInt<Q>{});
-                else if (kb == 1) give_and_take(KwInt<H>{}, KwInt<H + Q>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<H>{}, KwInt<Q>{});
-                else if (kb == 2) give_and_take(KwInt<Q>{}, KwInt<0>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<Q>{}, KwInt<Q>{});
-                else give_and_take(KwInt<H + Q>{}, KwInt<H>{}, KwInt<Q>{}, wave ^ 2), tiles(KwInt<H + Q>{}, KwInt<Q>{});
+                for (int x = 0; x < DT; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        put(x, i, f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]});
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+        } else {
+            // Half of the tile's columns at a time, all waves' side by side in LDS; each wave sums its share of them.
+            // (Exchanges of halves between pairs of waves move less, but are five times the code.)
+            f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
+            constexpr int H = DT / 2;
+            auto give = [&](auto half) {
+#pragma unroll
+                for (int x = 0; x < H; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x16 &t = o[decltype(half)::value * H + x];
+                        buf[((wave * H + x) * 4 + i) * 64 + lane] =
+                            f32x4{t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]};
+                    }
+            };
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {
+                if (p == 0) {
+                    give(KwInt<0>{});
+                } else {
+                    kw_barrier();
+                    give(KwInt<1>{});
+                }
+                kw_barrier();
+                if (nq > 0) {
+#pragma unroll 1
+                    for (int y = kb; y < H; y += WK)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f32x4 v = buf[((qt * H + y) * 4 + i) * 64 + lane] * f[0];
+#pragma unroll
+                            for (int w = 1; w < WK; ++w) v += buf[(((w * WQ + qt) * H + y) * 4 + i) * 64 + lane] * f[w];
+                            put(p * H + y, i, v);
+                        }
+                }
+            }
+        }
+        if (nq > 0 && kb == 0 && hi == 0) {
+            if (!whole) {
+                a.part_ml[(slot * 32 + ql) * 2] = ma;
+                a.part_ml[(slot * 32 + ql) * 2 + 1] = la;
+            } else if (ql < nq) {
+                kv_write_stats(a, qrow + ql, ma, la);
             }
         }
         kw_barrier();                                       // red_m, red_l and the ring are free again
