@@ -1175,14 +1175,17 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 kw_barrier();
                 if (nq > 0) {
 #pragma unroll 1
-                    for (int y = kb; y < H; y += WK)
+                    for (int y = kb; y < H; y += WK) {
+                        f32x4 v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            f32x4 v = buf[((qt * H + y) * 4 + i) * 64 + lane] * f[0];
+                            v[i] = buf[((qt * H + y) * 4 + i) * 64 + lane] * f[0];
 #pragma unroll
-                            for (int w = 1; w < WK; ++w) v += buf[(((w * WQ + qt) * H + y) * 4 + i) * 64 + lane] * f[w];
-                            put(p * H + y, i, v);
+                            for (int w = 1; w < WK; ++w) v[i] += buf[(((w * WQ + qt) * H + y) * 4 + i) * 64 + lane] * f[w];
                         }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(p * H + y, i, v[i]);
+                    }
                 }
             }
         }
