@@ -623,49 +623,58 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
     const int p0 = (at - bh * chunks) * KV_NT * 4;
     if (p0 >= n) return;
     int before = 0, total = 0;
-    if (!joined && !a.direct) kv_prefix(a, b, &before, &total);
+    // the lanes that share a head's parts, as many as there may be (one sequence of 43069 positions, 7 heads: 32 us
+    // with one lane a head, 10 with 32)
+    int share = 1;
+    if (!joined && !a.direct) {
+        kv_prefix(a, b, &before, &total);
+        const int most = kv_units(n) / kv_range(a, total * a.Hkv * a.q_tiles) + 2;
+        while (share < most && 2 * share <= 64 && 2 * share * G <= KV_NT) share *= 2;
+    }
     const int p = p0 + tid * 4;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < G; i0 += KV_NT) {
-        if (i0 + tid < G) {
-            const int i = i0 + tid;
-            const size_t q = (size_t)b * a.Hq + h * G + i;
-            float m, inv;
-            KvParts parts{};
-            if (!joined && !a.direct) parts = kv_parts(a, b, h * a.q_tiles + i / KV_QT, before, total);
-            if (parts.w0 == parts.w1) {
-                m = a.stats[2 * q];
-                inv = a.stats[2 * q + 1];
-            } else {
-                // one pass, eight parts' loads in flight
-                m = 0.f;
-                float mx = -INFINITY, l = 0.f;
-                for (int w = parts.w0; w <= parts.w1; w += 8) {
-                    float mw[8], lw[8];
+    const int heads = KV_NT / share, sub = tid & (share - 1);
+    for (int i0 = 0; i0 < G; i0 += heads) {
+        const int i = i0 + tid / share;
+        const size_t q = (size_t)b * a.Hq + h * G + i;
+        KvParts parts{};
+        if (i < G && !joined && !a.direct) parts = kv_parts(a, b, h * a.q_tiles + i / KV_QT, before, total);
+        const bool cut = parts.w0 != parts.w1;
+        float mx = -INFINITY, l = 0.f;
+        if (cut) {                            // four parts' loads in flight
+            for (int w = parts.w0 + sub; w <= parts.w1; w += 4 * share) {
+                float mw[4], lw[4];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float *ml = a.part_ml + ((size_t)parts.slot(min(w + x, parts.w1)) * KV_QT + i % KV_QT) * 2;
-                        mw[x] = w + x <= parts.w1 ? ml[0] : -INFINITY;
-                        lw[x] = ml[1];
-                    }
-                    float mn = mx;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) mn = fmaxf(mn, mw[x]);
-                    m = mn == -INFINITY ? 0.f : mn;
-                    l *= __builtin_amdgcn_exp2f(mx - m);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) l += mw[x] == -INFINITY ? 0.f : lw[x] * __builtin_amdgcn_exp2f(mw[x] - m);
-                    mx = mn;
+                for (int x = 0; x < 4; ++x) {
+                    const int at_w = w + x * share;
+                    const float *ml = a.part_ml + ((size_t)parts.slot(min(at_w, parts.w1)) * KV_QT + i % KV_QT) * 2;
+                    mw[x] = at_w <= parts.w1 ? ml[0] : -INFINITY;
+                    lw[x] = ml[1];
                 }
-                inv = l > 0.f ? 1.f / l : 0.f;
+                float mn = mx;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mn = fmaxf(mn, mw[x]);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                l *= __builtin_amdgcn_exp2f(mx - ref);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) l += mw[x] == -INFINITY ? 0.f : lw[x] * __builtin_amdgcn_exp2f(mw[x] - ref);
+                mx = mn;
             }
-            stat[tid][0] = m;
-            stat[tid][1] = inv;
+        }
+        for (int off = 1; off < share; off <<= 1) {
+            const float mo = __shfl_xor(mx, off), lo = __shfl_xor(l, off);
+            const float mn = fmaxf(mx, mo), ref = mn == -INFINITY ? 0.f : mn;
+            l = l * __builtin_amdgcn_exp2f(mx - ref) + lo * __builtin_amdgcn_exp2f(mo - ref);
+            mx = mn;
+        }
+        if (i < G && sub == 0) {
+            stat[tid / share][0] = cut ? (mx == -INFINITY ? 0.f : mx) : a.stats[2 * q];
+            stat[tid / share][1] = cut ? (l > 0.f ? 1.f / l : 0.f) : a.stats[2 * q + 1];
         }
         __syncthreads();
         if (p < n) {
 #pragma unroll 8
-            for (int i = i0; i < min(G, i0 + KV_NT); ++i) {
+            for (int i = i0; i < min(G, i0 + heads); ++i) {
                 const f32x4 t =
                     *reinterpret_cast<const f32x4 *>(a.scores + ((size_t)b * a.Hq + h * G + i) * a.s_ld + p);
                 const float m = stat[i - i0][0], inv = stat[i - i0][1];
