@@ -1334,18 +1334,33 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool laten
     }
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
     p.min_units = p.wide ? KV_ROW_UNITS : 4;
-    // Short rows: a workgroup each, and no join.  Of eight waves where the
-    // registers allow it, one a CU or fewer (us, four against eight, 8 cache
-    // heads of width 128: 8 sequences of 512 positions 13.4 / 11.1, 32 of 1024
-    // 33.1 / 30.0, 40 of 1024 41.9 / 45.7).  How long a row may be goes by the
-    // steps a wave takes one after the other, which many rows cover and few do
-    // not (whole against cut: 1 sequence of 512 positions 9.8 / 10.8, of 1024
-    // 14.1 / 11.7; 8 of 1024 16.0 / 15.7; 24 of 1024 25.0 / 31.5 with eight
-    // waves and 30.2 / 31.5 with four; 32 of 2048 53.6 / 61, but there lengths
-    // that differ would leave most CUs waiting).
+    // Short rows: a workgroup each, and no join.  A workgroup's waves: those
+    // that give the fewest rounds of resident workgroups times a row's steps
+    // one after the other, 2.5 more for its start and end (us, measured with
+    // 1 / 2 / 4 waves: bf16 width 128, 1024 rows of 20 positions 7.8 / 8.0 /
+    // 12.4, of 250 33 / 31 / 34, 1152 of 250 36 / 41 / 39; fp32 width 192, 512
+    // rows of 128 positions 65 / 47 / 57, 1024 of 250 142 / 155 / 174; with
+    // 4 / 8 bf16 width 128, 256 rows of 1024 33.1 / 30.0, 320 of them 41.9 /
+    // 45.7).  Fewer waves have to be a fifth cheaper: they leave a long row
+    // among short ones to itself (760 rows of up to 575 positions, width 192:
+    // 47 us with four, 57 with one).
     const long rows = (long)B * Hkv * p.q_tiles;
-    p.waves = d <= (bf16 ? 128 : 64) && rows <= 256 && steps > KV_WAVES ? 8 : KV_WAVES;
-    p.direct = !p.wide && steps <= 32 && steps <= p.waves * (rows < 64 ? 2 : rows < 192 ? 4 : 8);
+    const bool light = d <= (bf16 ? 128 : 64);              // two waves a SIMD
+    p.waves = KV_WAVES;
+    if (!p.wide && d <= 256) {
+        float best = INFINITY;
+        for (int nw = light ? 8 : 4; nw >= 1; nw /= 2) {
+            const long rounds = (rows * nw + 255) / 256;    // of all CUs' waves: 8 or 4 each
+            const float cost = (float)((rounds + (light ? 7 : 3)) / (light ? 8 : 4)) * (2.5f + (float)((steps + nw - 1) / nw));
+            if (cost < 0.8f * best) best = cost, p.waves = nw;
+        }
+    }
+    // How long a row may be goes by the steps a wave takes, which many rows
+    // cover and few do not (whole against cut, 8 cache heads of width 128: 1
+    // sequence of 512 positions 9.8 / 10.8, of 1024 14.1 / 11.7; 8 of 1024
+    // 16.0 / 15.7; 24 of 1024 25.0 / 31.5; 32 of 2048 53.6 / 61, but there
+    // lengths that differ would leave most CUs waiting).
+    p.direct = !p.wide && steps <= 32 && (rows >= 192 || steps <= p.waves * (rows < 64 ? 2 : 4));
     if (p.direct) p.n_wg = (int)rows;
     else p.waves = KV_WAVES;
     return p;
@@ -1354,11 +1369,12 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool laten
 template <bool BF16, int DK, int DV>
 static void launch_tier(const AttnLaunch &a, int waves, hipStream_t st)
 {
-    if constexpr (DV <= (BF16 ? 128 : 64)) {
-        if (waves == 8) {
-            attn_kernel<BF16, DK, DV, 8><<<a.n_wg, 512, 0, st>>>(a);
-            return;
-        }
+    if constexpr (DK <= 256) {
+        if (waves == 1) return attn_kernel<BF16, DK, DV, 1><<<a.n_wg, 64, 0, st>>>(a);
+        if (waves == 2) return attn_kernel<BF16, DK, DV, 2><<<a.n_wg, 128, 0, st>>>(a);
+    }
+    if constexpr (DK <= (BF16 ? 128 : 64)) {
+        if (waves == 8) return attn_kernel<BF16, DK, DV, 8><<<a.n_wg, 512, 0, st>>>(a);
     }
     attn_kernel<BF16, DK, DV, KV_WAVES><<<a.n_wg, KV_NT, 0, st>>>(a);
 }

@@ -675,3 +675,17 @@ def test_attn_latent_one_row_in_many_parts(Hq):
     # a row that every workgroup has a part of, alone and beside an empty one
     for lens in ([70000], [0, 66000, 3]):
         run_attn(ref.make_cache(lens, 1, 320, 256, 64, "bf16", True, seed=65), Hq, 0.1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hkv,D", [(8, 64), (5, 128), (3, 256)])
+@pytest.mark.parametrize("B,longest", [(3, 40), (40, 60), (130, 130), (260, 30), (400, 250)])
+def test_attn_short_rows_of_any_number(dtype, Hkv, D, B, longest):
+    # rows that a workgroup takes whole, with one wave or several
+    lens = np.random.default_rng(B).integers(0, longest + 1, size=B)
+    lens[0], lens[-1] = longest, 0
+    c = ref.make_cache(lens, Hkv, D, D, 16, dtype, seed=B + D, extra_cols=0)
+    run_attn(c, 2 * Hkv, 1.0 / np.sqrt(D))
+    if B == 40:
+        acc = np.random.default_rng(2).random((B, Hkv, c["max_pages"] * 16)).astype(np.float32)
+        run_attn(c, 2 * Hkv, 1.0 / np.sqrt(D), acc_in=acc)
