@@ -447,8 +447,8 @@ class KvShape:
 class KvCache:
     """The pools, the page table and the lengths (device tensors), see
     coli_kv_cache.  v None: a latent cache.  A handle that a program makes once
-    and uses in every step: its tensors are written in place (lens and table
-    change from step to step), not resized."""
+    and uses in every step; its tensors are written in place (lens and table
+    change from step to step)."""
     k: object
     v: object
     table: object
@@ -476,9 +476,10 @@ def _kv_check(where: str, device, *args) -> None:
 
 def _kv_handles(where: str, shape: KvShape, cache: KvCache):
     """The C forms of a shape and a cache and what calls on them share: (shape, cache, dtype, device).  Checked and
-    formed once for a pair of handles, and kept in the cache's."""
+    formed once for a pair of handles, and kept in the cache's until a tensor's memory is another one."""
     kept = cache.__dict__.get("_handles")
-    if kept is not None and kept[0] is shape:
+    at = (cache.k.data_ptr(), 0 if cache.v is None else cache.v.data_ptr(), cache.table.data_ptr(), cache.lens.data_ptr())
+    if kept is not None and kept[0] is shape and kept[2] == at:
         return kept[1]
     import torch
     dt, i32, dev = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32, cache.k.device
@@ -488,7 +489,7 @@ def _kv_handles(where: str, shape: KvShape, cache: KvCache):
     if dev.type != "cuda":
         raise ValueError(f"{where}: the cache must be on a GPU, not on {dev}")
     got = (C.byref(shape.c()), C.byref(cache.c()), dt, dev)
-    object.__setattr__(cache, "_handles", (shape, got))
+    object.__setattr__(cache, "_handles", (shape, got, at))
     return got
 
 
@@ -497,8 +498,10 @@ def _kv_call(where: str, device, *args) -> None:
     argument (the stream) is None."""
     import torch
     f = getattr(lib(), where)
-    if torch.cuda.current_device() == device.index:
-        code = f(*args[:-1], _stream(args[-1]))
+    now = torch._C._cuda_getDevice()          # (the cache is on a GPU: the runtime is up)
+    if now == device.index:
+        stream = args[-1]
+        code = f(*args[:-1], torch._C._cuda_getCurrentRawStream(now) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(device):
             code = f(*args[:-1], _stream(args[-1]))

@@ -689,3 +689,18 @@ def test_attn_short_rows_of_any_number(dtype, Hkv, D, B, longest):
     if B == 40:
         acc = np.random.default_rng(2).random((B, Hkv, c["max_pages"] * 16)).astype(np.float32)
         run_attn(c, 2 * Hkv, 1.0 / np.sqrt(D), acc_in=acc)
+
+
+def test_a_handle_whose_tensors_moved():
+    import torch
+    c = ref.make_cache([100, 37], 2, 64, 64, 16, "bf16", seed=66)
+    s, dev, q = shape_of(c, 2, 4), cache_of(c), queries(c, 2, 4)
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((2, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    coli_kv_attn(s, q.cuda(), dev, outs[0], 0.1, ws=ws)
+    half = torch.tensor([50, 37], dtype=torch.int32, device="cuda")
+    dev.lens.set_(half)                          # the handle's tensor now has other memory
+    coli_kv_attn(s, q.cuda(), dev, outs[1], 0.1, ws=ws)
+    few = dict(c, lens=half.cpu())
+    coli_kv_attn(s, q.cuda(), cache_of(few), outs[2], 0.1, ws=ws)
+    assert torch.equal(bits(outs[1]), bits(outs[2])) and not torch.equal(bits(outs[0]), bits(outs[1]))

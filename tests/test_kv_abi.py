@@ -205,7 +205,7 @@ def test_plain_eviction_by_hand():
 def test_a_copied_cache_forms_its_own_handles():
     t = torch.zeros(4)
     c = KvCache(t, None, t.clone(), t.clone())
-    object.__setattr__(c, "_handles", (None, C.byref(C.c_int())))     # as after a call
+    object.__setattr__(c, "_handles", (None, C.byref(C.c_int()), None))     # as after a call
     for d in (copy.copy(c), copy.deepcopy(c)):
         assert "_handles" not in d.__dict__ and torch.equal(d.k, c.k) and d.v is None
     assert copy.deepcopy(c).k.data_ptr() != c.k.data_ptr() and "_handles" in c.__dict__
