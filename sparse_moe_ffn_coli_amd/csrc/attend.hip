@@ -260,9 +260,14 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     using T = typename KT::T;
     constexpr int EPL = KT::EPL, KC = KT::KC, VE = KT::VE, VC = KT::VC, VW = KT::VW;
     // BIG: too wide for a step's rows in registers; keys are taken KP chunks at
-    // a time, values chunk by chunk, each read one ahead of its products.
-    constexpr bool BIG = DK > 256;
-    constexpr int KP = BIG ? (KC % 6 == 0 ? 6 : 5) : KC;
+    // a time, values chunk by chunk, each read one ahead of its products (fp32,
+    // 32 sequences of 4096 positions, 8 heads of 256: 662 us with the whole
+    // rows, which spill 57 registers, 356 so).
+    constexpr bool BIG = DK > (BF16 ? 256 : 192);
+    // KP: 32 sequences of 4096 positions at width 256, 16 latent ones of 4096
+    // at 576 and 320 elements (64 heads): 342, 229, 84 us with four chunks, 213
+    // with six at 576, 89 with five at 320.
+    constexpr int KP = BIG ? (KC % 6 == 0 ? 6 : 4) : KC;
     static_assert(!BIG || (KC % KP == 0 && !BF16), "whole groups; bf16 takes the LDS kernel");
     constexpr int RS = DV + 4;                // padded row of the join buffer
     __shared__ __attribute__((aligned(16))) float red[NW][KV_QT][RS];
@@ -1339,7 +1344,9 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool laten
         // sequences of 4096 positions (8 of 32 heads) take 210 -> 272 us at
         // width 64, 382 -> 446 at 128; 65536 positions alone 95 -> 112 at 256;
         // with 256 less 62 -> 69 us (width 64, one sequence of 65536).
-        p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 256 ? 256 : (d <= 320 && Dv <= 256) ? 320 : 512;
+        // (fp32 width 192, 32 sequences of 4096 positions, 8 heads: 301 us, 535
+        // in the 256-wide kernel, which spills; bf16 150 in both)
+        p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 && !bf16 ? 192 : d <= 256 ? 256 : (d <= 320 && Dv <= 256) ? 320 : 512;
         p.n_wg = 256 * (d <= (bf16 ? 128 : 64) ? 2 : 1);
     }
     p.q_tiles = (G + p.tile_rows - 1) / p.tile_rows;
@@ -1396,7 +1403,8 @@ static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
     else if (p.tier == 128) launch_tier<BF16, 128, 128>(a, p.waves, st);
     else if (p.tier == 256) launch_tier<BF16, 256, 256>(a, p.waves, st);
     else if constexpr (!BF16) {
-        if (p.tier == 320) launch_tier<BF16, 320, 256>(a, p.waves, st);
+        if (p.tier == 192) launch_tier<BF16, 192, 192>(a, p.waves, st);
+        else if (p.tier == 320) launch_tier<BF16, 320, 256>(a, p.waves, st);
         else launch_tier<BF16, 576, 512>(a, p.waves, st);
     }
 }

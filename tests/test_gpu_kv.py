@@ -704,3 +704,14 @@ def test_a_handle_whose_tensors_moved():
     few = dict(c, lens=half.cpu())
     coli_kv_attn(s, q.cuda(), cache_of(few), outs[2], 0.1, ws=ws)
     assert torch.equal(bits(outs[1]), bits(outs[2])) and not torch.equal(bits(outs[0]), bits(outs[1]))
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dk,Dv", [(6, 2, 192, 192), (5, 5, 136, 192), (20, 1, 144, 136), (4, 2, 200, 248), (9, 3, 256, 72),
+                                          (4, 4, 192, 256), (2, 2, 8, 184)])
+def test_attn_f32_widths(Hq, Hkv, Dk, Dv):
+    # every way a wide fp32 row is taken, whole and cut
+    c = ref.make_cache(BORDERS + [700], Hkv, Dk, Dv, 16, "f32", seed=Dk + Dv)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk))
+    c = ref.make_cache([1, 1300, 0, 257], Hkv, Dk, Dv, 64, "f32", seed=Dk + Dv, extra_cols=40)
+    acc = np.random.default_rng(2).random((4, Hkv, c["max_pages"] * 64)).astype(np.float32)
+    run_attn(c, Hq, 2.0 / np.sqrt(Dk), acc_in=acc)
