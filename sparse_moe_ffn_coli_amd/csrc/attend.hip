@@ -618,19 +618,27 @@ __device__ __forceinline__ void attn_join(const AttnLaunch &a, int bq)
     if (tid == 0) kv_write_lse(a, bq, mx, l);
 }
 
-// Running weights of 4 KV_NT positions of a (sequence, cache head):
-// acc_out = acc_in + sum over its query heads of e^(t - m) / l, four positions
-// a thread.  The references m and sums l come from the row's writer or, where
+// Running weights of kv_weight_positions(heads) positions of a (sequence,
+// cache head): acc_out = acc_in + sum over its query heads of e^(t - m) / l,
+// four positions a thread.  Of many heads each wave takes a fourth, and a
+// fourth of the positions (95 latent sequences of 1 to 2263 positions, 128
+// heads, the whole call: 75 us with all heads a thread, 69 so).  The references m and sums l come from the row's writer or, where
 // it was cut, from its parts (the wide kernel's join, which runs before,
 // leaves them like a writer).
+__host__ __device__ inline int kv_weight_positions(int heads) { return heads < 32 ? 4 * KV_NT : 4 * 64; }
+
 __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool joined)
 {
     __shared__ float stat[KV_NT][2];
-    const int chunks = (a.cap + 4 * KV_NT - 1) / (4 * KV_NT);
-    const int tid = threadIdx.x;
+    __shared__ f32x4 others[KV_WAVES - 1][64];
+    const int each = kv_weight_positions(a.Hq / a.Hkv);
+    const bool split = each < 4 * KV_NT;
+    const int chunks = (a.cap + each - 1) / each;
+    const int tid = threadIdx.x, mine = split ? tid & 63 : tid;
+    const int first = split ? tid >> 6 : 0, step = split ? KV_WAVES : 1;     // heads of the thread
     const int bh = at / chunks, b = bh / a.Hkv, h = bh - b * a.Hkv, G = a.Hq / a.Hkv;
     const int n = min(max(a.lens[b], 0), a.cap);
-    const int p0 = (at - bh * chunks) * KV_NT * 4;
+    const int p0 = (at - bh * chunks) * each;
     if (p0 >= n) return;
     int before = 0, total = 0;
     // the lanes that share a head's parts, as many as there may be (one sequence of 43069 positions, 7 heads: 32 us
@@ -641,7 +649,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
         const int most = kv_units(n) / kv_range(a, total * a.Hkv * a.q_tiles) + 2;
         while (share < most && 2 * share <= 64 && 2 * share * G <= KV_NT) share *= 2;
     }
-    const int p = p0 + tid * 4;
+    const int p = p0 + mine * 4;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     const int heads = KV_NT / share, sub = tid & (share - 1);
     for (int i0 = 0; i0 < G; i0 += heads) {
@@ -684,7 +692,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
         __syncthreads();
         if (p < n) {
 #pragma unroll 8
-            for (int i = i0; i < min(G, i0 + heads); ++i) {
+            for (int i = i0 + first; i < min(G, i0 + heads); i += step) {
                 const f32x4 t =
                     *reinterpret_cast<const f32x4 *>(a.scores + ((size_t)b * a.Hq + h * G + i) * a.s_ld + p);
                 const float m = stat[i - i0][0], inv = stat[i - i0][1];
@@ -693,6 +701,13 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
             }
         }
         __syncthreads();
+    }
+    if (split) {
+        if (first > 0) others[first - 1][mine] = sum;
+        __syncthreads();
+        if (first > 0) return;
+#pragma unroll
+        for (int w = 0; w < KV_WAVES - 1; ++w) sum += others[w][mine];
     }
     if (p >= n) return;
     const size_t to = (size_t)bh * a.ld + p;
@@ -1436,7 +1451,8 @@ hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
     else if (a.bf16) launch_main<true>(a, p, st);
     else launch_main<false>(a, p, st);
     const int n_join = p.wide || p.direct ? 0 : a.B * a.Hq;
-    const int n_weights = a.acc_out ? a.B * a.Hkv * ((a.cap + 4 * KV_NT - 1) / (4 * KV_NT)) : 0;
+    const int each = kv_weight_positions(a.Hq / a.Hkv);
+    const int n_weights = a.acc_out ? a.B * a.Hkv * ((a.cap + each - 1) / each) : 0;
     if (n_join + n_weights > 0) attn_finish_kernel<<<n_join + n_weights, KV_NT, 0, st>>>(a, n_join, p.wide);
     return hipGetLastError();
 }
