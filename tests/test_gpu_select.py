@@ -135,3 +135,40 @@ def test_index_topk_one_value():
     # nothing but ties: the lowest positions, whole threads' shares of them
     s = np.full((2, 50000), 1.5, np.float32)
     _check(s, 3000, 4, np.array([50000, 30000], np.int32), label="one value")
+
+
+@pytest.mark.parametrize("L", [16383, 16384, 16385, 32768, 32769])
+def test_index_topk_more_rows_than_workgroups(L):
+    # either side of the two sizes of the key cache, with rows that a workgroup takes after another one's
+    rng = np.random.default_rng(L)
+    rows = 520
+    s = rng.integers(-300, 300, size=(rows, L)).astype(np.float32)
+    lens = rng.integers(0, L + 1, size=rows).astype(np.int32)
+    lens[:6] = [L, 0, 1, 1023, 1024, 1025]
+    _check(s, 1023, 4, lens, label=f"{rows} rows of up to {L}")
+
+
+def test_index_topk_replayed_beside_another_stream():
+    # two captured selections, replayed at once on two streams, against the eager ones
+    import torch
+    rng = np.random.default_rng(5)
+    sets = []
+    for L, k in ((9000, 700), (40000, 2048)):
+        s = torch.from_numpy(rng.standard_normal((80, L)).astype(np.float32)).cuda()
+        want, got = (torch.full((80, k), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+        coli_index_topk(s, k, want, tail=4)
+        torch.cuda.synchronize()
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            coli_index_topk(s, k, got, tail=4)
+        sets.append((s, want, got, stream, graph))
+    for _ in range(4):
+        for _, _, got, _, _ in sets:
+            got.fill_(-7)
+        torch.cuda.synchronize()
+        for _, _, _, stream, graph in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, want, got, _, _ in sets:
+            assert torch.equal(got, want)
