@@ -746,7 +746,7 @@ __global__ __launch_bounds__(KV_NT) void attn_finish_kernel(AttnLaunch a, int n_
 // its reduction slots are given to the positions in the order the lanes hold
 // them.  O^T (256 registers) and the queries (144) stay in registers.
 // Waves that share a stage: WQ = 4, 2, 1 query tiles for up to 128, 64, 32
-// heads; with WQ < 4 the waves also split the positions (WK = 4 / WQ stages
+// heads, fewer where the work is small (attn_plan); with WQ < 4 the waves also split the positions (WK = 4 / WQ stages
 // at a time), and the parts are joined in LDS at the end of a row.
 // LDS layout of a stage: the columns that are values too (DV of them) first,
 // row after row, then the keys' last 64.  A row of the first part is whole
