@@ -100,6 +100,7 @@ struct AppendLaunch {
     int B, Hkv, rows, page_shift, n_pages, max_pages, cap;
     int k_chunks, v_chunks;     // 16-byte chunks of a key and a value (0: latent)
     int tokens;                 // of a workgroup
+    int first;                  // first row of the launch
     const void *k_new, *v_new;
     const int32_t *start, *table, *lens;
     void *k, *v;

@@ -10,6 +10,10 @@
 namespace coli {
 
 constexpr int KVC_NT = 256;
+// Most workgroups of an append's launch: 2^30 threads, a launch holds fewer
+// than 2^32.  More new tokens (2^22 of the widest are 8 GB and up) take
+// several launches.
+constexpr int KVC_MAX_WG = 1 << 22;
 
 // Pool row of position p of cache head h, -1 where the page id is none.
 __device__ __forceinline__ int pool_row(const int32_t *__restrict__ table_row, int p, int h, int Hkv, int page_shift,
@@ -31,7 +35,7 @@ __global__ __launch_bounds__(KVC_NT) void kv_append_kernel(AppendLaunch a)
 {
     const int per = a.k_chunks + a.v_chunks, width = a.Hkv * per;
     const int x = ONE ? 0 : (int)threadIdx.x / width;
-    const int r = ONE ? blockIdx.x : blockIdx.x * a.tokens + x;
+    const int r = a.first + (ONE ? blockIdx.x : blockIdx.x * a.tokens + x);
     if (!ONE && (x >= a.tokens || r >= a.rows)) return;
     int b = r, p;
     if (a.start) {
@@ -68,9 +72,16 @@ hipError_t launch_kv_append(const AppendLaunch &in, hipStream_t st)
     AppendLaunch a = in;
     const int width = a.Hkv * (a.k_chunks + a.v_chunks);
     a.tokens = width < KVC_NT ? KVC_NT / width : 1;
-    if (a.tokens == 1) kv_append_kernel<true><<<a.rows, KVC_NT, 0, st>>>(a);
-    else kv_append_kernel<false><<<(a.rows + a.tokens - 1) / a.tokens, KVC_NT, 0, st>>>(a);
-    return hipGetLastError();
+    const int all = (a.rows + a.tokens - 1) / a.tokens;       // workgroups
+    for (int at = 0; at < all; at += KVC_MAX_WG) {
+        const int n = min(all - at, KVC_MAX_WG);
+        a.first = at * a.tokens;
+        if (a.tokens == 1) kv_append_kernel<true><<<n, KVC_NT, 0, st>>>(a);
+        else kv_append_kernel<false><<<n, KVC_NT, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // The kept rows of one (sequence, cache head), `each` a workgroup: their old

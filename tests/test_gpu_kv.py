@@ -715,3 +715,20 @@ def test_attn_f32_widths(Hq, Hkv, Dk, Dv):
     c = ref.make_cache([1, 1300, 0, 257], Hkv, Dk, Dv, 64, "f32", seed=Dk + Dv, extra_cols=40)
     acc = np.random.default_rng(2).random((4, Hkv, c["max_pages"] * 64)).astype(np.float32)
     run_attn(c, Hq, 2.0 / np.sqrt(Dk), acc_in=acc)
+
+
+@pytest.mark.parametrize("Dk,tokens", [(520, 1), (344, 2)])
+def test_append_of_more_rows_than_a_launch_holds(Dk, tokens):
+    """New tokens on both sides of a launch's last workgroup (2^22 of them, of one or two tokens each).  Sequences of
+    a few positions: the rows before their last ones have no place, and are not looked at."""
+    import torch
+    border, lens, page = tokens << 22, [8, 6], 4
+    c = ref.make_cache(lens, 1, Dk, Dk, page, "f32", True, seed=81)
+    s, cache = shape_of(c, 2, 1), cache_of(c)
+    start = torch.tensor([0, border + 4, border + 13], dtype=torch.int32)
+    rows = border + 15
+    new = torch.empty((rows, 1, Dk), device="cuda")
+    new[border - 64:] = torch.randn((rows - border + 64, 1, Dk), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    coli_kv_append(s, new, None, cache, start=start.cuda())
+    k2, _ = ref.append(c, new[border - 64:].cpu(), None, start.numpy() - (border - 64) * (start.numpy() > 0))
+    same_pool(cache.k, k2, "k")
