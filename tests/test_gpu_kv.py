@@ -723,7 +723,7 @@ def test_append_of_more_rows_than_a_launch_holds(Dk, tokens):
     a few positions: the rows before their last ones have no place, and are not looked at."""
     import torch
     border, lens, page = tokens << 22, [8, 6], 4
-    c = ref.make_cache(lens, 1, Dk, Dk, page, "f32", True, seed=81)
+    c = ref.make_cache(lens, 1, Dk, 64, page, "f32", True, seed=81)
     s, cache = shape_of(c, 2, 1), cache_of(c)
     start = torch.tensor([0, border + 4, border + 13], dtype=torch.int32)
     rows = border + 15
