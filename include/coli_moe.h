@@ -289,7 +289,8 @@ coli_status coli_moe_bank_release(void *compute_stream, void *free_event);
  *   - n <= k: every position 0..n-1 is selected;
  *   - otherwise the last min(tail, k) positions are selected and the other
  *     k - min(tail, k) slots go to the remaining positions by score, larger
- *     first, ties to the lower position (+0 and -0 are equal).
+ *     first, ties to the lower position (+0 and -0 are equal; a NaN ranks
+ *     above every number, one with its sign bit set below).
  * idx [rows][k] int32 receives the selected positions in ascending order,
  * then -1 for the slots left when n < k.  1 <= k <= 4096, 0 <= tail,
  * 0 <= L <= 1 << 24, ld >= L (a multiple of 4), lens[r] >= 0. */

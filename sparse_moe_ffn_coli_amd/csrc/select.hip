@@ -33,11 +33,15 @@ constexpr int SEL_NT = 1024;             // threads per workgroup (16 waves)
 constexpr int SEL_WAVES = SEL_NT / 64;
 constexpr int SEL_BATCH = 8;             // positions per thread whose loads are in flight together
 
+// A tail position's key, above every score's: the last NaN's own key would be
+// the same and is one less.
+constexpr uint32_t TAIL_KEY = 0xffffffffu;
+
 __device__ __forceinline__ uint32_t score_key(float f)
 {
     uint32_t u = __float_as_uint(f);
     if (u == 0x80000000u) u = 0u;        // -0 ranks with +0
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u & 0x80000000u) ? ~u : min(u | 0x80000000u, TAIL_KEY - 1);
 }
 
 constexpr int SEL_CAP = 32768;           // positions whose keys a workgroup keeps in LDS (128 KB)
@@ -93,14 +97,14 @@ __device__ __forceinline__ void store_keys(const float *__restrict__ row, int n,
             uint32_t q[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                q[c] = (i + c >= tail0) ? 0xffffffffu : score_key(v[j][c]);
+                q[c] = (i + c >= tail0) ? TAIL_KEY : score_key(v[j][c]);
                 atomicAdd(&hist[q[c] >> 21], 1);
             }
             *reinterpret_cast<u32x4 *>(keys + i) = u32x4{q[0], q[1], q[2], q[3]};
         }
     }
     for (int i = n4 + (int)threadIdx.x; i < n; i += SEL_NT) {     // the last 0-3 positions
-        const uint32_t q = (i >= tail0) ? 0xffffffffu : score_key(row[i]);
+        const uint32_t q = (i >= tail0) ? TAIL_KEY : score_key(row[i]);
         keys[i] = q;
         atomicAdd(&hist[q >> 21], 1);
     }
@@ -202,7 +206,7 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
                                                 int32_t *ws, int32_t *sel_s, int32_t *__restrict__ out)
 {
     const int tid = threadIdx.x;
-    auto key_of = [&](float f, int i) { return i >= n ? 0u : i >= tail0 ? 0xffffffffu : score_key(f); };
+    auto key_of = [&](float f, int i) { return i >= n ? 0u : i >= tail0 ? TAIL_KEY : score_key(f); };
     // the scores of positions i .. i + 3 (i a multiple of four): one load inside the row, none past its end
     auto scores4 = [&](int i) {
         if (i + 4 <= n) return *reinterpret_cast<const f32x4 *>(row + i);

@@ -732,3 +732,14 @@ def test_append_of_more_rows_than_a_launch_holds(Dk, tokens):
     coli_kv_append(s, new, None, cache, start=start.cuda())
     k2, _ = ref.append(c, new[border - 64:].cpu(), None, start.numpy() - (border - 64) * (start.numpy() > 0))
     same_pool(cache.k, k2, "k")
+
+
+def test_evict_keeps_the_newest_beside_nans():
+    # running weights of a row that met a NaN: the newest positions stay all the same
+    import torch
+    c = ref.make_cache([300], 1, 8, 8, 16, "f32", seed=82, spare_pages=4)
+    s, cache, k, tail = shape_of(c, 1, 1), cache_of(c), 64, 4
+    acc = torch.full((1, 1, c["max_pages"] * 16), 0x7fffffff, dtype=torch.int32, device="cuda").view(torch.float32)
+    new_lens, kept = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty((1, 1, k), dtype=torch.int32, device="cuda")
+    coli_kv_evict(s, cache, acc, k, torch.from_numpy(c["free"][:4][None]).cuda(), new_lens, kept, tail=tail)
+    assert kept[0, 0].tolist() == list(range(k - tail)) + list(range(300 - tail, 300))

@@ -172,3 +172,16 @@ def test_index_topk_replayed_beside_another_stream():
         torch.cuda.synchronize()
         for _, want, got, _, _ in sets:
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("L", [300, 20000, 40000])
+def test_index_topk_tail_stays_beside_nans(L):
+    # the NaN of all ones: above every score, and still not above the tail
+    k, tail = 64, 4
+    s = np.zeros((2, L), np.float32)
+    s.view(np.uint32)[0, :100] = 0x7fffffff
+    s.view(np.uint32)[1, 10:10 + k - tail] = 0x7fffffff
+    got = _gpu(s, k, tail)
+    last = list(range(L - tail, L))
+    assert got[0].tolist() == list(range(k - tail)) + last
+    assert got[1].tolist() == list(range(10, 10 + k - tail)) + last
