@@ -185,3 +185,14 @@ def test_index_topk_tail_stays_beside_nans(L):
     last = list(range(L - tail, L))
     assert got[0].tolist() == list(range(k - tail)) + last
     assert got[1].tolist() == list(range(10, 10 + k - tail)) + last
+
+
+@pytest.mark.parametrize("L,k", [(300, 63), (17000, 64)])
+def test_index_topk_many_rows_taken_whole(L, k):
+    # workgroups that take many rows of at most k positions one after the other, longer ones among them
+    rng = np.random.default_rng(L)
+    s = rng.standard_normal((4000, L)).astype(np.float32)
+    lens = rng.integers(0, k + 1, size=4000).astype(np.int32)
+    lens[::37] = rng.integers(k + 1, L + 1, size=len(lens[::37]))
+    lens[:3], lens[-1] = [k, k + 1, 0], L
+    _check(s, k, 4, lens, label=f"4000 short rows of {L}")
