@@ -286,11 +286,11 @@ __global__ __launch_bounds__(SEL_NT, CAP == SEL_CAP ? 4 : 8) void index_topk_ker
     const int tid = threadIdx.x;
     for (int b = tid; b < 2048; b += SEL_NT) hist[b] = 0;
     int ahead = lens ? lens[rows_per_len == 1 ? blockIdx.x : blockIdx.x / rows_per_len] : L;
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    for (uint32_t r = blockIdx.x; r < (uint32_t)rows; r += gridDim.x) {     // (unsigned: r passes 2^31 by less than a grid)
         const int n = min(max(ahead, 0), L);
         if (lens) {                               // the next row's length is on its way while this row is taken
-            const int next = min(r + (int)gridDim.x, rows - 1);
-            ahead = lens[rows_per_len == 1 ? next : next / rows_per_len];
+            const uint32_t next = min(r + gridDim.x, (uint32_t)rows - 1u);
+            ahead = lens[rows_per_len == 1 ? next : next / (uint32_t)rows_per_len];
         }
         int32_t *__restrict__ out = idx + (size_t)r * k;
         if (n <= k) {                             // the whole row, then -1

@@ -196,3 +196,16 @@ def test_index_topk_many_rows_taken_whole(L, k):
     lens[::37] = rng.integers(k + 1, L + 1, size=len(lens[::37]))
     lens[:3], lens[-1] = [k, k + 1, 0], L
     _check(s, k, 4, lens, label=f"4000 short rows of {L}")
+
+
+def test_index_topk_as_many_rows_as_there_can_be():
+    # the last rows of 2^31 - 1: nothing behind them is written
+    import torch
+    rows, k = 2 ** 31 - 1, 1
+    buf = torch.full((rows + 4096,), -7, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    scores = torch.empty(0, device="cuda").expand(rows, 0)
+    for n in (None, lens):
+        buf.fill_(-7)
+        coli_index_topk(scores, k, buf[:rows].view(rows, 1), lens=n, L=0, ld=0)
+        assert int(buf[:rows].max()) == -1 and int(buf[:rows].min()) == -1 and bool((buf[rows:] == -7).all())
