@@ -353,7 +353,8 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
  *   out[b][i] = sum_p w_p v_p,  w = softmax(t),  lse[b][i] = log sum_p exp(t_p)
  * q [B][Hq][Dk], out [B][Hq][Dv] in the dtype; lse [B][Hq] fp32, nullable.
  * scale is finite (as is scale * log2 e in fp32; else COLI_E_SHAPE).
- * A row without positions gives out = 0 and lse = -inf.  Softmax statistics
+ * A position whose score is -inf has no weight; a row without positions, or
+ * without any other score, gives out = 0 and lse = -inf.  Softmax statistics
  * and sums are fp32; in bf16 the weights enter the products as two bf16
  * parts each (16 bits), so the output's own rounding is the one that counts.
  *   idx (nullable, int32 [B][idx_k], as coli_index_topk writes it): only the

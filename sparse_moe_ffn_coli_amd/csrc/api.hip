@@ -710,6 +710,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     // rounded factor would put on every large score
     a.scale_hi = (float)sc;
     a.scale_lo = (float)(sc - (double)a.scale_hi);
+    a.scale_cap = (float)(3e38 / fmax(1.0, fabs((double)a.scale_lo)));
     a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
     a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
     char *base = (char *)ws;

@@ -197,6 +197,17 @@ struct KvType<false> {
     static constexpr int EPL = 4;
 };
 
+// What a key's columns past its width read, and hidden positions of the latent
+// kernel: zeros, since a zero of the query would not stop an infinity there.
+static __device__ const u32x4 kv_zeros[72] = {};
+
+// A score in units of log2 e.  The factor's small part meets finite numbers
+// only: it may be of the other sign, and an infinite score keeps its own.
+__device__ __forceinline__ float kv_scaled(const AttnLaunch &a, float score)
+{
+    return fmaf(score, a.scale_hi, __builtin_amdgcn_fmed3f(score, -a.scale_cap, a.scale_cap) * a.scale_lo);
+}
+
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -286,7 +297,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     const T *kpool = (const T *)a.k;
     const T *vpool = (const T *)(a.v ? a.v : a.k);
     const int vstride = a.v ? a.Dv : a.Dk;
-    const int key_chunks = (a.Dk + 4 * EPL - 1) / (4 * EPL);
+    const int key_chunks = (a.Dk + 4 * EPL - 1) / (4 * EPL), full_chunks = a.Dk / (4 * EPL);
 
     for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
@@ -323,11 +334,21 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int r = max(__shfl(rows, 16 * t + j), 0);
-                const T *p = kpool + (size_t)r * a.Dk;
+                const T *p = kpool + (size_t)r * a.Dk + g * EPL;
+                // All chunks inside the row (fp32 width 128, 32 sequences of 4096 positions, 8 heads: 40.8 us, 43.0 the other
+                // way; in the widest kernel a second way sends the buffer to scratch, 440 us against 143).
+                if (DK <= 256 && c0 + KP <= full_chunks) {
+#pragma unroll
+                    for (int x = 0; x < KP; ++x)
+                        kf[t][BIG ? (c0 + x) % (2 * KP) : c0 + x] = *reinterpret_cast<const u32x4 *>(p + 4 * (c0 + x) * EPL);
+                    continue;
+                }
 #pragma unroll
                 for (int x = 0; x < KP; ++x) {
-                    const int c = c0 + x, d = (4 * c + g) * EPL;      // past the key's width: a zero of the query meets it
-                    if (BIG || c < key_chunks) kf[t][BIG ? c % (2 * KP) : c] = *reinterpret_cast<const u32x4 *>(p + (d < a.Dk ? d : 0));
+                    const int c = c0 + x;                 // past the row's width: zeros
+                    if (BIG || c < key_chunks)            // (the address space is named: with flat loads 300 -> 400 us at width 192)
+                        kf[t][BIG ? c % (2 * KP) : c] = *(const __attribute__((address_space(1))) u32x4 *)(
+                            (4 * c + g) * EPL < a.Dk ? (uint64_t)(p + 4 * c * EPL) : (uint64_t)kv_zeros);
                 }
             }
         };
@@ -412,7 +433,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
             float t2[8];
             const uint64_t hidden = __ballot(rows_now < 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t2[i] = fmaf(sc[i >> 2][i & 3], a.scale_hi, sc[i >> 2][i & 3] * a.scale_lo);
+            for (int i = 0; i < 8; ++i) t2[i] = kv_scaled(a, sc[i >> 2][i & 3]);
             if (hidden) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -774,9 +795,6 @@ struct KwInt {
     static constexpr int value = N;
 };
 
-// what hidden positions read: they must count as zeros, whatever their memory holds
-static __device__ const u32x4 kw_zeros[72] = {};
-
 __device__ __forceinline__ int kw_swz(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
 
 template <int N>
@@ -823,7 +841,9 @@ __device__ __forceinline__ void kw_mfma_v(f32x16 &d, bf16x8 a, bf16x8 b)
     asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
 }
 
-template <int DK, int DV, int WQ>
+// FULL: rows of DK elements.  Rows that are narrower take zeros past their
+// width, which costs their copies an address for each lane.
+template <int DK, int DV, int WQ, bool FULL>
 __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_kernel(AttnLaunch a)
 {
     constexpr int WK = KV_WAVES / WQ;
@@ -854,7 +874,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const char *pool = (const char *)a.k;
-    const int row_bytes = a.Dk * 2, chunks = a.Dk / 8;
+    const int row_bytes = FULL ? DK * 2 : a.Dk * 2;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
 
     for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
@@ -904,31 +924,32 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 rows_s[tid + x * KV_NT] =
                     (p[x] >= 0 && pg[x] >= 0 && pg[x] < a.n_pages)
                         ? (uint64_t)pool + (uint64_t)(uint32_t)kv_pool_row(a, pg[x], h, p[x]) * (uint32_t)row_bytes
-                        : (uint64_t)kw_zeros;
+                        : (uint64_t)kv_zeros;
         };
         // Copy instructions of 32 rows' two parts into the stage at byte dst; rows: lane i holds row i's address.
-        // Columns past the row's width repeat its last chunk: zeros of the query and output columns that are not
-        // written meet them.
-        const uint32_t last = (chunks - 1) * 16;
+        // Columns past the row's width are zeros.
+        const uint32_t last = row_bytes - 16;
         auto first_off = [&](int i) {                       // the lane's place in its row
             uint32_t lane_at = (lane & (RA - 1)) << 4;
             if constexpr (RPC == 2) lane_at ^= (lane >> 5) << 6;
             return lane_at ^ (kw_swz(i * RPC) << 4);
         };
         auto tail_off = [&](int i) { return (uint32_t)(RA + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))) << 4; };
+        auto inside = [&](uint64_t src, uint32_t off) { return (FULL || off <= last ? src : (uint64_t)kv_zeros) + off; };
         auto copy_first = [&](uint64_t rows, int i, uint32_t dst) {
-            const uint32_t off = min(first_off(i), last);
+            const uint32_t off = first_off(i);
             const uint64_t src = kw_lane(rows, i * RPC);
             if constexpr (RPC == 1) {
-                kw_copy(src, off, dst + i * 1024);
+                if constexpr (FULL) kw_copy(src, off, dst + i * 1024);
+                else kw_copy(inside(src, off), dst + i * 1024);
             } else {
                 const uint64_t other = kw_lane(rows, i * RPC + 1);
-                kw_copy((lane < 32 ? src : other) + off, dst + i * 1024);
+                kw_copy(inside(lane < 32 ? src : other, off), dst + i * 1024);
             }
         };
         auto copy_tail = [&](uint64_t rows, int i, uint32_t dst) {
-            const uint32_t off = min(tail_off(i), last);
-            kw_copy((uint64_t)__shfl((unsigned long long)rows, 8 * i + (lane >> 3)) + off, dst + FIRST + i * 1024);
+            const uint64_t src = (uint64_t)__shfl((unsigned long long)rows, 8 * i + (lane >> 3));
+            kw_copy(inside(src, tail_off(i)), dst + FIRST + i * 1024);
         };
         // copy number i of the wave's share of stage t
         auto copy = [&](int t, uint64_t rows, int i) {
@@ -939,7 +960,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         };
         // lane i's: address of row i (lane 32 + i: the same) of stage t, and which rows are hidden
         auto stage_rows = [&](int t) { return rows_s[(t % KW_BLOCK) * KW_ROWS + ql]; };
-        auto hidden = [&](uint64_t rows) { return (uint32_t)__ballot(rows == (uint64_t)kw_zeros); };
+        auto hidden = [&](uint64_t rows) { return (uint32_t)__ballot(rows == (uint64_t)kv_zeros); };
         auto issue = [&](int t) {
             const uint64_t rows = stage_rows(t);
 #pragma unroll 4
@@ -963,11 +984,11 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         // score operand.
         bf16x8 qf[KS];
         {
-            const uint64_t rows = ql < nq ? (uint64_t)a.q + (qrow + ql) * row_bytes : (uint64_t)kw_zeros;
+            const uint64_t rows = ql < nq ? (uint64_t)a.q + (qrow + ql) * row_bytes : (uint64_t)kv_zeros;
             const uint32_t dst = ring_at + qt * STAGE;
             auto bring = [&](int r, uint32_t off, uint32_t to) {
                 const uint64_t src = (uint64_t)__shfl((unsigned long long)rows, r);
-                kw_copy((off <= last ? src : (uint64_t)kw_zeros) + off, to);
+                kw_copy(inside(src, off), to);
             };
 #pragma unroll 1
             for (int i = kb; i < CA; i += WK) bring(i * RPC + (RPC == 1 ? 0 : lane >> 5), first_off(i), dst + i * 1024);
@@ -1072,7 +1093,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
                 float w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = fmaf(sc[i], a.scale_hi, sc[i] * a.scale_lo);
+                for (int i = 0; i < 16; ++i) w[i] = kv_scaled(a, sc[i]);
                 if (__ballot(hid != 0)) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -1427,7 +1448,8 @@ static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 template <int DK, int DV, int WQ>
 static void launch_wide(const AttnLaunch &a, hipStream_t st)
 {
-    attn_wide_kernel<DK, DV, WQ><<<a.n_wg, KV_NT, 0, st>>>(a);
+    if (a.Dk == DK) attn_wide_kernel<DK, DV, WQ, true><<<a.n_wg, KV_NT, 0, st>>>(a);
+    else attn_wide_kernel<DK, DV, WQ, false><<<a.n_wg, KV_NT, 0, st>>>(a);
     // Of few rows the parts are many and the tiles few: more threads for each
     // (64 heads, whole calls, us with 256 / 1024 threads: one row of 32768
     // positions 60 / 44, 4 of 32768 69 / 65, 16 of 2048 38 / 42).

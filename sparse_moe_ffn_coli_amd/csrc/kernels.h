@@ -70,6 +70,7 @@ struct AttnLaunch {
     const int32_t *table, *lens, *idx;
     int idx_k;
     float scale_hi, scale_lo;   // scale * log2(e) in two floats
+    float scale_cap;       // scores up to it times scale_lo are finite
     void *out;
     float *lse;            // nullable
     const float *acc_in;

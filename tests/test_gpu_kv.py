@@ -743,3 +743,49 @@ def test_evict_keeps_the_newest_beside_nans():
     new_lens, kept = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty((1, 1, k), dtype=torch.int32, device="cuda")
     coli_kv_evict(s, cache, acc, k, torch.from_numpy(c["free"][:4][None]).cuda(), new_lens, kept, tail=tail)
     assert kept[0, 0].tolist() == list(range(k - tail)) + list(range(300 - tail, 300))
+
+
+INFINITE = [("bf16", 8, 2, 128, 128, False), ("bf16", 6, 3, 80, 80, False), ("bf16", 5, 1, 96, 40, False),
+            ("bf16", 4, 2, 72, 136, False), ("bf16", 17, 1, 64, 64, False), ("bf16", 4, 2, 200, 248, False),
+            ("f32", 4, 2, 128, 128, False), ("f32", 3, 3, 8, 8, False), ("f32", 4, 4, 192, 128, False),
+            ("f32", 4, 2, 200, 256, False), ("f32", 18, 1, 576, 512, True), ("f32", 20, 1, 304, 256, True),
+            ("bf16", 20, 1, 576, 512, True), ("bf16", 64, 1, 576, 512, True), ("bf16", 100, 1, 520, 512, True),
+            ("bf16", 33, 1, 400, 384, True), ("bf16", 40, 1, 320, 256, True), ("bf16", 100, 1, 264, 8, True)]
+
+
+def hidden_by_scores(c, q, column, bad, every=5):
+    """Keys of every fifth position (pages of one; of a sequence of three all, if `bad` is infinite) get `bad` in a
+    column where every query is positive, so that their scores are -inf or far below all others: the same cache with
+    those pages hidden is what the plain form reads."""
+    import torch
+    q[..., column] = q[..., column].abs() + 0.5
+    same = dict(c, table=c["table"].clone())
+    for b, n in enumerate(c["lens"].tolist()):
+        for p in range(n):
+            if p % every == 1 or (n == 3 and np.isinf(bad)):
+                c["k"][c["table"][b, p], :, 0, column] = bad
+                same["table"][b, p] = -1
+    return same
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,Dk,Dv,latent", INFINITE)
+@pytest.mark.parametrize("bad", [-np.inf, "lowest"])
+@pytest.mark.parametrize("room", [0, 1 << 13])
+def test_attn_scores_of_minus_infinity(dtype, Hq, Hkv, Dk, Dv, latent, bad, room):
+    """Live keys with an infinity or the type's lowest value: their positions have no weight, whatever the sign of the
+    scale's rounding error, and a sequence of nothing but infinities is an empty row."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    for scale in (2.0, 2.0 / np.sqrt(Dk), 2.0 / np.sqrt(96)):
+        c = ref.make_cache([40, 3, 0, 300], Hkv, Dk, Dv, 1, dtype, latent, seed=91, extra_cols=room + 1)
+        q = queries(c, 4, Hq)
+        same = hidden_by_scores(c, q, Dk - 1, torch.finfo(dt).min if bad == "lowest" else bad)
+        acc = np.random.default_rng(2).random((4, Hkv, c["max_pages"] // 4 * 4 + 4)).astype(np.float32)
+        for acc_in in (None, acc):
+            got = run_attn(c, Hq, scale, acc_in=acc_in, q=q, want=False)
+            r = ref.attn(same, q, scale, acc_in=acc_in)
+            within(got[0].double().numpy(), r["out"], r["tol_out"], "out")
+            within(got[1].numpy(), r["lse"], r["tol_lse"], "lse")
+            for b, n in enumerate(c["lens"].tolist()):
+                if acc_in is not None:
+                    within(got[2][b, :, :n].numpy(), r["acc"][b, :, :n], r["tol_acc"][b, :, :n], "acc")
