@@ -354,7 +354,9 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
  * q [B][Hq][Dk], out [B][Hq][Dv] in the dtype; lse [B][Hq] fp32, nullable.
  * scale is finite (as is scale * log2 e in fp32; else COLI_E_SHAPE).
  * A position whose score is -inf has no weight; a row without positions, or
- * without any other score, gives out = 0 and lse = -inf.  Softmax statistics
+ * without any other score, gives out = 0 and lse = -inf; a NaN or +inf among
+ * a query head's scores makes its out and lse, and acc_out of its cache head
+ * at all positions of the sequence, NaN.  Softmax statistics
  * and sums are fp32; in bf16 the weights enter the products as two bf16
  * parts each (16 bits), so the output's own rounding is the one that counts.
  *   idx (nullable, int32 [B][idx_k], as coli_index_topk writes it): only the

@@ -228,16 +228,18 @@ struct KvTile {
 };
 
 // lse of a query row, and its reference and 1 / sum for the running weights.
+// A sum is 0 for an empty row only, and a NaN for one that met a NaN.
+__device__ __forceinline__ float kv_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ void kv_write_lse(const AttnLaunch &a, size_t q, float m, float l)
 {
-    if (a.lse) a.lse[q] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (a.lse) a.lse[q] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 __device__ __forceinline__ void kv_write_stats(const AttnLaunch &a, size_t q, float m, float l)
 {
     kv_write_lse(a, q, m, l);
     if (a.stats) {
         a.stats[2 * q] = m == -INFINITY ? 0.f : m;
-        a.stats[2 * q + 1] = l > 0.f ? 1.f / l : 0.f;
+        a.stats[2 * q + 1] = kv_inverse(l);
     }
 }
 
@@ -545,7 +547,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
                 v += *reinterpret_cast<const f32x4 *>(&red[w][q][d]) * f;
             }
             if (whole) {
-                const float inv = lq > 0.f ? 1.f / lq : 0.f;
+                const float inv = kv_inverse(lq);
                 const size_t at = (qrow + q) * a.Dv + d;
                 if constexpr (BF16)
                     *reinterpret_cast<u32x2 *>((uint16_t *)a.out + at) =
@@ -629,7 +631,7 @@ __device__ __forceinline__ void attn_join(const AttnLaunch &a, int bq)
     __syncthreads();
     if (tid < cols) {
         for (int x = 1; x < ng; ++x) acc += *reinterpret_cast<const f32x4 *>(red + 4 * (x * cols + col));
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = kv_inverse(l);
         const size_t at = (size_t)bq * a.Dv + 4 * col;
         if (a.bf16)
             *reinterpret_cast<u32x2 *>((uint16_t *)a.out + at) =
@@ -688,7 +690,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
                     const int at_w = w + x * share;
                     const float *ml = a.part_ml + ((size_t)parts.slot(min(at_w, parts.w1)) * KV_QT + i % KV_QT) * 2;
                     mw[x] = at_w <= parts.w1 ? ml[0] : -INFINITY;
-                    lw[x] = ml[1];
+                    lw[x] = at_w <= parts.w1 ? ml[1] : 0.f;
                 }
                 float mn = mx;
 #pragma unroll
@@ -696,7 +698,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
                 const float ref = mn == -INFINITY ? 0.f : mn;
                 l *= __builtin_amdgcn_exp2f(mx - ref);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) l += mw[x] == -INFINITY ? 0.f : lw[x] * __builtin_amdgcn_exp2f(mw[x] - ref);
+                for (int x = 0; x < 4; ++x) l += lw[x] * __builtin_amdgcn_exp2f(mw[x] - ref);
                 mx = mn;
             }
         }
@@ -708,7 +710,7 @@ __device__ __forceinline__ void attn_weights(const AttnLaunch &a, int at, bool j
         }
         if (i < G && sub == 0) {
             stat[tid / share][0] = cut ? (mx == -INFINITY ? 0.f : mx) : a.stats[2 * q];
-            stat[tid / share][1] = cut ? (l > 0.f ? 1.f / l : 0.f) : a.stats[2 * q + 1];
+            stat[tid / share][1] = cut ? kv_inverse(l) : a.stats[2 * q + 1];
         }
         __syncthreads();
         if (p < n) {
@@ -1187,7 +1189,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         }
         // columns 32 x + 8 i + 4 hi .. + 3 of query ql go out
         const bool whole = s0 == 0 && s1 == steps;
-        const float inv = la > 0.f ? 1.f / la : 0.f;
+        const float inv = kv_inverse(la);
         const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
         f32x4 *part = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
         uint16_t *out = (uint16_t *)a.out + (qrow + ql) * a.Dv;
@@ -1336,7 +1338,7 @@ __global__ __launch_bounds__(KV_NT * NG) void attn_wide_join_kernel(AttnLaunch a
         }
     }
     if (ng > 0 || ql >= nq) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = kv_inverse(l);
 #pragma unroll
     for (int x = 0; x < COLS; ++x) {
         const int d = 32 * (part * COLS + x) + 8 * wave + 4 * hi;

@@ -789,3 +789,50 @@ def test_attn_scores_of_minus_infinity(dtype, Hq, Hkv, Dk, Dv, latent, bad, room
             for b, n in enumerate(c["lens"].tolist()):
                 if acc_in is not None:
                     within(got[2][b, :, :n].numpy(), r["acc"][b, :, :n], r["tol_acc"][b, :, :n], "acc")
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,Dk,Dv,latent", [
+    ("bf16", 8, 2, 128, 128, False), ("f32", 6, 2, 80, 80, False), ("f32", 4, 2, 256, 256, False), ("f32", 20, 1, 576, 512, True),
+    ("bf16", 20, 1, 576, 512, True), ("bf16", 100, 1, 576, 512, True), ("bf16", 40, 1, 320, 256, True)])
+@pytest.mark.parametrize("room", [0, 1 << 13])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_attn_nan_and_infinite_queries(dtype, Hq, Hkv, Dk, Dv, latent, room, bad):
+    """One query head of each sequence has a NaN (or an infinity, so that its scores are +inf, -inf and no number): its
+    out, lse and its cache head's running weights are NaN, in rows taken whole and cut, and nothing else is."""
+    import torch
+    lens = [700, 1, 0, 300]
+    c = ref.make_cache(lens, Hkv, Dk, Dv, 16, dtype, latent, seed=92, extra_cols=room // 16 + 1)
+    q, G = queries(c, 4, Hq), Hq // Hkv
+    heads = [Hq - 1, 0, 1, Hq // 2]
+    clean = q.clone()
+    for b, i in enumerate(heads):
+        q[b, i, 3] = bad
+    acc = np.random.default_rng(2).random((4, Hkv, c["max_pages"] * 16)).astype(np.float32)
+    if np.isinf(bad):                        # a sequence of one position: its one score is +inf
+        c["k"][c["table"][1, 0], :, 0, 3] = 1.0
+    for acc_in in (None, acc):
+        out, lse, got_acc = run_attn(c, Hq, 0.2, acc_in=acc_in, q=q, want=False)
+        r = ref.attn(c, clean, 0.2, acc_in=acc_in)
+        for b, n in enumerate(lens):
+            hit = np.zeros(Hq, bool)
+            hit[heads[b]] = n > 0
+            assert bool(torch.isnan(out[b, hit]).all()) and bool(torch.isnan(lse[b, hit]).all()), f"sequence {b}"
+            within(out[b, ~hit].double().numpy(), r["out"][b, ~hit], r["tol_out"][b, ~hit], "out")
+            within(lse[b, ~hit].numpy(), r["lse"][b, ~hit], r["tol_lse"][b, ~hit], "lse")
+            if acc_in is not None:
+                h = hit.reshape(Hkv, G).any(1)
+                assert bool(torch.isnan(got_acc[b, h, :n]).all()), f"running weights of sequence {b}"
+                within(got_acc[b, ~h, :n].numpy(), r["acc"][b, ~h, :n], r["tol_acc"][b, ~h, :n], "acc")
+
+
+def test_attn_nan_in_one_part_of_a_cut_row():
+    # a live key that is all NaN: whatever part of the row it lies in, all heads that read it are NaN
+    import torch
+    for dtype, latent, Hq, D in (("bf16", False, 4, 128), ("bf16", True, 64, 576), ("f32", False, 3, 64)):
+        for at in (0, 9000, 20010):
+            c = ref.make_cache([20011, 50], 1, D, D if not latent else 512, 16, dtype, latent, seed=93)
+            c["k"][c["table"][0, at // 16], :, at % 16] = float("nan")
+            acc = np.zeros((2, 1, c["max_pages"] * 16), np.float32)
+            out, lse, got = run_attn(c, Hq, 0.1, acc_in=acc, want=False)
+            assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all()) and bool(torch.isnan(got[0, 0, :20011]).all())
+            assert not bool(torch.isnan(out[1]).any()) and not bool(torch.isnan(lse[1]).any()) and not bool(torch.isnan(got[1, 0, :50]).any())
