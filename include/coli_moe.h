@@ -359,6 +359,10 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
  * at all positions of the sequence, NaN.  Softmax statistics
  * and sums are fp32; in bf16 the weights enter the products as two bf16
  * parts each (16 bits), so the output's own rounding is the one that counts.
+ * The sum over the positions is divided last, by its weights' sum: the
+ * largest value times the number of positions stays below 2^100.  An
+ * infinite or NaN value of a position makes its column of the output no
+ * finite number.
  *   idx (nullable, int32 [B][idx_k], as coli_index_topk writes it): only the
  *     listed positions take part; entries outside [0, lens[b]) are skipped
  *     (the -1 padding among them), a position listed twice counts twice.

@@ -879,7 +879,14 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     const int row_bytes = FULL ? DK * 2 : a.Dk * 2;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
 
-    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
+    float known = -INFINITY;                  // the reference of a row that is run again
+    bool again = false;
+    auto advance = [&] {
+        u += kv_units(n) - s0;
+        s0 = 0;
+        kv_next_row(a, R, b, n, steps, row);
+    };
+    for (; u < u_end; again ? (void)0 : advance()) {
         const int s1 = min(steps, s0 + (u_end - u));
         if (s0 >= steps) continue;            // a row's units past its steps
         // The lane number is made opaque here (and in issue): the offsets that
@@ -905,7 +912,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
 
         f32x16 o[DT];
-        float m = -INFINITY, l, top;          // m: the reference; top: the largest score
+        float m = known, l, top;              // m: the reference; top: the largest score
 
         // row addresses of the block of stages that holds stage t0 (a multiple of KW_BLOCK)
         auto look_up = [&](int t0) {
@@ -1008,7 +1015,11 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         // weights are numbers of fp32's and bf16's whole range, so a later score
         // may pass it by up to 2^60 without harm, and O^T never has to be moved to
         // another one.  A row where some score passes it further is run again with
-        // its largest score as the reference, by all waves (they share the stages).
+        // its largest score as the reference, by all waves (they share the stages),
+        // and so is one where large values have met weights past 2^20 and a sum is
+        // no number.
+        float above;
+        bool far;
         for (;;) {
             l = 0.f;
             top = -INFINITY;
@@ -1160,8 +1171,9 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             }
             kw_wait_copies<0>();                            // stages past the row's end are copied too, as zeros
             top = fmaxf(top, __shfl_xor(top, 32));
-            const bool past = top > m + 60.f;
-            if (!__syncthreads_or(past)) break;
+            above = top - m;                                // (no number where nothing was seen: not above anything)
+            far = __syncthreads_or(above > 20.f);
+            if (!far || !__syncthreads_or(above > 60.f)) break;
             m = top;
             look_up(0);
             kw_barrier();
@@ -1259,7 +1271,33 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 kv_write_stats(a, qrow + ql, ma, la);
             }
         }
+        again = false;
+        if (far) {
+            // Weights of up to 2^60 may have taken sums past fp32's end: what this wave wrote is read back, and a row with
+            // no number among it is run again (its references are its largest scores then: `far` is false).
+            bool bad = false;
+            if (ql < nq) {
+#pragma unroll 1
+                for (int x = 0; x < DT; ++x) {
+                    if (WK > 1 && x % (DT / 2) % WK != kb) continue;
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        if (!whole) {
+                            const f32x4 v = part[(x * 4 + i) * 64];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) bad |= !(fabsf(v[c]) < INFINITY);
+                        } else if (32 * x + 8 * i + 4 * hi < a.Dv) {
+                            const u32x2 v = *reinterpret_cast<const u32x2 *>(out + 32 * x + 8 * i + 4 * hi);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) bad |= (v[c] & 0x7f80u) == 0x7f80u || (v[c] & 0x7f800000u) == 0x7f800000u;
+                        }
+                    }
+                }
+            }
+            again = __syncthreads_or(bad);
+        }
         kw_barrier();                                       // red_m, red_l and the ring are free again
+        known = again ? top : -INFINITY;
     }
 }
 

@@ -836,3 +836,24 @@ def test_attn_nan_in_one_part_of_a_cut_row():
             out, lse, got = run_attn(c, Hq, 0.1, acc_in=acc, want=False)
             assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all()) and bool(torch.isnan(got[0, 0, :20011]).all())
             assert not bool(torch.isnan(out[1]).any()) and not bool(torch.isnan(lse[1]).any()) and not bool(torch.isnan(got[1, 0, :50]).any())
+
+
+@pytest.mark.parametrize("Hq,Dk,Dv", [(20, 576, 512), (64, 576, 512), (100, 576, 512), (100, 520, 512), (40, 320, 256), (100, 264, 256)])
+@pytest.mark.parametrize("room", [0, 1 << 14])
+@pytest.mark.parametrize("growth", [15.0, 50.0, 90.0])
+def test_attn_latent_large_values(Hq, Dk, Dv, room, growth):
+    """Values near 1e25 beside scores that grow by 2^15 to 2^90 along a sequence: sums under the first stage's reference
+    pass fp32's end, the results are far inside it."""
+    c = ref.make_cache([900, 0, 70, 1], 1, Dk, Dv, 16, "bf16", True, seed=94, extra_cols=room // 16 + 1)
+    q = queries(c, 4, Hq)
+    q[..., :Dv] = 0                          # scores come from the columns that are no values
+    q[..., Dv] = 1.0
+    for b, n in enumerate(c["lens"].tolist()):
+        for p in range(n):
+            row = c["k"][c["table"][b, p // 16], :, p % 16]
+            row[..., :Dv] *= 1e25
+            row[..., Dv:] *= 0.125
+            row[..., Dv] = p / n
+    run_attn(c, Hq, growth * np.log(2.0), q=q)
+    acc = np.random.default_rng(2).random((4, 1, c["max_pages"] * 16)).astype(np.float32)
+    run_attn(c, Hq, growth * np.log(2.0), q=q, acc_in=acc)
