@@ -476,9 +476,13 @@ def _kv_check(where: str, device, *args) -> None:
 
 def _kv_handles(where: str, shape: KvShape, cache: KvCache):
     """The C forms of a shape and a cache and what calls on them share: (shape, cache, dtype, device).  Checked and
-    formed once for a pair of handles, and kept in the cache's until a tensor's memory is another one."""
+    formed once for a pair of handles, and kept in the cache's until a tensor's memory, type, sizes or order is another
+    one (its methods can change them in place)."""
     kept = cache.__dict__.get("_handles")
-    at = (cache.k.data_ptr(), 0 if cache.v is None else cache.v.data_ptr(), cache.table.data_ptr(), cache.lens.data_ptr())
+    k, v, table, lens = cache.k, cache.v, cache.table, cache.lens
+    at = (k.data_ptr(), k.dtype, k.shape, k.is_contiguous(), table.data_ptr(), table.dtype, table.shape, table.is_contiguous(),
+          lens.data_ptr(), lens.dtype, lens.shape, lens.is_contiguous(),
+          None if v is None else (v.data_ptr(), v.dtype, v.shape, v.is_contiguous()))
     if kept is not None and kept[0] is shape and kept[2] == at:
         return kept[1]
     import torch

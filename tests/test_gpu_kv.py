@@ -857,3 +857,30 @@ def test_attn_latent_large_values(Hq, Dk, Dv, room, growth):
     run_attn(c, Hq, growth * np.log(2.0), q=q)
     acc = np.random.default_rng(2).random((4, 1, c["max_pages"] * 16)).astype(np.float32)
     run_attn(c, Hq, growth * np.log(2.0), q=q, acc_in=acc)
+
+
+def test_a_handle_whose_tensors_change_in_place():
+    # the memory stays, the sizes, the order or the type do not: refused, and taken again once they are as before
+    import torch
+    c = ref.make_cache([100, 37], 2, 64, 64, 16, "bf16", seed=67)
+    s, q = shape_of(c, 2, 4), queries(c, 2, 4).cuda()
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((2, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    changes = [("lens", lambda t: t.set_(t[:1])), ("lens", lambda t: t.resize_(1)), ("table", lambda t: t.transpose_(0, 1)),
+               ("table", lambda t: t.resize_(2, 3)), ("k", lambda t: t.transpose_(1, 2)), ("v", lambda t: t.transpose_(0, 3)),
+               ("k", lambda t: setattr(t, "data", t.data.view(torch.float16))), ("lens", lambda t: setattr(t, "data", t.data.view(torch.float32)))]
+    for name, change in changes:
+        dev = cache_of(c)
+        coli_kv_attn(s, q, dev, outs[0], 0.1, ws=ws)
+        t = getattr(dev, name)
+        before, at = t.detach(), t.data_ptr()
+        change(t)
+        assert t.data_ptr() == at
+        new = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(ValueError):
+            coli_kv_attn(s, q, dev, outs[1], 0.1, ws=ws)
+        with pytest.raises(ValueError):
+            coli_kv_append(s, new, new, dev)
+        t.data = before
+        coli_kv_attn(s, q, dev, outs[1], 0.1, ws=ws)
+        assert torch.equal(bits(outs[0]), bits(outs[1]))
