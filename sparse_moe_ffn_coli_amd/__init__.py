@@ -465,12 +465,13 @@ class KvCache:
 def _kv_check(where: str, device, *args) -> None:
     """(name, tensor, dtype, shape) each: the C ABI takes addresses only, so
     types, sizes and devices are checked here."""
+    at = -1 if device.index is None else device.index
     for name, t, dtype, size in args:
         if t is None:
             continue
         if t.dtype is not dtype or t.shape != size:
             raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
-        if t.device != device:
+        if t.get_device() != at:
             raise ValueError(f"{where}: {name} is on {t.device}, the cache on {device}")
 
 

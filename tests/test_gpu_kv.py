@@ -884,3 +884,54 @@ def test_a_handle_whose_tensors_change_in_place():
         t.data = before
         coli_kv_attn(s, q, dev, outs[1], 0.1, ws=ws)
         assert torch.equal(bits(outs[0]), bits(outs[1]))
+
+
+def big_pool(pages=1100):
+    """Pools of more than 2^32 elements (9 GB each), zero but for the first and the last page."""
+    import torch
+    page, D, Hkv = 4096, 256, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros((pages, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    for pool in (k, v):
+        for pg in (0, pages - 1):
+            pool[pg] = torch.randn(pool[pg].shape, generator=g, device="cuda").bfloat16()
+    return k, v, page, D, Hkv, g
+
+
+def test_append_offsets_past_32_bits():
+    import torch
+    k, v, page, D, Hkv, g = big_pool()
+    n = k.shape[0]
+    table = torch.tensor([[n - 1, n - 2]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([page + 3], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    new = torch.randn((8, Hkv, D), generator=g, device="cuda").bfloat16()
+    want = [torch.cat([p[n - 2:], p[:1]]) for p in (k, v)]
+    for x in range(8):
+        p = page + 3 - 8 + x
+        for w, rows in zip(want, (new, -new)):
+            w[1 if p < page else 0, :, p % page] = rows[x]
+    coli_kv_append(KvShape(1, 4, Hkv, D, D, page, n, 2, COLI_BF16), new, -new, KvCache(k, v, table, lens), start=start)
+    for pool, w in zip((k, v), want):
+        assert torch.equal(bits(torch.cat([pool[n - 2:], pool[:1]])), bits(w))
+        assert not bool(pool[1:n - 2].any()), "written elsewhere"
+
+
+def test_evict_offsets_past_32_bits():
+    import torch
+    k, v, page, D, Hkv, g = big_pool()
+    n, keep = k.shape[0], 700
+    table = torch.tensor([[n - 1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([page], dtype=torch.int32, device="cuda")
+    acc = torch.stack([torch.randperm(page, generator=g, device="cuda") for _ in range(Hkv)])[None].float()
+    new_lens, kept = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty((1, Hkv, keep), dtype=torch.int32, device="cuda")
+    last = [p[n - 1:].clone() for p in (k, v)]
+    coli_kv_evict(KvShape(1, 4, Hkv, D, D, page, n, 1, COLI_BF16), KvCache(k, v, table, lens), acc, keep,
+                  torch.tensor([[n - 2]], dtype=torch.int32, device="cuda"), new_lens, kept)
+    want = torch.topk(acc[0], keep, dim=-1).indices.sort(-1).values
+    assert torch.equal(kept[0].long(), want)
+    for pool, old in zip((k, v), last):
+        assert torch.equal(bits(pool[n - 1:]), bits(old)) and not bool(pool[1:n - 2].any()) and not bool(pool[n - 2, :, keep:].any())
+        for h in range(Hkv):
+            assert torch.equal(bits(pool[n - 2, h, :keep]), bits(old[0, h, want[h]]))
