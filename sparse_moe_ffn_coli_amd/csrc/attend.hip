@@ -99,7 +99,7 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
     kv_prefix(a, 0, &before, &total);
     total *= R;
     const int range = kv_range(a, total);
-    const int u = blockIdx.x * range;         // at most total + n_wg * min_units: below 2^31 by the host's check
+    const int u = blockIdx.x * range;         // below total + n_wg * (KV_ROW_UNITS + 1), and 2^31 by the host's check
     if (u >= total) return false;
     int base = 0;
     if (a.idx) {
@@ -275,12 +275,12 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     // BIG: too wide for a step's rows in registers; keys are taken KP chunks at
     // a time, values chunk by chunk, each read one ahead of its products (fp32,
     // 32 sequences of 4096 positions, 8 heads of 256: 662 us with the whole
-    // rows, which spill 57 registers, 356 so).
+    // rows, which spill 57 registers, 354 so).
     constexpr bool BIG = DK > (BF16 ? 256 : 192);
     // KP: 32 sequences of 4096 positions at width 256, 16 latent ones of 4096
-    // at 576 and 320 elements (64 heads): 342, 229, 84 us with four chunks, 213
-    // with six at 576, 89 with five at 320.
-    constexpr int KP = BIG ? (KC % 6 == 0 ? 6 : 4) : KC;
+    // at 576 and 320 elements (64 heads): 354, 140, 80 us with four chunks, 144
+    // with six at 576, 80 with five at 320.
+    constexpr int KP = BIG ? 4 : KC;
     static_assert(!BIG || (KC % KP == 0 && !BF16), "whole groups; bf16 takes the LDS kernel");
     constexpr int RS = DV + 4;                // padded row of the join buffer
     __shared__ __attribute__((aligned(16))) float red[NW][KV_QT][RS];
@@ -843,9 +843,12 @@ __device__ __forceinline__ void kw_mfma_v(f32x16 &d, bf16x8 a, bf16x8 b)
     asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
 }
 
-// FULL: rows of DK elements.  Rows that are narrower take zeros past their
-// width, which costs their copies an address for each lane.
-template <int DK, int DV, int WQ, bool FULL>
+// PAST: which of a row's parts lie past its width in some columns and take
+// zeros there, which costs their copies an address for each lane (one row of
+// 512 positions, 512 elements, 16 heads: 24.0 us with the tail so, 25.0 with
+// both).
+enum KwPast { KW_NONE, KW_TAIL, KW_BOTH };
+template <int DK, int DV, int WQ, KwPast PAST>
 __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_kernel(AttnLaunch a)
 {
     constexpr int WK = KV_WAVES / WQ;
@@ -876,7 +879,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const char *pool = (const char *)a.k;
-    const int row_bytes = FULL ? DK * 2 : a.Dk * 2;
+    const int row_bytes = PAST == KW_NONE ? DK * 2 : a.Dk * 2;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
 
     float known = -INFINITY;                  // the reference of a row that is run again
@@ -944,21 +947,21 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
             return lane_at ^ (kw_swz(i * RPC) << 4);
         };
         auto tail_off = [&](int i) { return (uint32_t)(RA + ((lane & 7) ^ ((4 * i + (lane >> 4)) & 7))) << 4; };
-        auto inside = [&](uint64_t src, uint32_t off) { return (FULL || off <= last ? src : (uint64_t)kv_zeros) + off; };
+        auto inside = [&](uint64_t src, uint32_t off) { return (off <= last ? src : (uint64_t)kv_zeros) + off; };
         auto copy_first = [&](uint64_t rows, int i, uint32_t dst) {
             const uint32_t off = first_off(i);
             const uint64_t src = kw_lane(rows, i * RPC);
             if constexpr (RPC == 1) {
-                if constexpr (FULL) kw_copy(src, off, dst + i * 1024);
-                else kw_copy(inside(src, off), dst + i * 1024);
+                if constexpr (PAST == KW_BOTH) kw_copy(inside(src, off), dst + i * 1024);
+                else kw_copy(src, off, dst + i * 1024);
             } else {
-                const uint64_t other = kw_lane(rows, i * RPC + 1);
-                kw_copy(inside(lane < 32 ? src : other, off), dst + i * 1024);
+                const uint64_t other = kw_lane(rows, i * RPC + 1), mine = lane < 32 ? src : other;
+                kw_copy(PAST == KW_BOTH ? inside(mine, off) : mine + off, dst + i * 1024);
             }
         };
         auto copy_tail = [&](uint64_t rows, int i, uint32_t dst) {
             const uint64_t src = (uint64_t)__shfl((unsigned long long)rows, 8 * i + (lane >> 3));
-            kw_copy(inside(src, tail_off(i)), dst + FIRST + i * 1024);
+            kw_copy(PAST == KW_NONE ? src + tail_off(i) : inside(src, tail_off(i)), dst + FIRST + i * 1024);
         };
         // copy number i of the wave's share of stage t
         auto copy = [&](int t, uint64_t rows, int i) {
@@ -1420,8 +1423,8 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool laten
         // sequences of 4096 positions (8 of 32 heads) take 210 -> 272 us at
         // width 64, 382 -> 446 at 128; 65536 positions alone 95 -> 112 at 256;
         // with 256 less 62 -> 69 us (width 64, one sequence of 65536).
-        // (fp32 width 192, 32 sequences of 4096 positions, 8 heads: 301 us, 535
-        // in the 256-wide kernel, which spills; bf16 150 in both)
+        // (fp32 width 192, 32 sequences of 4096 positions, 8 heads: 288 us, 297
+        // in the 256-wide kernel; bf16 150 in both)
         p.tier = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 && !bf16 ? 192 : d <= 256 ? 256 : (d <= 320 && Dv <= 256) ? 320 : 512;
         p.n_wg = 256 * (d <= (bf16 ? 128 : 64) ? 2 : 1);
     }
@@ -1488,8 +1491,9 @@ static void launch_main(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 template <int DK, int DV, int WQ>
 static void launch_wide(const AttnLaunch &a, hipStream_t st)
 {
-    if (a.Dk == DK) attn_wide_kernel<DK, DV, WQ, true><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else attn_wide_kernel<DK, DV, WQ, false><<<a.n_wg, KV_NT, 0, st>>>(a);
+    if (a.Dk == DK) attn_wide_kernel<DK, DV, WQ, KW_NONE><<<a.n_wg, KV_NT, 0, st>>>(a);
+    else if (a.Dk >= DV) attn_wide_kernel<DK, DV, WQ, KW_TAIL><<<a.n_wg, KV_NT, 0, st>>>(a);
+    else attn_wide_kernel<DK, DV, WQ, KW_BOTH><<<a.n_wg, KV_NT, 0, st>>>(a);
     // Of few rows the parts are many and the tiles few: more threads for each
     // (64 heads, whole calls, us with 256 / 1024 threads: one row of 32768
     // positions 60 / 44, 4 of 32768 69 / 65, 16 of 2048 38 / 42).

@@ -31,7 +31,7 @@ namespace coli {
 
 constexpr int SEL_NT = 1024;             // threads per workgroup (16 waves)
 constexpr int SEL_WAVES = SEL_NT / 64;
-constexpr int SEL_BATCH = 8;             // positions per thread whose loads are in flight together
+constexpr int SEL_GROUPS = 4;            // groups of four scores a thread of a long row has in flight
 
 // A tail position's key, above every score's: the last NaN's own key would be
 // the same and is one less.
@@ -49,7 +49,7 @@ constexpr int SEL_CAP = 32768;           // positions whose keys a workgroup kee
 constexpr int SEL_SHORT = 16384;         // the same where no row is longer: two workgroups a CU
 
 // Barrier for LDS traffic only: every wave's LDS operations have completed
-// (global loads in flight, such as the next row's prefetch, are not waited for).
+// (global loads and stores in flight are not waited for).
 __device__ __forceinline__ void lds_barrier()
 {
     __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0)
@@ -217,7 +217,6 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
             if (i + c < n) v[c] = row[i + c];
         return v;
     };
-    constexpr int GRP = SEL_BATCH / 2;            // groups of four positions a thread has in flight
     uint32_t prefix = 0;
     int need = k;
 #pragma unroll 1
@@ -225,12 +224,12 @@ __device__ __forceinline__ void select_uncached(const float *__restrict__ row, i
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int nb = pass == 2 ? 1024 : 2048;
         const uint32_t hi = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 2 ? 10 : 11));
-        for (int b0 = 4 * tid; b0 < n; b0 += 4 * GRP * SEL_NT) {
-            f32x4 v[GRP];
+        for (int b0 = 4 * tid; b0 < n; b0 += 4 * SEL_GROUPS * SEL_NT) {
+            f32x4 v[SEL_GROUPS];
 #pragma unroll
-            for (int j = 0; j < GRP; ++j) v[j] = scores4(b0 + 4 * j * SEL_NT);
+            for (int j = 0; j < SEL_GROUPS; ++j) v[j] = scores4(b0 + 4 * j * SEL_NT);
 #pragma unroll
-            for (int j = 0; j < GRP; ++j)
+            for (int j = 0; j < SEL_GROUPS; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int i = b0 + 4 * j * SEL_NT + c;
@@ -356,8 +355,8 @@ hipError_t launch_index_topk(const float *scores, int rows, int L, long ld, cons
                              int k, int tail, int32_t *idx, hipStream_t st)
 {
     if (rows == 0) return hipSuccess;
-    // two workgroups a CU where rows are short (2048 rows of 8192 scores: 49 us,
-    // 64 with one; of 300 scores 33 and 45), with room for long ones else
+    // two workgroups a CU where rows are short (2048 rows of 8192 scores: 46 us,
+    // 59 with one; of 300 scores 32 and 44), with room for long ones else
     if (L <= SEL_SHORT)
         index_topk_kernel<SEL_SHORT><<<min(rows, 512), SEL_NT, 0, st>>>(scores, rows, L, ld, lens, rows_per_len, k, tail, idx);
     else

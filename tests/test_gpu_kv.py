@@ -750,7 +750,7 @@ INFINITE = [("bf16", 8, 2, 128, 128, False), ("bf16", 6, 3, 80, 80, False), ("bf
             ("f32", 4, 2, 128, 128, False), ("f32", 3, 3, 8, 8, False), ("f32", 4, 4, 192, 128, False),
             ("f32", 4, 2, 200, 256, False), ("f32", 18, 1, 576, 512, True), ("f32", 20, 1, 304, 256, True),
             ("bf16", 20, 1, 576, 512, True), ("bf16", 64, 1, 576, 512, True), ("bf16", 100, 1, 520, 512, True),
-            ("bf16", 33, 1, 400, 384, True), ("bf16", 40, 1, 320, 256, True), ("bf16", 100, 1, 264, 8, True)]
+            ("bf16", 33, 1, 400, 384, True), ("bf16", 40, 1, 320, 256, True), ("bf16", 100, 1, 264, 8, True), ("bf16", 40, 1, 200, 128, True)]
 
 
 def hidden_by_scores(c, q, column, bad, every=5):
