@@ -376,7 +376,10 @@ coli_status coli_kv_append(const coli_kv_shape *s, const void *k_new, const void
  *     error).  Not together with idx.
  * ws: coli_kv_attn_workspace_bytes(s, idx_k, acc != 0) bytes (0 for an
  * invalid shape; idx_k = 0 without idx).  Calls that may run at the same time
- * need a workspace each. */
+ * need a workspace each.  The workspace and how the call is cut go by
+ * max_pages * page, not by lens: tables no wider than the call needs are
+ * faster, and with running weights take less workspace (B * Hq * max_pages *
+ * page floats). */
 size_t coli_kv_attn_workspace_bytes(const coli_kv_shape *s, int32_t idx_k, int32_t acc);
 coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
                          const int32_t *idx, int32_t idx_k, const float *acc_in, float *acc_out,

@@ -779,10 +779,12 @@ __global__ __launch_bounds__(KV_NT) void attn_finish_kernel(AttnLaunch a, int n_
 // instruction brings one row (or two of 256 columns), so its address is
 // uniform: a few scalar instructions, which go between the products.
 // Measured, 576 / 512 elements: 32 sequences of 8000 to 32768 positions, 128
-// heads, 253-296 us (658 MB and 157 GFLOP of the formula, 231 with the weights'
-// second parts: the matrix cores at the clock they keep under this load);
-// 64 heads over 64 rows of 2048 listed positions 53 us (151 MB, 2.9 TB/s: a
-// workgroup starts, takes 16 stages and leaves a part), and 9 for the join.
+// heads, 253-273 us (658 MB and 157 GFLOP of the formula, 231 with the weights'
+// second parts).  Bound by the order of a stage's work: scores, weights and
+// output follow one another, on one wave a SIMD, so the matrix cores are busy
+// half of the time that the CUs are (and HBM is at half its rate).  64 heads
+// over 64 rows of 2048 listed positions: 53 us (151 MB, 2.9 TB/s: a workgroup
+// starts, takes 16 stages and leaves a part), and 9 for the join.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -1390,8 +1392,11 @@ __global__ __launch_bounds__(KV_NT * NG) void attn_wide_join_kernel(AttnLaunch a
     if (part == 0 && wave == 0 && hi == 0) kv_write_stats(a, q, mx, l);
 }
 
-// How a call runs.  entries: the longest row (the cache's capacity, or the
-// listed positions).
+// How a call runs.  entries: the longest row there may be (the table's room, or
+// the listed positions): the lengths are on the device.  Short sequences in
+// wide tables are cut like long ones (64 sequences of 1 to 200 positions, 32 /
+// 8 heads of 128: 9.3 us in tables for 224 positions, 14.4 for 1792 or 14336;
+// with running weights 13.7, 19.8, 25.5, by the second pass's grid).
 AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int entries)
 {
     AttnPlan p{};

@@ -1,7 +1,7 @@
 // kvcache.hip -- writing a paged key-value cache: new tokens' rows into their
 // sequences' pages, and the copy of an eviction's kept rows into new pages.
 // Both move rows of 16-byte chunks and nothing else: bound by the bytes read
-// and written.  16384 tokens of eight 128-wide heads: 28.4 us (134 MB, 4.7
+// and written.  16384 tokens of eight 128-wide heads: 28.8 us (134 MB, 4.7
 // TB/s); 262144 kept rows of 512 bytes (268 MB) 61 us, 4.4 TB/s; a device copy
 // moves 4.9.
 #include "device_common.h"
@@ -28,7 +28,7 @@ __device__ __forceinline__ int pool_row(const int32_t *__restrict__ table_row, i
 // One new token a workgroup, or several narrow ones (a.tokens), so that its threads have a chunk each: with
 // one, 16384 tokens of two 64-wide heads (32 chunks) took 15.8 us, with
 // eight 6.9.  (With one the place is looked up in scalar registers: 16384
-// tokens of eight 128-wide heads 30 us, 41 without.)  The sequence of row r is the last b with start[b] <= r (found by
+// tokens of eight 128-wide heads 28.8 us, 41.9 without.)  The sequence of row r is the last b with start[b] <= r (found by
 // halving; start ascends), its position lens[b] - (start[b + 1] - r).
 template <bool ONE>
 __global__ __launch_bounds__(KVC_NT) void kv_append_kernel(AppendLaunch a)
