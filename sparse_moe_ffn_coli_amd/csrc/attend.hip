@@ -779,7 +779,7 @@ __global__ __launch_bounds__(KV_NT) void attn_finish_kernel(AttnLaunch a, int n_
 // instruction brings one row (or two of 256 columns), so its address is
 // uniform: a few scalar instructions, which go between the products.
 // Measured, 576 / 512 elements: 32 sequences of 8000 to 32768 positions, 128
-// heads, 253-273 us (658 MB and 157 GFLOP of the formula, 231 with the weights'
+// heads, 246-273 us (658 MB and 157 GFLOP of the formula, 231 with the weights'
 // second parts).  Bound by the order of a stage's work: scores, weights and
 // output follow one another, on one wave a SIMD, so the matrix cores are busy
 // half of the time that the CUs are (and HBM is at half its rate).  64 heads
