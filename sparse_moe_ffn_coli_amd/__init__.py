@@ -462,66 +462,64 @@ class KvCache:
         return CKvCache(_ptr(self.k), _ptr(self.v), _ptr(self.table), _ptr(self.lens))
 
 
-def _kv_check(where: str, device, *args) -> None:
-    """(name, tensor, dtype, shape) each: the C ABI takes addresses only, so
-    types, sizes and devices are checked here."""
-    at = -1 if device.index is None else device.index
-    for name, t, dtype, size in args:
-        if t is None:
-            continue
-        if t.dtype is not dtype or t.shape != size:
-            raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
-        if t.get_device() != at:
-            raise ValueError(f"{where}: {name} is on {t.device}, the cache on {device}")
+def _kv_arg(where: str, at: int, name: str, t, dtype, size) -> Optional[int]:
+    """Address of an argument (None: none).  The C ABI takes addresses only, so types, sizes, order and device numbers
+    are checked here."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != size:
+        raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"{where}: {name} is on {t.device}, the cache on device {at}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _kv_handles(where: str, shape: KvShape, cache: KvCache):
-    """The C forms of a shape and a cache and what calls on them share: (shape, cache, dtype, device).  Checked and
-    formed once for a pair of handles, and kept in the cache's until a tensor's memory, type, sizes or order is another
-    one (its methods can change them in place)."""
+    """The C forms of a shape and a cache and what calls on them share: (shape, cache, dtype, device number, torch).
+    Checked and formed once for a pair of handles, and kept in the cache's until a tensor's memory, type, sizes or order
+    is another one (its methods can change them in place)."""
     kept = cache.__dict__.get("_handles")
     k, v, table, lens = cache.k, cache.v, cache.table, cache.lens
-    at = (k.data_ptr(), k.dtype, k.shape, k.is_contiguous(), table.data_ptr(), table.dtype, table.shape, table.is_contiguous(),
-          lens.data_ptr(), lens.dtype, lens.shape, lens.is_contiguous(),
-          None if v is None else (v.data_ptr(), v.dtype, v.shape, v.is_contiguous()))
-    if kept is not None and kept[0] is shape and kept[2] == at:
+    now = (k.data_ptr(), k.dtype, k.shape, k.is_contiguous(), table.data_ptr(), table.dtype, table.shape, table.is_contiguous(),
+           lens.data_ptr(), lens.dtype, lens.shape, lens.is_contiguous(),
+           None if v is None else (v.data_ptr(), v.dtype, v.shape, v.is_contiguous()))
+    if kept is not None and kept[0] is shape and kept[2] == now:
         return kept[1]
     import torch
-    dt, i32, dev = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32, cache.k.device
+    dt, i32, at = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32, k.get_device()
     pool = (shape.n_pages, shape.Hkv, shape.page)
-    _kv_check(where, dev, ("cache.k", cache.k, dt, pool + (shape.Dk,)), ("cache.v", cache.v, dt, pool + (shape.Dv,)),
-              ("cache.table", cache.table, i32, (shape.B, shape.max_pages)), ("cache.lens", cache.lens, i32, (shape.B,)))
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: the cache must be on a GPU, not on {dev}")
-    got = (C.byref(shape.c()), C.byref(cache.c()), dt, dev)
-    object.__setattr__(cache, "_handles", (shape, got, at))
+    c = CKvCache(_kv_arg(where, at, "cache.k", k, dt, pool + (shape.Dk,)), _kv_arg(where, at, "cache.v", v, dt, pool + (shape.Dv,)),
+                 _kv_arg(where, at, "cache.table", table, i32, (shape.B, shape.max_pages)),
+                 _kv_arg(where, at, "cache.lens", lens, i32, (shape.B,)))
+    if k.device.type != "cuda":
+        raise ValueError(f"{where}: the cache must be on a GPU, not on {k.device}")
+    got = (C.byref(shape.c()), C.byref(c), dt, at, torch)
+    object.__setattr__(cache, "_handles", (shape, got, now))
     return got
 
 
-def _kv_call(where: str, device, *args) -> None:
-    """The library's function with the cache's device as the current one, on its current stream where the last
-    argument (the stream) is None."""
-    import torch
+def _kv_call(torch, where: str, at: int, stream, *args) -> None:
+    """The library's function with the cache's device as the current one, on its current stream where `stream` is None."""
     f = getattr(lib(), where)
-    now = torch._C._cuda_getDevice()          # (the cache is on a GPU: the runtime is up)
-    if now == device.index:
-        stream = args[-1]
-        code = f(*args[:-1], torch._C._cuda_getCurrentRawStream(now) if stream is None else _stream(stream))
+    if torch._C._cuda_getDevice() == at:          # (the cache is on a GPU: the runtime is up)
+        code = f(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            code = f(*args[:-1], _stream(args[-1]))
+        with torch.cuda.device(at):
+            code = f(*args, _stream(stream))
     if code:
         _check(code, where)
 
 
 def coli_kv_append(shape: KvShape, k_new, v_new, cache: KvCache, start=None, stream=None) -> None:
     """k_new [rows][Hkv][Dk], v_new [rows][Hkv][Dv] (None for a latent cache); start int32 [B + 1] or None."""
-    import torch
-    cs, cc, dt, dev = _kv_handles("coli_kv_append", shape, cache)
-    rows = k_new.shape[0]
-    _kv_check("coli_kv_append", dev, ("k_new", k_new, dt, (rows, shape.Hkv, shape.Dk)),
-              ("v_new", v_new, dt, (rows, shape.Hkv, shape.Dv)), ("start", start, torch.int32, (shape.B + 1,)))
-    _kv_call("coli_kv_append", dev, cs, _ptr(k_new), _ptr(v_new), rows, _ptr(start), cc, stream)
+    me = "coli_kv_append"
+    cs, cc, dt, at, torch = _kv_handles(me, shape, cache)
+    rows, H = k_new.shape[0], shape.Hkv
+    _kv_call(torch, me, at, stream, cs, _kv_arg(me, at, "k_new", k_new, dt, (rows, H, shape.Dk)),
+             _kv_arg(me, at, "v_new", v_new, dt, (rows, H, shape.Dv)), rows,
+             _kv_arg(me, at, "start", start, torch.int32, (shape.B + 1,)), cc)
 
 
 def coli_kv_attn_workspace_bytes(shape: KvShape, idx_k: int = 0, acc: bool = False) -> int:
@@ -532,38 +530,36 @@ def coli_kv_attn_workspace_bytes(shape: KvShape, idx_k: int = 0, acc: bool = Fal
 def coli_kv_attn(shape: KvShape, q, cache: KvCache, out, scale: float, idx=None, acc_in=None, acc_out=None, lse=None,
                  ws=None, ws_bytes=None, stream=None) -> None:
     """q [B][Hq][Dk], out [B][Hq][Dv], lse fp32 [B][Hq], idx int32 [B][idx_k], acc fp32 [B][Hkv][ld]."""
-    import torch
-    cs, cc, dt, dev = _kv_handles("coli_kv_attn", shape, cache)
-    B, Hq, f32 = shape.B, shape.Hq, torch.float32
+    me = "coli_kv_attn"
+    cs, cc, dt, at, torch = _kv_handles(me, shape, cache)
+    B, Hq, H, f32 = shape.B, shape.Hq, shape.Hkv, torch.float32
     ld = 0 if acc_out is None else acc_out.shape[-1]
     idx_k = 0 if idx is None else idx.shape[-1]
-    _kv_check("coli_kv_attn", dev, ("q", q, dt, (B, Hq, shape.Dk)), ("out", out, dt, (B, Hq, shape.Dv)),
-              ("lse", lse, f32, (B, Hq)), ("idx", idx, torch.int32, (B, idx_k)),
-              ("acc_in", acc_in, f32, (B, shape.Hkv, ld)), ("acc_out", acc_out, f32, (B, shape.Hkv, ld)))
     # an empty tensor has no address, and without one the argument would count as absent
     if (idx is not None and idx_k == 0) or (acc_out is not None and ld == 0):
         raise ValueError("coli_kv_attn: idx and acc_out must not be empty")
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"coli_kv_attn: ws is on {ws.device}, the cache on {dev}")
-    _kv_call("coli_kv_attn", dev, cs, _ptr(q), cc, scale, _ptr(idx), idx_k, _ptr(acc_in), _ptr(acc_out), ld, _ptr(out),
-             _ptr(lse), _ptr(ws), _nbytes(ws, ws_bytes), stream)
+    if ws is not None and ws.get_device() != at:
+        raise ValueError(f"coli_kv_attn: ws is on {ws.device}, the cache on device {at}")
+    _kv_call(torch, me, at, stream, cs, _kv_arg(me, at, "q", q, dt, (B, Hq, shape.Dk)), cc, scale,
+             _kv_arg(me, at, "idx", idx, torch.int32, (B, idx_k)), idx_k, _kv_arg(me, at, "acc_in", acc_in, f32, (B, H, ld)),
+             _kv_arg(me, at, "acc_out", acc_out, f32, (B, H, ld)), ld, _kv_arg(me, at, "out", out, dt, (B, Hq, shape.Dv)),
+             _kv_arg(me, at, "lse", lse, f32, (B, Hq)), _ptr(ws), _nbytes(ws, ws_bytes))
 
 
 def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_lens, kept, tail: int = 0, new_acc=None,
                   stream=None) -> None:
     """acc fp32 [B][Hkv][ld], new_table int32 [B][pages], new_lens int32 [B], kept int32 [B][Hkv][k],
     new_acc fp32 [B][Hkv][new_ld]."""
-    import torch
-    cs, cc, _, dev = _kv_handles("coli_kv_evict", shape, cache)
+    me = "coli_kv_evict"
+    cs, cc, _, at, torch = _kv_handles(me, shape, cache)
     B, H, f32, i32 = shape.B, shape.Hkv, torch.float32, torch.int32
     ld, cols = acc.shape[-1], new_table.shape[-1]
     new_ld = 0 if new_acc is None else new_acc.shape[-1]
-    _kv_check("coli_kv_evict", dev, ("acc", acc, f32, (B, H, ld)), ("new_table", new_table, i32, (B, cols)),
-              ("new_lens", new_lens, i32, (B,)), ("kept", kept, i32, (B, H, k)), ("new_acc", new_acc, f32, (B, H, new_ld)))
     if new_acc is not None and new_ld == 0:
         raise ValueError("coli_kv_evict: new_acc must not be empty")
-    _kv_call("coli_kv_evict", dev, cs, cc, _ptr(acc), ld, k, tail, _ptr(new_table), cols, _ptr(new_lens), _ptr(kept),
-             _ptr(new_acc), new_ld, stream)
+    _kv_call(torch, me, at, stream, cs, cc, _kv_arg(me, at, "acc", acc, f32, (B, H, ld)), ld, k, tail,
+             _kv_arg(me, at, "new_table", new_table, i32, (B, cols)), cols, _kv_arg(me, at, "new_lens", new_lens, i32, (B,)),
+             _kv_arg(me, at, "kept", kept, i32, (B, H, k)), _kv_arg(me, at, "new_acc", new_acc, f32, (B, H, new_ld)), new_ld)
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
