@@ -935,3 +935,83 @@ def test_evict_offsets_past_32_bits():
         assert torch.equal(bits(pool[n - 1:]), bits(old)) and not bool(pool[1:n - 2].any()) and not bool(pool[n - 2, :, keep:].any())
         for h in range(Hkv):
             assert torch.equal(bits(pool[n - 2, h, :keep]), bits(old[0, h, want[h]]))
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [("bf16", 8, 2, 128), ("bf16", 4, 4, 64), ("f32", 4, 2, 128), ("f32", 2, 1, 256)])
+def test_attn_large_values(dtype, Hq, Hkv, D):
+    # the largest values the documentation allows for 900 positions, scores far apart
+    c = ref.make_cache([900, 3, 0, 130], Hkv, D, D, 16, dtype, seed=95)
+    c["v"] *= 2.0 ** 86
+    run_attn(c, Hq, 1.0)
+
+
+@pytest.mark.parametrize("Hq,Dk,Dv", [(20, 576, 512), (64, 576, 512), (128, 576, 512), (100, 512, 512), (100, 320, 256)])
+@pytest.mark.parametrize("growth", [0.0, 90.0])
+def test_attn_latent_replays_bitwise(Hq, Dk, Dv, growth):
+    """Eager calls and replays of a captured one, with other calls on the workspace in between: the same bits, also in
+    rows that are run again."""
+    import torch
+    c = ref.make_cache([3000, 0, 17, 900, 2100], 1, Dk, Dv, 16, "bf16", True, seed=96, extra_cols=1 << 10)
+    if growth:
+        for b, n in enumerate(c["lens"].tolist()):
+            for p in range(0, n, 3):
+                c["k"][c["table"][b, p // 16], :, p % 16] *= 1.0 + 2.0 * p / 3000
+    s, dev, scale = shape_of(c, 5, Hq), cache_of(c), 0.1 if not growth else 3.0
+    q, other = queries(c, 5, Hq).cuda(), queries(c, 5, Hq, seed=2).cuda()
+    out, lse = torch.empty((5, Hq, Dv), dtype=torch.bfloat16, device="cuda"), torch.empty((5, Hq), device="cuda")
+    acc = torch.zeros((5, 1, c["max_pages"] * 16), device="cuda")
+    ws = torch.empty(coli_kv_attn_workspace_bytes(s, acc=True), dtype=torch.uint8, device="cuda")
+
+    def step(q=q):
+        coli_kv_attn(s, q, dev, out, scale, acc_out=acc, lse=lse, ws=ws)
+
+    step()
+    want = [t.clone() for t in (out, lse, acc)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(6):
+        step(other)
+        out.fill_(3.0)
+        if i % 2:
+            torch.cuda.synchronize()
+            graph.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want[0])) and torch.equal(bits(lse), bits(want[1])) and torch.equal(bits(acc), bits(want[2]))
+
+
+def test_evict_replays():
+    # a captured eviction with work of the program's own between its replays
+    import torch
+    c = ref.make_cache([500, 40, 0, 300], 2, 64, 64, 16, "bf16", seed=97, spare_pages=32)
+    s, dev, k = shape_of(c, 4, 2), cache_of(c), 100
+    table = torch.from_numpy(c["free"][:28].reshape(4, 7)).cuda()
+    acc = torch.zeros((4, 2, c["max_pages"] * 16), device="cuda")
+    new_lens, kept = torch.empty(4, dtype=torch.int32, device="cuda"), torch.empty((4, 2, k), dtype=torch.int32, device="cuda")
+    new_acc = torch.empty((4, 2, 112), device="cuda")
+
+    def step():
+        coli_kv_evict(s, dev, acc, k, table, new_lens, kept, tail=4, new_acc=new_acc)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    before = dev.k.clone(), dev.v.clone()
+    for i in range(4):
+        host = np.random.default_rng(i).random(tuple(acc.shape)).astype(np.float32)
+        acc.copy_(torch.from_numpy(host))
+        dev.lens.copy_(torch.tensor([500 - i, 40 + i, i, 300], dtype=torch.int32))
+        dev.k.copy_(before[0])
+        dev.v.copy_(before[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        now = dict(c, lens=dev.lens.cpu(), k=before[0].cpu(), v=before[1].cpu())
+        r = ref.evict(now, host, k, 4, table.cpu().numpy(), new_acc.cpu().numpy())
+        assert np.array_equal(kept.cpu().numpy(), r["kept"]) and np.array_equal(new_acc.cpu().numpy(), r["new_acc"])
+        assert np.array_equal(new_lens.cpu().numpy(), r["new_lens"])
+        same_pool(dev.k, r["k"], "k")
+        same_pool(dev.v, r["v"], "v")
