@@ -410,6 +410,99 @@ coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const 
                           int32_t *new_lens, int32_t *kept, float *new_acc, int64_t new_ld,
                           void *stream);
 
+/* ---- a step's plan: pages, places and positions of new tokens ---------------
+ * From the lengths that the sequences of a batch have and want, on the GPU:
+ * which pages go back and which are taken, the page tables, and where every
+ * new token of the step goes.  For each sequence b of lens[b] positions:
+ *   want[b] <  lens[b]: it is cut to want[b] positions (0: it has ended); the
+ *     pages behind them go to the tail of the ring of free pages, except the
+ *     first shared[b] of its row, which are not its own (shared nullable: all
+ *     are; shared[b] is at most the pages it holds, before and after);
+ *   want[b] >  lens[b]: it grows by want[b] - lens[b] new tokens and takes the
+ *     pages it needs more from the head of the ring, in the order of the
+ *     sequences and of their positions.
+ * Pages that go back can be taken in the same call.  First come, first served:
+ * the first growing sequence that the ring cannot serve, or whose tokens pass
+ * the step's `rows`, stays as it is, and so does every growing one after it.
+ *   ring [n_pages] int32: free page ids, the first at ring[head], from the
+ *     array's end on to its start.  Every page is at most once in the ring or
+ *     in one sequence's hands
+ *   state [4] int32: head and number of free pages; new_state receives them,
+ *     the new tokens of the step and the number of sequences that were refused
+ *   table [B][max_pages] int32: the taken pages are written behind the held
+ *     ones; all other entries stay
+ *   new_lens [B] int32 receives the lengths
+ *   start [B+1] int32 receives the new tokens' first rows (as coli_kv_append
+ *     reads them, with new_lens)
+ *   slot, pos [rows] int32 receive each row's place in the pool (page id *
+ *     page + position % page; -1 where the page id is outside the pool) and
+ *     its position; -1 and -1 behind the last one
+ * Lengths (lens and want) outside [0, max_pages * page] are clamped to it.
+ * new_lens may be lens and new_state may be state (a step in place; any other
+ * overlap is an error).  The shape's B, page, n_pages and max_pages count;
+ * n_pages <= 2^30, 0 <= rows <= 2^25.  B = 0: start[0] = 0, no rows. */
+coli_status coli_kv_plan(const coli_kv_shape *s, int32_t *table, const int32_t *lens, const int32_t *want,
+                         const int32_t *shared, int32_t *ring, const int32_t *state, int32_t *new_lens,
+                         int32_t *new_state, int32_t *start, int32_t rows, int32_t *slot, int32_t *pos,
+                         void *stream);
+
+/* ---- queries and keys of new tokens: norm, rotation, places -------------------
+ * One pass from a projection's output to the attention's input.  Of each
+ * token's rows (q [Hq][Dk], k [Hkv][Dk], v [Hkv][Dv]; the token's rows begin
+ * q_ld, k_ld, v_ld elements apart, so q, k and v may lie in one tensor):
+ *   norm (nullable): the first `width` elements of every query head (where q_w
+ *     is given) and key head (k_w) become x_i w_i / sqrt(mean(x^2) + eps)
+ *   rope (nullable): `rot` elements of every query and key head from rot_at on
+ *     are rotated in pairs by the angle a = pos[r] * freq[i] (64 bits):
+ *       (x_i, x_j) <- amp (x_i cos a - x_j sin a, x_j cos a + x_i sin a)
+ *     pairs (2 i, 2 i + 1) of them if interleaved, else (i, i + rot / 2)
+ * Norm and rotation are fp32 and are rounded once.
+ *   q_out [rows][Hq][Dk] receives the queries (q NULL: none)
+ *   k_out [rows][Hkv][Dk] (nullable) receives the keys
+ *   slot [rows] int32 (nullable, as coli_kv_plan writes it): the keys go to
+ *     pool_k [n_pages][Hkv][page][Dk] and v to pool_v [n_pages][Hkv][page][Dv]
+ *     (v and pool_v NULL: latent rows).  A slot outside [0, n_pages * page)
+ *     takes nothing; no two rows of a call have the same slot
+ *   pos [rows] int32: a row of negative position is left out, nothing of it is
+ *     written.  NULL (every row counts) only without rope
+ * q_out may be q and k_out may be k where their rows lie side by side (q_ld =
+ * Hq * Dk, k_ld = Hkv * Dk).  The shape's Hq, Hkv, Dk, Dv, page, n_pages and
+ * dtype count.  rows <= 2^25; width, rot and rot_at multiples of 8, width <=
+ * Dk, rot_at + rot <= Dk; q_ld, k_ld, v_ld multiples of 8, at least a token's
+ * row; eps >= 0. */
+typedef struct {
+    const void *q_w; /* [width] in the dtype, NULL: queries are not normed */
+    const void *k_w; /* [width] in the dtype, NULL: keys are not normed */
+    int32_t width;
+    float eps;
+} coli_qk_norm;
+
+typedef struct {
+    const double *freq; /* [rot / 2] device: angle per position */
+    int32_t rot, rot_at;
+    int32_t interleaved;
+    float amp;          /* factor on cosines and sines, finite; 1 */
+} coli_rope;
+
+coli_status coli_kv_rope(const coli_kv_shape *s, int32_t rows, const void *q, int64_t q_ld, const void *k,
+                         int64_t k_ld, const void *v, int64_t v_ld, const coli_qk_norm *norm,
+                         const coli_rope *rope, const int32_t *pos, const int32_t *slot, void *q_out,
+                         void *k_out, void *pool_k, void *pool_v, void *stream);
+
+/* The angles per position and the factor for coli_rope, written to HOST memory:
+ * f_i = base^(-2 i / rot), amp = 1, and for contexts `factor` times as long as
+ * the `length` positions that a model was trained on:
+ *   COLI_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   COLI_ROPE_NTK     base * factor^(rot / (rot - 2)) in base's place
+ *   COLI_ROPE_YARN    f_i where length * f_i / 2 pi >= 32 turns, f_i / factor
+ *                     where it is at most 1, in between the share of f_i rises
+ *                     with the turns; amp = 0.1 ln(factor) + 1
+ * rot a multiple of 8 in [8, 576], base > 1, factor >= 1, length >= 1 (all
+ * finite). */
+enum { COLI_ROPE_PLAIN = 0, COLI_ROPE_LINEAR = 1, COLI_ROPE_NTK = 2, COLI_ROPE_YARN = 3 };
+coli_status coli_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double length,
+                            double *freq, float *amp);
+
 /* Static description of a status code. */
 const char *coli_moe_status_str(coli_status st);
 

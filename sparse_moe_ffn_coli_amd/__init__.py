@@ -23,6 +23,11 @@ The entry points keep the C names:
   coli_kv_attn_workspace_bytes(shape, idx_k=0, acc=False) -> int
   coli_kv_attn(shape, q, cache, out, scale, idx=None, acc_in=None, acc_out=None, lse=None, ws, stream=None)
   coli_kv_evict(shape, cache, acc, k, new_table, new_lens, kept, tail=0, new_acc=None, stream=None)
+  coli_kv_plan(shape, table, lens, want, ring, state, start, slot, pos, shared=None, new_lens=None,
+               new_state=None, stream=None)
+  coli_rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, length=4096) -> (freq, amp)
+  coli_kv_rope(shape, q, k, v, q_out, pos=None, rope=None, norm=None, k_out=None, pool_k=None, pool_v=None,
+               slot=None, stream=None)
   coli_moe_status_str(code) -> str
 
 If the library has not been built the import still works, but every call
@@ -48,6 +53,7 @@ EXPORTED = ("coli_moe_workspace_bytes", "coli_moe_route", "coli_moe_ffn", "coli_
             "coli_moe_bank_fill", "coli_moe_bank_acquire", "coli_moe_bank_release",
             "coli_index_topk_workspace_bytes", "coli_index_topk", "coli_moe_ffn_noalloc",
             "coli_kv_append", "coli_kv_attn_workspace_bytes", "coli_kv_attn", "coli_kv_evict",
+            "coli_kv_plan", "coli_rope_freqs", "coli_kv_rope",
             "coli_moe_status_str", "coli_moe_version")
 ROUTE_STAGES = ("router", "topk", "perm")
 FFN_STAGES = ("gate_up", "down", "combine")
@@ -96,6 +102,14 @@ class CKvShape(C.Structure):
 
 class CKvCache(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p), ("lens", C.c_void_p)]
+
+
+class CQkNorm(C.Structure):
+    _fields_ = [("q_w", C.c_void_p), ("k_w", C.c_void_p), ("width", C.c_int32), ("eps", C.c_float)]
+
+
+class CRope(C.Structure):
+    _fields_ = [("freq", C.c_void_p), ("rot", C.c_int32), ("rot_at", C.c_int32), ("interleaved", C.c_int32), ("amp", C.c_float)]
 
 
 _lib = None
@@ -157,6 +171,13 @@ def lib():
         L.coli_kv_attn.argtypes = [kp, vp, cp, C.c_float, vp, i32, vp, vp, i64, vp, vp, vp, sz, vp]
         L.coli_kv_evict.restype = C.c_int
         L.coli_kv_evict.argtypes = [kp, cp, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp]
+        L.coli_kv_plan.restype = C.c_int
+        L.coli_kv_plan.argtypes = [kp] + [vp] * 9 + [i32, vp, vp, vp]
+        f64 = C.c_double
+        L.coli_rope_freqs.restype = C.c_int
+        L.coli_rope_freqs.argtypes = [i32, f64, i32, f64, f64, C.POINTER(f64), C.POINTER(C.c_float)]
+        L.coli_kv_rope.restype = C.c_int
+        L.coli_kv_rope.argtypes = [kp, i32, vp, i64, vp, i64, vp, i64, C.POINTER(CQkNorm), C.POINTER(CRope)] + [vp] * 7
         L.coli_moe_status_str.restype = C.c_char_p
         L.coli_moe_status_str.argtypes = [C.c_int]
         L.coli_moe_version.restype = C.c_int32
@@ -560,6 +581,114 @@ def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_le
     _kv_call(torch, me, at, stream, cs, cc, _kv_arg(me, at, "acc", acc, f32, (B, H, ld)), ld, k, tail,
              _kv_arg(me, at, "new_table", new_table, i32, (B, cols)), cols, _kv_arg(me, at, "new_lens", new_lens, i32, (B,)),
              _kv_arg(me, at, "kept", kept, i32, (B, H, k)), _kv_arg(me, at, "new_acc", new_acc, f32, (B, H, new_ld)), new_ld)
+
+
+def coli_kv_plan(shape: KvShape, table, lens, want, ring, state, start, slot, pos, shared=None, new_lens=None, new_state=None,
+                 stream=None) -> None:
+    """All int32 on one GPU: table [B][max_pages], lens, want, shared and new_lens [B], ring [n_pages], state and new_state
+    [4], start [B + 1], slot and pos [rows].  new_lens or new_state None: lens or state is written in place."""
+    me = "coli_kv_plan"
+    import torch
+    i32, B, rows = torch.int32, (shape.B,), slot.shape
+    if ring.device.type != "cuda":
+        raise ValueError(f"{me}: ring must be on a GPU, not on {ring.device}")
+    if len(rows) != 1:
+        raise ValueError(f"{me}: slot must have one dimension")
+    at = ring.get_device()
+
+    def arg(name, t, size):
+        return _kv_arg(me, at, name, t, i32, size)
+
+    plens, pstate = arg("lens", lens, B), arg("state", state, (4,))
+    _kv_call(torch, me, at, stream, C.byref(shape.c()), arg("table", table, (shape.B, shape.max_pages)), plens,
+             arg("want", want, B), arg("shared", shared, B), arg("ring", ring, (shape.n_pages,)), pstate,
+             plens if new_lens is None else arg("new_lens", new_lens, B),
+             pstate if new_state is None else arg("new_state", new_state, (4,)), arg("start", start, (shape.B + 1,)), rows[0],
+             arg("slot", slot, rows), arg("pos", pos, rows))
+
+
+ROPE_SCALINGS = ("plain", "linear", "ntk", "yarn")
+
+
+def coli_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, length: float = 4096):
+    """The angle per position of each pair (float64 tensor [rot / 2] on the CPU) and the factor on cosines and sines."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"coli_rope_freqs: scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
+    freq, amp = (C.c_double * max(rot // 2, 1))(), C.c_float()
+    _check(lib().coli_rope_freqs(rot, base, ROPE_SCALINGS.index(scaling), factor, length, freq, C.byref(amp)), "coli_rope_freqs")
+    return torch.tensor(list(freq), dtype=torch.float64), amp.value
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Rotation by positions, see coli_rope.  freq: float64 on the GPU, one of each pair; 2 * its length elements of a
+    head are rotated, from rot_at on."""
+    freq: object
+    rot_at: int = 0
+    interleaved: bool = False
+    amp: float = 1.0
+
+
+@dataclass(frozen=True)
+class QkNorm:
+    """Norm of each head's first elements, see coli_qk_norm; as many as the weights have."""
+    q_w: object = None
+    k_w: object = None
+    eps: float = 1e-6
+
+
+def _kv_rows(where: str, at: int, name: str, t, dtype, size):
+    """Address of [rows][heads][width] values and the elements from a row to the next; only whole rows may lie apart."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape != size:
+        raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"{where}: {name} is on {t.device}, the other tensors on device {at}")
+    ld, *rest = t.stride()
+    H, D = size[1:]
+    if size[0] < 2:
+        ld = max(ld, H * D)                          # (of one row the stride says nothing)
+    if (D > 1 and rest[1] != 1) or (H > 1 and rest[0] != D):
+        raise ValueError(f"{where}: the heads of a row of {name} must lie side by side")
+    return t.data_ptr(), ld
+
+
+def coli_kv_rope(shape: KvShape, q, k, v, q_out, pos=None, rope: Optional[Rope] = None, norm: Optional[QkNorm] = None, k_out=None,
+                 pool_k=None, pool_v=None, slot=None, stream=None) -> None:
+    """q [rows][Hq][Dk], k [rows][Hkv][Dk], v [rows][Hkv][Dv] (slices of a wider tensor may be passed), q_out and k_out of
+    their sizes, pos and slot int32 [rows], the cache's pools."""
+    me = "coli_kv_rope"
+    import torch
+    some = k if q is None else q
+    if some is None:
+        raise ValueError(f"{me}: q or k must be given")
+    if some.device.type != "cuda":
+        raise ValueError(f"{me}: the tensors must be on a GPU, not on {some.device}")
+    at, rows = some.get_device(), some.shape[0]
+    dt, i32 = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32
+    Hq, H, Dk, Dv = shape.Hq, shape.Hkv, shape.Dk, shape.Dv
+    pool = (shape.n_pages, H, shape.page)
+    pq, q_ld = _kv_rows(me, at, "q", q, dt, (rows, Hq, Dk))
+    pk, k_ld = _kv_rows(me, at, "k", k, dt, (rows, H, Dk))
+    pv, v_ld = _kv_rows(me, at, "v", v, dt, (rows, H, Dv))
+    cn = cr = None
+    if norm is not None and not (norm.q_w is None and norm.k_w is None):
+        n = (norm.k_w if norm.q_w is None else norm.q_w).shape
+        if len(n) != 1:
+            raise ValueError(f"{me}: the norm's weights must have one dimension")
+        cn = C.byref(CQkNorm(_kv_arg(me, at, "norm.q_w", norm.q_w, dt, n), _kv_arg(me, at, "norm.k_w", norm.k_w, dt, n), n[0], norm.eps))
+    if rope is not None:
+        n = rope.freq.shape
+        if len(n) != 1:
+            raise ValueError(f"{me}: rope.freq must have one dimension")
+        cr = C.byref(CRope(_kv_arg(me, at, "rope.freq", rope.freq, torch.float64, n), 2 * n[0], rope.rot_at,
+                           1 if rope.interleaved else 0, rope.amp))
+    _kv_call(torch, me, at, stream, C.byref(shape.c()), rows, pq, q_ld, pk, k_ld, pv, v_ld, cn, cr,
+             _kv_arg(me, at, "pos", pos, i32, (rows,)), _kv_arg(me, at, "slot", slot, i32, (rows,)),
+             _kv_arg(me, at, "q_out", q_out, dt, (rows, Hq, Dk)), _kv_arg(me, at, "k_out", k_out, dt, (rows, H, Dk)),
+             _kv_arg(me, at, "pool_k", pool_k, dt, pool + (Dk,)), _kv_arg(me, at, "pool_v", pool_v, dt, pool + (Dv,)))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

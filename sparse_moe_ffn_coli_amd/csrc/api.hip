@@ -5,6 +5,7 @@
 // outright when data is missing: "Add GLM-5.3-Flash (glm5next) support with
 // ROCmFP mix qtypes (105/106)", section "Loader").
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -263,7 +264,7 @@ coli_status scratch_for_current_device(void **out)
 
 extern "C" {
 
-int32_t coli_moe_version(void) { return 200; }
+int32_t coli_moe_version(void) { return 300; }
 
 const char *coli_moe_status_str(coli_status st)
 {
@@ -758,6 +759,121 @@ coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const 
     a.acc = acc; a.ld = (long)ld; a.keep = k; a.tail = tail;
     a.new_table = new_table; a.new_lens = new_lens; a.kept = kept; a.new_acc = new_acc; a.new_ld = (long)new_ld;
     return coli::launch_kv_evict(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+}
+
+coli_status coli_kv_plan(const coli_kv_shape *s, int32_t *table, const int32_t *lens, const int32_t *want,
+                         const int32_t *shared, int32_t *ring, const int32_t *state, int32_t *new_lens,
+                         int32_t *new_state, int32_t *start, int32_t rows, int32_t *slot, int32_t *pos,
+                         void *stream)
+{
+    coli_status st = check_kv_shape(s, false);
+    if (st == COLI_E_SHAPE) st = check_kv_shape(s, true);      // either kind of cache
+    if (st != COLI_OK) return st;
+    if (rows < 0 || rows > (1 << 25) || s->n_pages > (1 << 30)) return COLI_E_SHAPE;
+    if (!ring || !state || !new_state || !start) return COLI_E_NULL;
+    if (s->B > 0 && (!table || !lens || !want || !new_lens)) return COLI_E_NULL;
+    if (rows > 0 && (!slot || !pos)) return COLI_E_NULL;
+    if (!aligned16(table) || !aligned16(lens) || !aligned16(want) || !aligned16(shared) || !aligned16(ring) ||
+        !aligned16(state) || !aligned16(new_lens) || !aligned16(new_state) || !aligned16(start) || !aligned16(slot) ||
+        !aligned16(pos))
+        return COLI_E_ALIGN;
+    const size_t B4 = (size_t)s->B * 4, R4 = (size_t)rows * 4;
+    const Region outs[] = {{table, B4 * s->max_pages}, {ring, (size_t)s->n_pages * 4}, {new_lens, B4}, {new_state, 16},
+                           {start, B4 + 4}, {slot, R4}, {pos, R4}};
+    // lens and state may be written in place
+    const Region ins[] = {{want, B4}, {shared, B4}, {lens, lens == new_lens ? 0 : B4}, {state, state == new_state ? (size_t)0 : (size_t)16}};
+    if (any_overlap(outs, 7, ins, 4)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    coli::PlanLaunch a{};
+    a.B = s->B; a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
+    a.cap = s->max_pages * s->page; a.rows = rows;
+    a.want = want; a.shared = shared; a.ring = ring; a.state = state; a.lens = lens;
+    a.new_state = new_state; a.new_lens = new_lens;
+    a.table = table; a.start = start; a.slot = slot; a.pos = pos;
+    return coli::launch_kv_plan(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+}
+
+coli_status coli_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double length, double *freq, float *amp)
+{
+    if (rot < 8 || rot > 576 || rot % 8 || scaling < COLI_ROPE_PLAIN || scaling > COLI_ROPE_YARN) return COLI_E_SHAPE;
+    if (!(base > 1) || !(base < INFINITY) || !(factor >= 1) || !(factor < INFINITY) || !(length >= 1) || !(length < INFINITY))
+        return COLI_E_SHAPE;
+    if (!freq || !amp) return COLI_E_NULL;
+    if (scaling == COLI_ROPE_NTK) base *= pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        if (scaling == COLI_ROPE_LINEAR) f /= factor;
+        if (scaling == COLI_ROPE_YARN) {
+            const double turns = length * f / 6.283185307179586477;
+            const double keep = fmin(fmax((turns - 1) / 31, 0.0), 1.0);
+            f = f * keep + f / factor * (1 - keep);
+        }
+        freq[i] = f;
+    }
+    *amp = scaling == COLI_ROPE_YARN ? (float)(0.1 * log(factor) + 1) : 1.f;
+    return COLI_OK;
+}
+
+coli_status coli_kv_rope(const coli_kv_shape *s, int32_t rows, const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                         const void *v, int64_t v_ld, const coli_qk_norm *norm, const coli_rope *rope,
+                         const int32_t *pos, const int32_t *slot, void *q_out, void *k_out, void *pool_k, void *pool_v,
+                         void *stream)
+{
+    coli_status st = check_kv_shape(s, !v);
+    if (st == COLI_E_SHAPE && !k && !v) st = check_kv_shape(s, false);   // queries alone: for either kind of cache
+    if (st != COLI_OK) return st;
+    if (rows < 0 || rows > (1 << 25)) return COLI_E_SHAPE;
+    const int64_t qw = (int64_t)s->Hq * s->Dk, kw = (int64_t)s->Hkv * s->Dk, vw = (int64_t)s->Hkv * s->Dv;
+    const int64_t most = (int64_t)1 << 32;
+    if (q && (q_ld < qw || q_ld % 8 || q_ld > most)) return COLI_E_SHAPE;
+    if (k && (k_ld < kw || k_ld % 8 || k_ld > most)) return COLI_E_SHAPE;
+    if (v && (v_ld < vw || v_ld % 8 || v_ld > most)) return COLI_E_SHAPE;
+    if (norm && (norm->width < 8 || norm->width % 8 || norm->width > s->Dk || !(norm->eps >= 0) || !(norm->eps <= 3e38f)))
+        return COLI_E_SHAPE;
+    if (rope && (rope->rot < 8 || rope->rot % 8 || rope->rot_at < 0 || rope->rot_at % 8 ||
+                 rope->rot > s->Dk || rope->rot_at > s->Dk - rope->rot || !(fabsf(rope->amp) <= 3e38f)))
+        return COLI_E_SHAPE;
+    if (rows == 0) return check_device();
+    if (!q && !k) return COLI_E_NULL;
+    if (!q != !q_out || (k_out && !k) || (rope && (!rope->freq || !pos))) return COLI_E_NULL;
+    if (slot ? (!k || !pool_k || !v != !pool_v) : (v || pool_k || pool_v)) return COLI_E_NULL;
+    if (k && !slot && !k_out) return COLI_E_NULL;              // keys with nowhere to go
+    const void *q_w = norm ? norm->q_w : nullptr, *k_w = norm ? norm->k_w : nullptr;
+    const void *freq = rope ? rope->freq : nullptr;
+    const void *all[] = {q, k, v, q_w, k_w, freq, pos, slot, q_out, k_out, pool_k, pool_v};
+    for (const void *p : all)
+        if (!aligned16(p)) return COLI_E_ALIGN;
+    const size_t elt = kv_elt(s), pool = kv_pool_rows(s), n = (size_t)rows;
+    const Region outs[] = {{q_out, n * qw * elt}, {k_out, n * kw * elt}, {pool_k, pool * s->Dk * elt}, {pool_v, pool * s->Dv * elt}};
+    auto span = [&](const void *p, int64_t ld, int64_t w) { return p ? ((n - 1) * (size_t)ld + (size_t)w) * elt : (size_t)0; };
+    // in place: the same rows, side by side
+    const bool q_in = q && q == q_out && q_ld == qw, k_in = k && k == k_out && k_ld == kw;
+    const Region ins[] = {{q, q_in ? 0 : span(q, q_ld, qw)}, {k, k_in ? 0 : span(k, k_ld, kw)}, {v, span(v, v_ld, vw)},
+                          {q_w, q_w ? norm->width * elt : 0}, {k_w, k_w ? norm->width * elt : 0},
+                          {freq, rope ? (size_t)rope->rot * 4 : 0}, {pos, pos ? n * 4 : 0}, {slot, slot ? n * 4 : 0}};
+    if (any_overlap(outs, 4, ins, 8)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    coli::RopeLaunch a{};
+    a.rows = rows;
+    a.nq = q ? s->Hq : 0; a.nk = k ? s->Hkv : 0; a.nv = v ? s->Hkv : 0;
+    a.Hkv = s->Hkv; a.Dk = s->Dk; a.Dv = s->Dv;
+    a.bf16 = s->dtype == COLI_BF16;
+    a.q = q; a.k = k; a.v = v;
+    a.q_ld = (long)q_ld; a.k_ld = (long)k_ld; a.v_ld = (long)v_ld;
+    a.q_w = q_w; a.k_w = k_w;
+    a.width = q_w || k_w ? norm->width : 0;
+    a.inv_width = a.width ? 1.f / (float)a.width : 0.f;
+    a.eps = norm ? norm->eps : 0.f;
+    if (rope) {
+        a.freq = rope->freq; a.rot = rope->rot; a.rot_at = rope->rot_at;
+        a.interleaved = rope->interleaved != 0; a.amp = rope->amp;
+    }
+    a.pos = pos; a.slot = slot;
+    a.q_out = q_out; a.k_out = k_out; a.pool_k = pool_k; a.pool_v = pool_v;
+    a.page_shift = page_shift(s); a.places = s->n_pages * s->page;
+    return coli::launch_kv_rope(a, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
 }
 
 coli_status coli_moe_ffn_noalloc(const coli_moe_shape *s, const void *x, const coli_moe_routing *r,

@@ -1,5 +1,5 @@
 // kernels.h -- internal launch interface between the C ABI (api.hip) and the
-// kernels (route.hip, ffn.hip, select.hip, attend.hip, kvcache.hip).  Not part of the public interface.
+// kernels (route.hip, ffn.hip, select.hip, attend.hip, kvcache.hip, plan.hip, rope.hip).  Not part of the public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -121,6 +121,38 @@ struct EvictLaunch {
     long new_ld;
 };
 
+struct PlanLaunch {
+    int B, page_shift, n_pages, max_pages, cap, rows;
+    const int32_t *want, *shared;   // shared nullable
+    int32_t *ring;
+    const int32_t *state, *lens;
+    int32_t *new_state, *new_lens;  // may be state and lens
+    int32_t *table, *start, *slot, *pos;
+};
+
+struct RopeLaunch {
+    int rows, nq, nk, nv;           // heads of each kind (0: absent)
+    int Hkv, Dk, Dv;
+    bool bf16;
+    const void *q, *k, *v;
+    long q_ld, k_ld, v_ld;          // elements from a token's row to the next
+    const void *q_w, *k_w;          // nullable
+    int width;                      // normed elements (0: none)
+    float inv_width, eps;
+    const double *freq;
+    int rot, rot_at;                // rotated elements (0: none), first of them
+    bool interleaved;
+    float amp;
+    const int32_t *pos, *slot;      // nullable
+    void *q_out, *k_out, *pool_k, *pool_v;
+    int page_shift, places;
+    int heads, lane_shift;          // of a token, in all; log2 of the lanes of a head
+    int first;                      // first token of the launch
+    int tokens, parts, part_heads;  // tokens of a workgroup; workgroups that share them, and their heads
+};
+
+hipError_t launch_kv_plan(const PlanLaunch &a, hipStream_t st);
+hipError_t launch_kv_rope(const RopeLaunch &a, hipStream_t st);
 hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st);
 hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
