@@ -385,6 +385,27 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
                          const int32_t *idx, int32_t idx_k, const float *acc_in, float *acc_out,
                          int64_t ld, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* coli_kv_attn where groups of sequences begin with the same pages (a system
+ * prompt, the samples of one prompt): the pages that a group shares are read
+ * once for the query heads of all its sequences.  The same values as
+ * coli_kv_attn gives on the same cache, summed in another order.
+ *   group_start [n_groups+1] int32, ascending: group g is sequences
+ *     group_start[g] .. group_start[g+1]-1.  The groups cover the batch (the
+ *     first entry counts as 0, the last as B); 1 <= n_groups <= B
+ *   shared [B] int32: leading pages of the sequence's row of the table that it
+ *     has in common with its group, all of them full; the same for all
+ *     sequences of a group, 0 for a group that shares nothing (clamped to
+ *     [0, max_pages]).  They are read through the group's first row, whatever
+ *     that sequence's length.  A sequence that ends before them (an empty slot
+ *     among them) is taken by itself, through its own row
+ * No listed positions and no running weights.  ws:
+ * coli_kv_attn_shared_workspace_bytes(s, n_groups) bytes (0 for an invalid
+ * shape or number); calls that may run at the same time need one each. */
+size_t coli_kv_attn_shared_workspace_bytes(const coli_kv_shape *s, int32_t n_groups);
+coli_status coli_kv_attn_shared(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
+                                const int32_t *shared, const int32_t *group_start, int32_t n_groups, void *out,
+                                float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Eviction by accumulated attention weight: of each sequence b and cache head
  * h the k positions with the largest acc stay, by the rules of
  * coli_index_topk (the last min(tail, k) always, ties to the lower position),

@@ -23,6 +23,8 @@ The entry points keep the C names:
   coli_kv_attn_workspace_bytes(shape, idx_k=0, acc=False) -> int
   coli_kv_attn(shape, q, cache, out, scale, idx=None, acc_in=None, acc_out=None, lse=None, ws, stream=None)
   coli_kv_evict(shape, cache, acc, k, new_table, new_lens, kept, tail=0, new_acc=None, stream=None)
+  coli_kv_attn_shared_workspace_bytes(shape, n_groups) -> int
+  coli_kv_attn_shared(shape, q, cache, out, scale, shared, group_start, lse=None, ws, stream=None)
   coli_kv_plan(shape, table, lens, want, ring, state, start, slot, pos, shared=None, new_lens=None,
                new_state=None, stream=None)
   coli_rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, length=4096) -> (freq, amp)
@@ -54,6 +56,7 @@ EXPORTED = ("coli_moe_workspace_bytes", "coli_moe_route", "coli_moe_ffn", "coli_
             "coli_index_topk_workspace_bytes", "coli_index_topk", "coli_moe_ffn_noalloc",
             "coli_kv_append", "coli_kv_attn_workspace_bytes", "coli_kv_attn", "coli_kv_evict",
             "coli_kv_plan", "coli_rope_freqs", "coli_kv_rope",
+            "coli_kv_attn_shared_workspace_bytes", "coli_kv_attn_shared",
             "coli_moe_status_str", "coli_moe_version")
 ROUTE_STAGES = ("router", "topk", "perm")
 FFN_STAGES = ("gate_up", "down", "combine")
@@ -173,6 +176,10 @@ def lib():
         L.coli_kv_evict.argtypes = [kp, cp, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp]
         L.coli_kv_plan.restype = C.c_int
         L.coli_kv_plan.argtypes = [kp] + [vp] * 9 + [i32, vp, vp, vp]
+        L.coli_kv_attn_shared_workspace_bytes.restype = sz
+        L.coli_kv_attn_shared_workspace_bytes.argtypes = [kp, i32]
+        L.coli_kv_attn_shared.restype = C.c_int
+        L.coli_kv_attn_shared.argtypes = [kp, vp, cp, C.c_float, vp, vp, i32, vp, vp, vp, sz, vp]
         f64 = C.c_double
         L.coli_rope_freqs.restype = C.c_int
         L.coli_rope_freqs.argtypes = [i32, f64, i32, f64, f64, C.POINTER(f64), C.POINTER(C.c_float)]
@@ -565,6 +572,27 @@ def coli_kv_attn(shape: KvShape, q, cache: KvCache, out, scale: float, idx=None,
              _kv_arg(me, at, "idx", idx, torch.int32, (B, idx_k)), idx_k, _kv_arg(me, at, "acc_in", acc_in, f32, (B, H, ld)),
              _kv_arg(me, at, "acc_out", acc_out, f32, (B, H, ld)), ld, _kv_arg(me, at, "out", out, dt, (B, Hq, shape.Dv)),
              _kv_arg(me, at, "lse", lse, f32, (B, Hq)), _ptr(ws), _nbytes(ws, ws_bytes))
+
+
+def coli_kv_attn_shared_workspace_bytes(shape: KvShape, n_groups: int) -> int:
+    cs = shape.c()
+    return lib().coli_kv_attn_shared_workspace_bytes(C.byref(cs), n_groups)
+
+
+def coli_kv_attn_shared(shape: KvShape, q, cache: KvCache, out, scale: float, shared, group_start, lse=None, ws=None, ws_bytes=None,
+                        stream=None) -> None:
+    """q [B][Hq][Dk], out [B][Hq][Dv], lse fp32 [B][Hq], shared int32 [B], group_start int32 [n_groups + 1]."""
+    me = "coli_kv_attn_shared"
+    cs, cc, dt, at, torch = _kv_handles(me, shape, cache)
+    B, Hq, i32, groups = shape.B, shape.Hq, torch.int32, group_start.shape
+    if len(groups) != 1 or groups[0] < 1:
+        raise ValueError(f"{me}: group_start must have one dimension and at least one entry")
+    if ws is not None and ws.get_device() != at:
+        raise ValueError(f"{me}: ws is on {ws.device}, the cache on device {at}")
+    _kv_call(torch, me, at, stream, cs, _kv_arg(me, at, "q", q, dt, (B, Hq, shape.Dk)), cc, scale,
+             _kv_arg(me, at, "shared", shared, i32, (B,)), _kv_arg(me, at, "group_start", group_start, i32, groups), groups[0] - 1,
+             _kv_arg(me, at, "out", out, dt, (B, Hq, shape.Dv)), _kv_arg(me, at, "lse", lse, torch.float32, (B, Hq)), _ptr(ws),
+             _nbytes(ws, ws_bytes))
 
 
 def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_lens, kept, tail: int = 0, new_acc=None,

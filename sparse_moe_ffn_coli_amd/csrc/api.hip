@@ -218,6 +218,43 @@ AttnWs attn_ws(const coli_kv_shape *s, int32_t idx_k, bool acc, bool latent)
     return w;
 }
 
+struct SharedWs {
+    size_t own_o, own_ml, own_full, own_full_ml, pre_o, pre_ml, pre_full, pre_full_ml, total;
+    coli::SharedPlan plan;
+};
+
+SharedWs shared_ws(const coli_kv_shape *s, int32_t n_groups, bool latent)
+{
+    SharedWs w{};
+    w.plan = coli::attn_shared_plan(s->B, s->Hq, s->Hkv, s->Dk, s->Dv, s->dtype == COLI_BF16, latent, n_groups,
+                                    s->max_pages * s->page);
+    // parts of rows that are cut (two a range) and of those that are not (by query)
+    auto rows = [](const coli::AttnPlan &p) { return (size_t)2 * p.n_wg * p.tile_rows; };
+    const size_t heads = (size_t)s->B * s->Hq;
+    w.own_o = 0;
+    w.own_ml = align_up(w.own_o + rows(w.plan.own) * w.plan.own.out_cols * 4);
+    w.own_full = align_up(w.own_ml + rows(w.plan.own) * 8);
+    w.own_full_ml = align_up(w.own_full + heads * s->Dv * 4);
+    w.pre_o = align_up(w.own_full_ml + heads * 8);
+    w.pre_ml = align_up(w.pre_o + rows(w.plan.pre) * w.plan.pre.out_cols * 4);
+    w.pre_full = align_up(w.pre_ml + rows(w.plan.pre) * 8);
+    w.pre_full_ml = align_up(w.pre_full + heads * s->Dv * 4);
+    w.total = align_up(w.pre_full_ml + heads * 8);
+    if (w.total < 256) w.total = 256;
+    return w;
+}
+
+bool set_scale(coli::AttnLaunch &a, double sc)
+{
+    if (!(sc >= -3e38 && sc <= 3e38)) return false;
+    // scale * log2(e) as the sum of two floats, without the error that one
+    // rounded factor would put on every large score
+    a.scale_hi = (float)sc;
+    a.scale_lo = (float)(sc - (double)a.scale_hi);
+    a.scale_cap = (float)(3e38 / fmax(1.0, fabs((double)a.scale_lo)));
+    return true;
+}
+
 // Kind of memory behind a pointer: 1 device, 2 pinned (registered or
 // hipHostMalloc) host memory, 0 anything else (pageable host memory, or a
 // pointer the runtime does not know).
@@ -678,8 +715,8 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     coli_status st = check_kv_cache(s, c);
     if (st != COLI_OK) return st;
     const int32_t cap = s->max_pages * s->page;
-    const double sc = (double)scale * 1.4426950408889634074;     // exponents are taken to base 2
-    if (!(sc >= -3e38 && sc <= 3e38)) return COLI_E_SHAPE;
+    coli::AttnLaunch a{};
+    if (!set_scale(a, (double)scale * 1.4426950408889634074)) return COLI_E_SHAPE;     // exponents are taken to base 2
     if (idx ? (idx_k < 1 || idx_k > (1 << 24) || acc_out) : idx_k != 0) return COLI_E_SHAPE;
     if (kv_work(s, idx_k) > (1 << 28)) return COLI_E_SHAPE;
     if (acc_in && !acc_out) return COLI_E_NULL;
@@ -700,20 +737,14 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     if (any_overlap(outs, 4, ins, 7, acc_in == acc_out ? (const void *)acc_out : nullptr)) return COLI_E_ALIAS;
     if ((st = check_device()) != COLI_OK) return st;
 
-    coli::AttnLaunch a{};
     a.B = s->B; a.Hq = s->Hq; a.Hkv = s->Hkv; a.Dk = s->Dk; a.Dv = s->Dv;
     a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
     a.cap = cap;
     a.bf16 = s->dtype == COLI_BF16;
     a.q = q; a.k = c->k; a.v = c->v;
     a.table = c->table; a.lens = c->lens; a.idx = idx; a.idx_k = idx_k;
-    // scale * log2(e) as the sum of two floats, without the error that one
-    // rounded factor would put on every large score
-    a.scale_hi = (float)sc;
-    a.scale_lo = (float)(sc - (double)a.scale_hi);
-    a.scale_cap = (float)(3e38 / fmax(1.0, fabs((double)a.scale_lo)));
     a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
-    a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
+    a.tile_rows = L.plan.tile_rows; a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
     char *base = (char *)ws;
     a.part_o = (float *)(base + L.part_o);
     a.part_ml = (float *)(base + L.part_ml);
@@ -721,6 +752,61 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     a.scores = acc_out ? (float *)(base + L.scores) : nullptr;
     a.s_ld = L.s_ld;
     return coli::launch_attn(a, L.plan, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
+}
+
+size_t coli_kv_attn_shared_workspace_bytes(const coli_kv_shape *s, int32_t n_groups)
+{
+    const bool pair = check_kv_shape(s, false) == COLI_OK, latent = check_kv_shape(s, true) == COLI_OK;
+    if ((!pair && !latent) || n_groups < 0 || n_groups > s->B || (s->B > 0 && n_groups == 0)) return 0;
+    const size_t a = pair ? shared_ws(s, n_groups, false).total : 0;
+    const size_t b = latent ? shared_ws(s, n_groups, true).total : 0;
+    return a > b ? a : b;
+}
+
+coli_status coli_kv_attn_shared(const coli_kv_shape *s, const void *q, const coli_kv_cache *c, float scale,
+                                const int32_t *shared, const int32_t *group_start, int32_t n_groups, void *out,
+                                float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    coli_status st = check_kv_cache(s, c);
+    if (st != COLI_OK) return st;
+    coli::AttnLaunch a{};
+    if (!set_scale(a, (double)scale * 1.4426950408889634074)) return COLI_E_SHAPE;
+    if (n_groups < 0 || n_groups > s->B || (s->B > 0 && n_groups == 0)) return COLI_E_SHAPE;
+    if (s->B == 0) return check_device();
+    if (!q || !shared || !group_start || !out || !ws) return COLI_E_NULL;
+    if (!aligned16(q) || !aligned16(shared) || !aligned16(group_start) || !aligned16(out) || !aligned16(lse) || !aligned16(ws))
+        return COLI_E_ALIGN;
+    const SharedWs L = shared_ws(s, n_groups, !c->v);
+    if (ws_bytes < L.total) return COLI_E_WORKSPACE;
+    const size_t elt = kv_elt(s), pool = kv_pool_rows(s), heads = (size_t)s->B * s->Hq;
+    const Region outs[] = {{out, heads * s->Dv * elt}, {lse, heads * 4}, {ws, L.total}};
+    const Region ins[] = {{q, heads * s->Dk * elt}, {c->k, pool * s->Dk * elt}, {c->v, pool * s->Dv * elt},
+                          {c->table, (size_t)s->B * s->max_pages * 4}, {c->lens, (size_t)s->B * 4},
+                          {shared, (size_t)s->B * 4}, {group_start, ((size_t)n_groups + 1) * 4}};
+    if (any_overlap(outs, 3, ins, 7)) return COLI_E_ALIAS;
+    if ((st = check_device()) != COLI_OK) return st;
+
+    a.B = s->B; a.Hq = s->Hq; a.Hkv = s->Hkv; a.Dk = s->Dk; a.Dv = s->Dv;
+    a.page_shift = page_shift(s); a.n_pages = s->n_pages; a.max_pages = s->max_pages;
+    a.cap = s->max_pages * s->page;
+    a.bf16 = s->dtype == COLI_BF16;
+    a.q = q; a.k = c->k; a.v = c->v;
+    a.table = c->table; a.lens = c->lens;
+    a.shared = shared; a.group_start = group_start; a.n_groups = n_groups;
+    a.out = out; a.lse = lse;
+    char *base = (char *)ws;
+    coli::AttnLaunch pre = a;
+    auto part = [&](coli::AttnLaunch &x, const coli::AttnPlan &p, size_t o, size_t ml, size_t full, size_t full_ml) {
+        x.tile_rows = p.tile_rows; x.out_cols = p.out_cols; x.q_tiles = p.q_tiles;
+        x.n_wg = p.n_wg; x.min_units = p.min_units;
+        x.part_o = (float *)(base + o);
+        x.part_ml = (float *)(base + ml);
+        x.full_o = (float *)(base + full);
+        x.full_ml = (float *)(base + full_ml);
+    };
+    part(a, L.plan.own, L.own_o, L.own_ml, L.own_full, L.own_full_ml);
+    part(pre, L.plan.pre, L.pre_o, L.pre_ml, L.pre_full, L.pre_full_ml);
+    return coli::launch_attn_shared(a, pre, L.plan, (hipStream_t)stream) == hipSuccess ? COLI_OK : COLI_E_LAUNCH;
 }
 
 coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const float *acc, int64_t ld,

@@ -42,10 +42,48 @@ constexpr int KV_MAX_WG = 512;                // most ranges
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short bf16x8s __attribute__((ext_vector_type(8)));
 
-// Entries of sequence b: positions, or listed ones.
+// What a launch takes of the sequences: all positions; those behind the pages
+// that a sequence shares; or those pages, a group of sequences in the place of
+// a sequence and all its members' query heads in the place of one's.
+enum KvPart { KV_ALL, KV_OWN, KV_PREFIX };
+
+// Sequences of group g: the groups are a partition of the batch.
+__device__ __forceinline__ int kv_group_first(const AttnLaunch &a, int g) { return g <= 0 ? 0 : min(max(a.group_start[g], 0), a.B); }
+__device__ __forceinline__ int kv_group_end(const AttnLaunch &a, int g)
+{
+    return g + 1 >= a.n_groups ? a.B : min(max(a.group_start[g + 1], 0), a.B);
+}
+// Pages that sequence b shares with its group, and the ones that its own part
+// leaves to it: none where the sequence ends before them (it is then taken
+// whole as its own, and what the group finds for it does not count).
+__device__ __forceinline__ int kv_shared(const AttnLaunch &a, int b) { return min(max(a.shared[b], 0), a.max_pages); }
+__device__ __forceinline__ int kv_left(const AttnLaunch &a, int b)
+{
+    const int pages = kv_shared(a, b);
+    return min(max(a.lens[b], 0), a.cap) >= pages << a.page_shift ? pages : 0;
+}
+
+// Entries of sequence (or group) b: positions, or listed ones.
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ int kv_len(const AttnLaunch &a, int b)
 {
+    if constexpr (PART == KV_OWN) return min(max(a.lens[b], 0), a.cap) - (kv_left(a, b) << a.page_shift);
+    if constexpr (PART == KV_PREFIX) {
+        const int first = kv_group_first(a, b);
+        return first < kv_group_end(a, b) ? kv_shared(a, first) << a.page_shift : 0;
+    }
     return a.idx ? a.idx_k : min(max(a.lens[b], 0), a.cap);
+}
+
+// Sequences (or groups), and their rows: query tiles of all cache heads.
+template <KvPart PART>
+__device__ __forceinline__ int kv_items(const AttnLaunch &a) { return PART == KV_PREFIX ? a.n_groups : a.B; }
+template <KvPart PART>
+__device__ __forceinline__ int kv_tiles(const AttnLaunch &a, int b)
+{
+    if constexpr (PART != KV_PREFIX) return a.q_tiles;
+    const int queries = (kv_group_end(a, b) - kv_group_first(a, b)) * (a.Hq / a.Hkv);
+    return (queries + a.tile_rows - 1) / a.tile_rows;
 }
 __device__ __forceinline__ int kv_steps(int n) { return (n + KV_STEP - 1) / KV_STEP; }
 
@@ -60,10 +98,17 @@ __device__ __forceinline__ int kv_units(int n) { return (kv_steps(n) + KV_ROW_UN
 
 // Units of all sequences before b, and of all (per row of a sequence).  Every
 // wave computes it by itself: no barriers, and one load for up to 64
-// sequences.
+// sequences.  Of groups: the units of all their rows.
+template <KvPart PART = KV_ALL>
+__device__ __forceinline__ int kv_item_units(const AttnLaunch &a, int b)
+{
+    const int units = kv_units(kv_len<PART>(a, b));
+    return PART == KV_PREFIX ? units * a.Hkv * kv_tiles<PART>(a, b) : units;
+}
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int *before, int *total)
 {
-    if (a.idx) {
+    if (PART == KV_ALL && a.idx) {
         const int per = kv_units(a.idx_k);
         *before = b * per;
         *total = a.B * per;
@@ -71,8 +116,8 @@ __device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int *befor
     }
     const int lane = threadIdx.x & 63;
     int lo = 0, all = 0;
-    for (int i = lane; i < a.B; i += 64) {
-        const int st = kv_units(kv_len(a, i));
+    for (int i = lane; i < kv_items<PART>(a); i += 64) {
+        const int st = kv_item_units<PART>(a, i);
         all += st;
         lo += (i < b) ? st : 0;
     }
@@ -94,17 +139,19 @@ struct KvRange {
     int u, u_end, b, n, steps, row, s0;
 };
 
-// False: the range is empty.  R rows a sequence.  The same for every wave.
+// False: the range is empty.  R rows a sequence (groups: 1, their units are
+// all rows').  The same for every wave.
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg)
 {
     int before, total;
-    kv_prefix(a, 0, &before, &total);
+    kv_prefix<PART>(a, 0, &before, &total);
     total *= R;
     const int range = kv_range(a, total);
     const int u = blockIdx.x * range;         // below total + n_wg * (KV_ROW_UNITS + 1), and 2^31 by the host's check
     if (u >= total) return false;
     int base = 0;
-    if (a.idx) {
+    if (PART == KV_ALL && a.idx) {
         const int per = kv_units(a.idx_k) * R;
         rg.b = u / per;
         base = rg.b * per;
@@ -112,7 +159,7 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
         const int lane = threadIdx.x & 63;
         int sum = 0;                          // units (per row) before this chunk of sequences
         for (int c = 0;; c += 64) {
-            const int st = (c + lane < a.B) ? kv_units(kv_len(a, c + lane)) : 0;
+            const int st = (c + lane < kv_items<PART>(a)) ? kv_item_units<PART>(a, c + lane) : 0;
             const int incl = wave_scan_incl(st) + sum;
             const uint64_t here = __ballot(u < incl * R);
             if (here) {                       // the first lane that ends behind u (u < total: there is one)
@@ -126,7 +173,7 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
     }
     rg.u = u;
     rg.u_end = min(u + range, total);
-    rg.n = kv_len(a, rg.b);
+    rg.n = kv_len<PART>(a, rg.b);
     rg.steps = kv_steps(rg.n);
     const int per = kv_units(rg.n);
     rg.row = (u - base) / per;
@@ -135,12 +182,13 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
 }
 
 // A workgroup's range, or (direct) its row, which may be empty.
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ bool kv_begin(const AttnLaunch &a, int R, KvRange &rg)
 {
-    if (!a.direct) return kv_first(a, R, rg);
+    if (!a.direct) return kv_first<PART>(a, PART == KV_PREFIX ? 1 : R, rg);
     rg.b = blockIdx.x / R;
     rg.row = blockIdx.x - rg.b * R;
-    rg.n = kv_len(a, rg.b);
+    rg.n = kv_len<PART>(a, rg.b);
     rg.steps = kv_steps(rg.n);
     rg.u = rg.s0 = 0;
     rg.u_end = max(rg.steps, 1);
@@ -148,15 +196,37 @@ __device__ __forceinline__ bool kv_begin(const AttnLaunch &a, int R, KvRange &rg
 }
 
 // The next row of a range (past the last sequence: one that is never taken).
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, int &n, int &steps, int &row)
 {
-    if (++row < R) return;
+    if (++row < (PART == KV_PREFIX ? a.Hkv * kv_tiles<PART>(a, b) : R)) return;
     row = 0;
     do {
         ++b;
-        n = b < a.B ? kv_len(a, b) : 1;
+        n = b < kv_items<PART>(a) ? kv_len<PART>(a, b) : 1;
     } while (n == 0);
     steps = kv_steps(n);
+}
+
+// A row's query tile: cache head, the first of its queries and how many the
+// cache head has in all.  Query i of a cache head is row kv_query_row of q.
+struct KvTileOf {
+    int h, q0, queries;
+};
+template <KvPart PART = KV_ALL>
+__device__ __forceinline__ KvTileOf kv_tile_of(const AttnLaunch &a, int b, int row)
+{
+    const int tiles = kv_tiles<PART>(a, b), G = a.Hq / a.Hkv;
+    KvTileOf t;
+    t.h = tiles == 1 ? row : row / tiles;
+    t.q0 = (row - t.h * tiles) * a.tile_rows;
+    t.queries = PART == KV_PREFIX ? (kv_group_end(a, b) - kv_group_first(a, b)) * G : G;
+    return t;
+}
+__device__ __forceinline__ size_t kv_query_row(const AttnLaunch &a, int first, int h, int i)
+{
+    const int G = a.Hq / a.Hkv, x = i / G;
+    return (size_t)(first + x) * a.Hq + h * G + (i - x * G);
 }
 
 __device__ __forceinline__ int kv_pool_row(const AttnLaunch &a, int pg, int h, int p)
@@ -168,12 +238,21 @@ __device__ __forceinline__ int kv_pool_row(const AttnLaunch &a, int pg, int h, i
 // Pool row of entry e < end of sequence b's positions (of its list, where
 // there is one) for cache head h; -1: hidden.  No branches, and the table is
 // read before the length is known: its loads wait for nothing.
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ int kv_row(const AttnLaunch &a, int b, int h, int end, int len, int e)
 {
     int p = e;
-    if (a.idx) p = a.idx[(size_t)b * a.idx_k + min(e, a.idx_k - 1)];
-    const int at = min(max(p, 0), a.cap - 1);
-    const int pg = a.table[(size_t)b * a.max_pages + (at >> a.page_shift)];
+    if (PART == KV_ALL && a.idx) p = a.idx[(size_t)b * a.idx_k + min(e, a.idx_k - 1)];
+    int at = min(max(p, 0), a.cap - 1);
+    size_t entry;
+    if constexpr (PART == KV_ALL) {
+        entry = (size_t)b * a.max_pages + (at >> a.page_shift);
+    } else {
+        const int first = PART == KV_OWN ? kv_left(a, b) : 0;              // (of a row with entries: a page is left)
+        at = min(at, max(a.cap - (first << a.page_shift), 1) - 1);
+        entry = (size_t)(PART == KV_PREFIX ? kv_group_first(a, b) : b) * a.max_pages + first + (at >> a.page_shift);
+    }
+    const int pg = a.table[entry];
     const bool ok = e < end && p >= 0 && p < len && pg >= 0 && pg < a.n_pages;
     return ok ? kv_pool_row(a, pg, h, at) : -1;
 }
@@ -268,7 +347,9 @@ __device__ __forceinline__ void kv_write_empty(const AttnLaunch &a, size_t qrow,
 }
 
 // NW waves; `a.direct`: a workgroup per row, none of them cut.
-template <bool BF16, int DK, int DV, int NW>
+// PART other than KV_ALL: rows that are not cut are left as parts too, by their
+// queries (a.full_o, a.full_ml).
+template <bool BF16, int DK, int DV, int NW, KvPart PART = KV_ALL>
 __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
 {
     using KT = KvTile<BF16, DK, DV>;
@@ -294,7 +375,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     const int R = a.Hkv * a.q_tiles;
 
     KvRange rg;
-    if (!kv_begin(a, R, rg)) return;
+    if (!kv_begin<PART>(a, R, rg)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
 
@@ -303,16 +384,27 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     const int vstride = a.v ? a.Dv : a.Dk;
     const int key_chunks = (a.Dk + 4 * EPL - 1) / (4 * EPL), full_chunks = a.Dk / (4 * EPL);
 
-    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row(a, R, b, n, steps, row)) {
+    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row<PART>(a, R, b, n, steps, row)) {
         const int s1 = min(steps, s0 + (u_end - u));
-        const int h = a.q_tiles == 1 ? row : row / a.q_tiles, q0 = (row - h * a.q_tiles) * KV_QT;
-        const int nq = min(KV_QT, G - q0);    // query heads of this tile
+        int h, q0, nq;                        // (nq: query heads of this tile)
+        if constexpr (PART == KV_PREFIX) {
+            const KvTileOf t = kv_tile_of<PART>(a, b, row);
+            h = t.h, q0 = t.q0, nq = min(KV_QT, t.queries - q0);
+        } else {
+            h = a.q_tiles == 1 ? row : row / a.q_tiles, q0 = (row - h * a.q_tiles) * KV_QT;
+            nq = min(KV_QT, G - q0);
+        }
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
         if (s0 >= steps) {                    // a row's units past its steps, or (direct) an empty row
-            if (a.direct) return kv_write_empty(a, qrow, nq);
+            if (a.direct) {
+                if (PART == KV_ALL) kv_write_empty(a, qrow, nq);
+                return;
+            }
             continue;
         }
-        const int len = min(max(a.lens[b], 0), a.cap);
+        const int len = PART == KV_ALL ? min(max(a.lens[b], 0), a.cap) : n;
+        size_t query = qrow + j;              // the lane's
+        if constexpr (PART == KV_PREFIX) query = kv_query_row(a, kv_group_first(a, b), h, q0 + min(j, nq - 1));
 
         // the query tile: lane (j, g) holds query j's elements as a key's
         u32x4 qf[KC];
@@ -321,7 +413,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
             const int d = (4 * c + g) * EPL;
             qf[c] = u32x4{0, 0, 0, 0};
             if (j < nq && d < a.Dk)
-                qf[c] = *reinterpret_cast<const u32x4 *>((const T *)a.q + (qrow + j) * a.Dk + d);
+                qf[c] = *reinterpret_cast<const u32x4 *>((const T *)a.q + query * a.Dk + d);
         }
         f32x4 o[VC][VE];
 #pragma unroll
@@ -332,7 +424,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
 
         // pool row of position `lane & 31` of step s (-1: hidden)
         const int end = min(n, s1 * KV_STEP);
-        auto rows_of = [&](int s) { return kv_row(a, b, h, end, len, s * KV_STEP + (lane & 31)); };
+        auto rows_of = [&](int s) { return kv_row<PART>(a, b, h, end, len, s * KV_STEP + (lane & 31)); };
         u32x4 kf[2][BIG ? 2 * KP : KC];
         auto load_keys = [&](int rows, int c0 = 0) {      // (BIG: KP chunks from c0 on, into their half of the buffer)
 #pragma unroll
@@ -443,7 +535,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
                 for (int i = 0; i < 8; ++i)
                     if (__shfl(rows_now, 16 * (i >> 2) + 4 * g + (i & 3)) < 0) t2[i] = -INFINITY;
             }
-            if (a.scores) {
+            if (PART == KV_ALL && a.scores) {
                 // raw scores for the running weights (query j's row)
                 if (j < nq) {
                     float *dst = a.scores + (qrow + j) * a.s_ld + s * KV_STEP + 4 * g;
@@ -548,7 +640,14 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
                 lq += red_l[w][q] * f;
                 v += *reinterpret_cast<const f32x4 *>(&red[w][q][d]) * f;
             }
-            if (whole) {
+            if (PART != KV_ALL && whole) {
+                const size_t at = PART == KV_PREFIX ? kv_query_row(a, kv_group_first(a, b), h, q0 + q) : qrow + q;
+                *reinterpret_cast<f32x4 *>(a.full_o + at * a.Dv + d) = v;
+                if (d == 0) {
+                    a.full_ml[2 * at] = mq;
+                    a.full_ml[2 * at + 1] = lq;
+                }
+            } else if (whole) {
                 const float inv = kv_inverse(lq);
                 const size_t at = (qrow + q) * a.Dv + d;
                 if constexpr (BF16)
@@ -576,15 +675,18 @@ struct KvParts {
     int steps, w0, w1, first;
     __device__ __forceinline__ int slot(int w) const { return w == w0 ? first : 2 * w; }
 };
+template <KvPart PART = KV_ALL>
 __device__ __forceinline__ KvParts kv_parts(const AttnLaunch &a, int b, int row, int before, int total)
 {
-    const int R = a.Hkv * a.q_tiles, n = kv_len(a, b);
+    const int R = PART == KV_PREFIX ? 1 : a.Hkv * a.q_tiles, n = kv_len<PART>(a, b);
     KvParts p{kv_steps(n), 0, 0, 0};
     if (p.steps == 0) return p;
     const int range = kv_range(a, total * R);
     const int u0 = before * R + row * kv_units(n);
     p.w0 = u0 / range;
     p.w1 = (u0 + p.steps - 1) / range;
+    // (groups that are no partition have sums past every range)
+    if constexpr (PART == KV_PREFIX) p.w0 = min(max(p.w0, 0), a.n_wg - 1), p.w1 = min(max(p.w1, p.w0), a.n_wg - 1);
     p.first = 2 * p.w0 + (u0 == p.w0 * range ? 0 : 1);
     return p;
 }
@@ -687,7 +789,7 @@ __device__ __forceinline__ void kw_mfma_v(f32x16 &d, bf16x8 a, bf16x8 b)
 // 512 positions, 512 elements, 16 heads: 24.0 us with the tail so, 25.0 with
 // both).
 enum KwPast { KW_NONE, KW_TAIL, KW_BOTH };
-template <int DK, int DV, int WQ, KwPast PAST>
+template <int DK, int DV, int WQ, KwPast PAST, KvPart PART = KV_ALL>
 __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_kernel(AttnLaunch a)
 {
     constexpr int WK = KV_WAVES / WQ;
@@ -714,7 +816,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     const int G = a.Hq / a.Hkv;
     const int R = a.Hkv * a.q_tiles;
     KvRange rg;
-    if (!kv_first(a, R, rg)) return;
+    if (!kv_first<PART>(a, PART == KV_PREFIX ? 1 : R, rg)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const char *pool = (const char *)a.k;
@@ -726,7 +828,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
     auto advance = [&] {
         u += kv_units(n) - s0;
         s0 = 0;
-        kv_next_row(a, R, b, n, steps, row);
+        kv_next_row<PART>(a, R, b, n, steps, row);
     };
     for (; u < u_end; again ? (void)0 : advance()) {
         const int s1 = min(steps, s0 + (u_end - u));
@@ -747,10 +849,16 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         const int rr = (lane & 15) >> 2;
         const int val_at = (4 * hi + rr) * (RA * 16) + (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ (rr << 2) ^ hi) << 4) +
                            (lane & 1) * 8;
-        const int h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
-        const int nq = G - q0;                // query heads of this wave's tile (may be none)
+        int h, q0, nq;                        // (nq: query heads of this wave's tile, may be none)
+        if constexpr (PART == KV_PREFIX) {
+            const KvTileOf t = kv_tile_of<PART>(a, b, row);
+            h = t.h, q0 = t.q0 + 32 * qt, nq = t.queries - q0;
+        } else {
+            h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;
+            nq = G - q0;
+        }
         const size_t qrow = (size_t)b * a.Hq + h * G + q0;
-        const int len = min(max(a.lens[b], 0), a.cap);
+        const int len = PART == KV_ALL ? min(max(a.lens[b], 0), a.cap) : n;
         const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
 
         f32x16 o[DT];
@@ -764,12 +872,16 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
 #pragma unroll
             for (int x = 0; x < PER; ++x) {   // no branches: all loads of a kind in flight together
                 const int e = first + x * KV_NT;
-                p[x] = a.idx ? a.idx[(size_t)b * a.idx_k + min(e, n - 1)] : e;
+                p[x] = PART == KV_ALL && a.idx ? a.idx[(size_t)b * a.idx_k + min(e, n - 1)] : e;
                 p[x] = (e < end && p[x] >= 0 && p[x] < len) ? p[x] : -1;
             }
             int pg[PER];
 #pragma unroll
-            for (int x = 0; x < PER; ++x) pg[x] = a.table[(size_t)b * a.max_pages + (max(p[x], 0) >> a.page_shift)];
+            for (int x = 0; x < PER; ++x) {
+                size_t entry = (size_t)(PART == KV_PREFIX ? kv_group_first(a, b) : b) * a.max_pages + (max(p[x], 0) >> a.page_shift);
+                if constexpr (PART == KV_OWN) entry += kv_left(a, b);
+                pg[x] = a.table[entry];
+            }
 #pragma unroll
             for (int x = 0; x < PER; ++x)
                 rows_s[tid + x * KV_NT] =
@@ -835,7 +947,9 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         // score operand.
         bf16x8 qf[KS];
         {
-            const uint64_t rows = ql < nq ? (uint64_t)a.q + (qrow + ql) * row_bytes : (uint64_t)kv_zeros;
+            size_t query = qrow + ql;
+            if constexpr (PART == KV_PREFIX) query = kv_query_row(a, kv_group_first(a, b), h, min(q0 + ql, q0 + max(nq, 1) - 1));
+            const uint64_t rows = ql < nq ? (uint64_t)a.q + query * row_bytes : (uint64_t)kv_zeros;
             const uint32_t dst = ring_at + qt * STAGE;
             auto bring = [&](int r, uint32_t off, uint32_t to) {
                 const uint64_t src = (uint64_t)__shfl((unsigned long long)rows, r);
@@ -954,7 +1068,7 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                     for (int i = 0; i < 16; ++i)
                         if (hid >> (8 * (i >> 2) + (i & 3)) & 1) w[i] = -INFINITY;
                 }
-                if (a.scores && ql < nq && t < seg) {
+                if (PART == KV_ALL && a.scores && ql < nq && t < seg) {
                     float *dst = a.scores + (qrow + ql) * a.s_ld + (s0 + t) * KV_STEP + 4 * hi;
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -1047,9 +1161,14 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
         const size_t slot = (size_t)(2 * blockIdx.x + (u == u_begin ? 0 : 1)) * WQ + qt;
         f32x4 *part = reinterpret_cast<f32x4 *>(a.part_o + slot * OUT) + lane;
         uint16_t *out = (uint16_t *)a.out + (qrow + ql) * a.Dv;
+        size_t query = qrow + ql;             // (groups: a row past the tile's queries is not written)
+        if constexpr (PART == KV_PREFIX) query = kv_query_row(a, kv_group_first(a, b), h, q0 + ql);
+        float *full = PART == KV_ALL ? nullptr : a.full_o + query * a.Dv;
         auto put = [&](int x, int i, f32x4 v) {
             if (!whole) {                     // a part: lanes side by side (attn_wide_join_kernel reads it the same way)
                 part[(x * 4 + i) * 64] = v;
+            } else if (PART != KV_ALL) {
+                if (ql < nq && 32 * x + 8 * i + 4 * hi < a.Dv) *reinterpret_cast<f32x4 *>(full + 32 * x + 8 * i + 4 * hi) = v;
             } else if (ql < nq && 32 * x + 8 * i + 4 * hi < a.Dv) {  // Dv is a multiple of 8: all four columns or none
                 *reinterpret_cast<u32x2 *>(out + 32 * x + 8 * i + 4 * hi) =
                     u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
@@ -1110,7 +1229,8 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                 a.part_ml[(slot * 32 + ql) * 2] = ma;
                 a.part_ml[(slot * 32 + ql) * 2 + 1] = la;
             } else if (ql < nq) {
-                kv_write_stats(a, qrow + ql, ma, la);
+                if constexpr (PART == KV_ALL) kv_write_stats(a, qrow + ql, ma, la);
+                else a.full_ml[2 * query] = ma, a.full_ml[2 * query + 1] = la;
             }
         }
         again = false;
@@ -1128,6 +1248,10 @@ __global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) v
                             const f32x4 v = part[(x * 4 + i) * 64];
 #pragma unroll
                             for (int c = 0; c < 4; ++c) bad |= !(fabsf(v[c]) < INFINITY);
+                        } else if (PART != KV_ALL) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                bad |= 32 * x + 8 * i + 4 * hi < a.Dv && !(fabsf(full[32 * x + 8 * i + 4 * hi + c]) < INFINITY);
                         } else if (32 * x + 8 * i + 4 * hi < a.Dv) {
                             const u32x2 v = *reinterpret_cast<const u32x2 *>(out + 32 * x + 8 * i + 4 * hi);
 #pragma unroll

@@ -1,5 +1,6 @@
 // kernels.h -- internal launch interface between the C ABI (api.hip) and the
-// kernels (route.hip, ffn.hip, select.hip, attend.hip, kvcache.hip, plan.hip, rope.hip).  Not part of the public interface.
+// kernels (route.hip, ffn.hip, select.hip, attend.hip, shared.hip, kvcache.hip,
+// plan.hip, rope.hip).  Not part of the public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,7 +77,7 @@ struct AttnLaunch {
     const float *acc_in;
     float *acc_out;        // nullable
     long ld;
-    int q_tiles;           // query tiles per cache head
+    int q_tiles;           // query tiles per cache head (of groups: each has its own number)
     bool direct;           // a workgroup per row
     int n_wg, min_units;   // ranges of the main kernel (direct: rows); fewest steps in one
     float *part_o;         // workspace [2 n_wg][tile rows][Dv]: unnormalised parts
@@ -84,6 +85,13 @@ struct AttnLaunch {
     float *stats;          // workspace [B][Hq][2]: reference and 1 / sum (running weights only)
     float *scores;         // workspace [B][Hq][s_ld]: scores in units of log2 e (running weights only)
     long s_ld;
+    // calls with shared pages only
+    const int32_t *shared, *group_start;   // groups of sequences that share their first pages
+    int n_groups;
+    int tile_rows;         // query heads of a tile
+    int out_cols;          // columns of a part's rows
+    float *full_o;         // workspace [B][Hq][Dv]: unnormalised outputs of rows that are not cut
+    float *full_ml;        // workspace [B][Hq][2]
 };
 
 // Which kernel an attention call takes and how its workspace is laid out.
@@ -95,6 +103,11 @@ struct AttnPlan {
     int tier, waves;       // the other kernels' width and waves per workgroup
     bool direct;           // a workgroup per row, no parts
     int n_wg, min_units;
+};
+
+// The two parts of a call with shared pages.
+struct SharedPlan {
+    AttnPlan own, pre;
 };
 
 struct AppendLaunch {
@@ -154,6 +167,8 @@ struct RopeLaunch {
 hipError_t launch_kv_plan(const PlanLaunch &a, hipStream_t st);
 hipError_t launch_kv_rope(const RopeLaunch &a, hipStream_t st);
 hipError_t launch_attn(const AttnLaunch &a, const AttnPlan &p, hipStream_t st);
+hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, const SharedPlan &p, hipStream_t st);
+SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int n_groups, int entries);
 hipError_t launch_kv_append(const AppendLaunch &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictLaunch &a, hipStream_t st);
 AttnPlan attn_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int entries);

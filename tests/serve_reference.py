@@ -77,3 +77,27 @@ def norm_rope(x, w, eps, pos, freq, rot_at, interleaved, amp, bf16):
 
 def to_np(t):
     return t.detach().cpu().to(torch.float64).numpy()
+
+
+def make_shared(groups, Hkv, Dk, Dv, page, dtype="bf16", latent=False, seed=0):
+    """A cache for kv_reference.attn whose sequences share pages: groups [(pages, [positions behind them])].  A value of
+    (n,) in place of a number: a sequence of n positions all in all, within its group's pages."""
+    import kv_reference as kv
+    tails = [t for _, ts in groups for t in ts]
+    own = [0 if isinstance(t, tuple) else t for t in tails]
+    c = kv.make_cache([p * page for p, _ in groups] + own, Hkv, Dk, Dv, page, dtype, latent, seed=seed)
+    G, table = len(groups), c["table"].numpy()
+    shared = np.repeat([p for p, _ in groups], [len(ts) for _, ts in groups]).astype(np.int32)
+    group = np.repeat(np.arange(G), [len(ts) for _, ts in groups])
+    mp = max(int(s) + -(-t // page) for s, t in zip(shared, own)) + 1
+    mp = max(mp, 1)
+    new = np.full((len(tails), mp), -1, np.int32)
+    lens = np.zeros(len(tails), np.int32)
+    for b, t in enumerate(tails):
+        new[b, :shared[b]] = table[group[b], :shared[b]]
+        n = -(-own[b] // page)
+        new[b, shared[b]:shared[b] + n] = table[G + b, :n]
+        lens[b] = t[0] if isinstance(t, tuple) else shared[b] * page + t
+    c.update(table=torch.from_numpy(new), lens=torch.from_numpy(lens), max_pages=mp, shared=torch.from_numpy(shared),
+             group_start=torch.from_numpy(np.concatenate([[0], np.cumsum([len(ts) for _, ts in groups])]).astype(np.int32)))
+    return c

@@ -102,6 +102,36 @@ def test_rope_refusals():
     assert rope(q_out=fake(11)) == E_ALIAS and rope(pool_v=fake(8)) == E_ALIAS and rope(q_out=fake(7)) == E_ALIAS
 
 
+def attend(s=None, c=None, q=fake(5), scale=0.1, shared=fake(20), start=fake(21), groups=2, out=fake(6), lse=None, ws=fake(7), ws_bytes=1 << 40):
+    cs = (s or shape()).c()
+    cc = c or pkg.CKvCache(k=fake(1), v=fake(2), table=fake(3), lens=fake(4))
+    return pkg.lib().coli_kv_attn_shared(C.byref(cs), q, C.byref(cc), scale, shared, start, groups, out, lse, ws, ws_bytes, None)
+
+
+@no_gpu
+def test_shared_attention_refusals():
+    assert attend() == E_DEVICE and attend(lse=fake(22)) == E_DEVICE
+    for k in ("q", "shared", "start", "out", "ws"):
+        assert attend(**{k: None}) == E_NULL, k
+        assert attend(**{k: fake(30, 4)}) == E_ALIGN, k
+    assert attend(lse=fake(30, 4)) == E_ALIGN
+    assert attend(groups=0) == E_SHAPE and attend(groups=5) == E_SHAPE and attend(groups=-1) == E_SHAPE and attend(groups=4) == E_DEVICE
+    assert attend(shape(B=0), groups=0, q=None) == E_DEVICE
+    for bad in (math.nan, math.inf, 3.4e38):
+        assert attend(scale=bad) == E_SHAPE
+    for kw in (dict(Hq=33), dict(Dk=264), dict(page=24), dict(B=1 << 20, max_pages=1 << 12)):
+        assert attend(shape(**kw)) == E_SHAPE and pkg.coli_kv_attn_shared_workspace_bytes(shape(**kw), 1) == 0, kw
+    assert attend(shape(dtype=5)) == E_DTYPE
+    lat = pkg.CKvCache(k=fake(1), v=None, table=fake(3), lens=fake(4))
+    assert attend(shape(Hkv=1, Dk=576, Dv=512), lat) == E_DEVICE and attend(shape(Hkv=1, Dk=576, Dv=512)) == E_SHAPE
+    need = pkg.coli_kv_attn_shared_workspace_bytes(shape(), 2)
+    assert need > 0 and attend(ws_bytes=need - 1) == E_WS and attend(ws_bytes=need) == E_DEVICE
+    assert pkg.coli_kv_attn_shared_workspace_bytes(shape(), 0) == 0 == pkg.coli_kv_attn_shared_workspace_bytes(shape(), 5)
+    assert pkg.coli_kv_attn_shared_workspace_bytes(shape(B=0), 0) > 0
+    for other in (dict(q=fake(6)), dict(shared=fake(6)), dict(start=fake(7)), dict(lse=fake(6)), dict(out=fake(1)), dict(ws=fake(3)), dict(lse=fake(4))):
+        assert attend(**other) == E_ALIAS, other
+
+
 @no_gpu
 def test_the_binding_takes_gpu_tensors_only():
     i = torch.zeros(64, dtype=torch.int32)
