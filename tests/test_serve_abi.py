@@ -119,7 +119,7 @@ def test_shared_attention_refusals():
     assert attend(shape(B=0), groups=0, q=None) == E_DEVICE
     for bad in (math.nan, math.inf, 3.4e38):
         assert attend(scale=bad) == E_SHAPE
-    for kw in (dict(Hq=33), dict(Dk=264), dict(page=24), dict(B=1 << 20, max_pages=1 << 12)):
+    for kw in (dict(Hq=33), dict(Dk=600), dict(page=24), dict(B=1 << 20, max_pages=1 << 12)):
         assert attend(shape(**kw)) == E_SHAPE and pkg.coli_kv_attn_shared_workspace_bytes(shape(**kw), 1) == 0, kw
     assert attend(shape(dtype=5)) == E_DTYPE
     lat = pkg.CKvCache(k=fake(1), v=None, table=fake(3), lens=fake(4))
