@@ -14,6 +14,252 @@
 
 namespace coli {
 
+// ---- shared pages of many query heads ------------------------------------------
+// With 64 sequences of four query heads a cache head meets 256 queries: 128
+// products a byte of the cache, so the matrix cores bind and not HBM.  Each
+// key and value is brought into LDS once per workgroup (copies that pass no
+// registers, a ring of 32-position stages), every wave takes 32 queries on
+// 32 x 32 x 16 matrix tiles, as the wide latent kernel does:
+//   scores  D[key][query] = K Q^T
+//   output  O^T[column][query] += V^T w   (values by the transposing LDS read)
+// Eight waves (four where rows are 256 wide: twice the registers), two a SIMD:
+// one's softmax runs while the other multiplies.  WQ of them have different
+// queries; the waves of a query tile split the positions, NW / WQ stages a
+// round, and are joined in LDS at the end of a row.
+// LDS rows are RK or RV chunks of 16 bytes (a power of two), chunk c of row r
+// at c XOR kp_swz(r): 16 rows of one chunk (scores) and 4 rows of 4 chunks
+// (output) fall in distinct banks.
+constexpr int KP_BLOCK = 32;                  // stages whose rows are looked up at a time
+
+template <int R>
+__device__ __forceinline__ int kp_swz(int row)
+{
+    if constexpr (R == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);      // two rows to a bank round
+    else return kw_swz(row);
+}
+constexpr int kp_chunks(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
+
+template <int DK, int DV, int WQ, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attn_prefix_kernel(AttnLaunch a)
+{
+    constexpr int WK = NW / WQ;
+    constexpr int RK = kp_chunks(DK), RV = kp_chunks(DV);
+    constexpr int KB = KW_ROWS * RK * 16, STAGE = KB + KW_ROWS * RV * 16;         // bytes of a stage's keys, and of all
+    constexpr int CK = RK / 2, CPS = CK + RV / 2;             // copy instructions of a stage
+    constexpr int CPW = CPS * WK / NW;                        // of a wave in a round
+    constexpr int OUT = 32 * DV;                              // floats of a query tile's output
+    constexpr int RING = 147456 / STAGE < 8 ? 147456 / STAGE : 8;                 // stages in LDS; a row's outputs fit too
+    constexpr int AHEAD = RING / WK - 1;                      // rounds in flight beside the one computed
+    constexpr int KS = DK / 16, DT = DV / 32;
+    static_assert(CPS * WK % NW == 0 && AHEAD >= 1 && (AHEAD - 1) * CPW < 64, "copies of a round");
+    static_assert(NW * OUT * 4 <= RING * STAGE, "outputs of all waves");
+    __shared__ __attribute__((aligned(256))) char ring[RING * STAGE];
+    __shared__ int32_t rows_s[2][KP_BLOCK * KW_ROWS];         // pool rows of the stages' positions, -1: hidden
+    __shared__ float red_m[NW][32], red_l[NW][32];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int qt = wave % WQ, kb = wave / WQ;
+    const int ql = lane & 31, hi = lane >> 5;
+    KvRange rg;
+    if (!kv_first<KV_PREFIX>(a, 1, rg)) return;
+    int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
+    const int u_begin = u, u_end = rg.u_end;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
+    const uint64_t kpool = (uint64_t)a.k, vpool = (uint64_t)(a.v ? a.v : a.k);
+    const uint32_t k_bytes = a.Dk * 2, v_bytes = a.v ? a.Dv * 2 : k_bytes;        // from a row to the next
+
+    // this lane's places in a stage: key row ql, chunk hi; and the transposing reads' rows 4 hi + rr, of whose columns
+    // bit 4 of the lane gives the sixteen
+    const int key_at = ql * (RK * 16) + ((hi ^ kp_swz<RK>(ql)) << 4);
+    const int rr = (lane & 15) >> 2;
+    const int val_at = KB + (4 * hi + rr) * (RV * 16) +
+                       (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ kp_swz<RV>(4 * hi + rr)) << 4) + (lane & 1) * 8;
+
+    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row<KV_PREFIX>(a, 1, b, n, steps, row)) {
+        const int s1 = min(steps, s0 + (u_end - u));
+        if (s0 >= steps) continue;            // a row's units past its steps
+        const KvTileOf tile = kv_tile_of<KV_PREFIX>(a, b, row);
+        const int first = kv_group_first(a, b), h = tile.h, q0 = tile.q0 + 32 * qt;
+        const int nq = tile.queries - q0;     // query heads of this wave's tile (may be none)
+        const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
+
+        bf16x8 qf[KS];
+        {
+            const uint16_t *q = (const uint16_t *)a.q + kv_query_row(a, first, h, q0 + min(ql, max(nq, 1) - 1)) * a.Dk;
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+                const int d = 16 * c + 8 * hi;
+                qf[c] = bf16x8{};
+                if (ql < nq && d < a.Dk) qf[c] = *reinterpret_cast<const bf16x8 *>(q + d);
+            }
+        }
+        // pool rows of the block of stages that holds stage t0 (a multiple of KP_BLOCK)
+        auto look_up = [&](int t0) {
+            constexpr int PER = KP_BLOCK * KW_ROWS / (64 * NW);
+            const int end = min(n, s1 * KV_STEP);
+            int p[PER], pg[PER];
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                p[x] = (s0 + t0) * KV_STEP + tid + x * (64 * NW);
+                pg[x] = a.table[(size_t)first * a.max_pages + (min(p[x], end - 1) >> a.page_shift)];
+            }
+#pragma unroll
+            for (int x = 0; x < PER; ++x)
+                rows_s[(t0 / KP_BLOCK) & 1][tid + x * (64 * NW)] =
+                    p[x] < end && pg[x] >= 0 && pg[x] < a.n_pages ? kv_pool_row(a, pg[x], h, p[x]) : -1;
+        };
+        // the wave's copies of round r
+        auto issue = [&](int r) {
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) {
+                const int j = wave + x * NW, t = r * WK + j / CPS, i = j % CPS;
+                const bool key = i < CK;
+                const int32_t *rows = rows_s[(t / KP_BLOCK) & 1] + (t % KP_BLOCK) * KW_ROWS;
+                const uint32_t dst = ring_at + (t % RING) * STAGE;
+                auto copy = [&](auto chunks, int i, uint64_t pool, uint32_t bytes, uint32_t width, uint32_t dst) {
+                    constexpr int R = decltype(chunks)::value;
+                    const int at = i * (64 / R) + lane / R;
+                    const uint32_t off = ((lane % R) ^ kp_swz<R>(at)) << 4;
+                    const int from = rows[at];
+                    kw_copy(from >= 0 && off < width ? pool + (uint64_t)(uint32_t)from * bytes + off : (uint64_t)kv_zeros, dst + i * 1024);
+                };
+                if (key) copy(KwInt<RK>{}, i, kpool, k_bytes, k_bytes, dst);
+                else copy(KwInt<RV>{}, i - CK, vpool, v_bytes, a.Dv * 2, dst + KB);
+            }
+        };
+
+        f32x16 o[DT];
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+        float m = -INFINITY, l = 0.f;
+        look_up(0);
+        kw_barrier();
+#pragma unroll 1
+        for (int r = 0; r < AHEAD; ++r) issue(r);
+        for (int r = 0; r < rounds; ++r) {
+            // this wave's copies of round r have landed, then everyone's; round r - 1 is done with its stages
+            kw_wait_copies<(AHEAD - 1) * CPW>();
+            kw_barrier();
+            const int ahead = (r + AHEAD) * WK;
+            if (ahead % KP_BLOCK == 0) {
+                look_up(ahead);
+                kw_barrier();
+            }
+            issue(r + AHEAD);
+            const int t = r * WK + kb;
+            const char *st = ring + (t % RING) * STAGE;
+            const uint32_t hid = (uint32_t)__ballot(rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + ql] < 0) >> (4 * hi);
+
+            // ---- scores ----
+            f32x16 sc;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(st + (key_at ^ (32 * (c & 7))) + (c >> 3) * 256);
+                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[c], sc, 0, 0, 0);
+            }
+            // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = kv_scaled(a, sc[i]);
+            if (__ballot(hid != 0)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (hid >> (8 * (i >> 2) + (i & 3)) & 1) w[i] = -INFINITY;
+            }
+            float mx = w[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, w[i]);
+            // The reference moves only when a score passes it by 2^8: weights
+            // stay below 256 and the sums far inside fp32.
+            if (__ballot(mx > m + 8.f)) {
+                const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
+                const float f = (mn == -INFINITY) ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) o[t] *= f;
+            }
+            const float ref = (m == -INFINITY) ? 0.f : m;
+            // each weight as two bf16 parts: 16 bits of it enter the products
+            u32x4 whi[2], wlo[2];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float w0 = __builtin_amdgcn_exp2f(w[i] - ref), w1 = __builtin_amdgcn_exp2f(w[i + 1] - ref);
+                l += w0;
+                l += w1;
+                const uint32_t p = pack_bf16(w0, w1);
+                whi[i / 8][i / 2 % 4] = p;
+                wlo[i / 8][i / 2 % 4] = pack_bf16(w0 - __uint_as_float(p << 16), w1 - __uint_as_float(p & 0xffff0000u));
+            }
+            // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further ----
+#pragma unroll
+            for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    s16x4 half[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        // row 8 y further: the swizzle's second bit; column tile x: four chunks each
+                        const int at = (val_at ^ (32 * y) ^ (64 * (x & 3))) + (x >> 2) * 256 + (16 * ks + 8 * y) * (RV * 16);
+                        half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
+                    }
+                    const bf16x8 vb = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(whi[ks]), o[x], 0, 0, 0);
+                    o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(wlo[ks]), o[x], 0, 0, 0);
+                }
+        }
+        kw_wait_copies<0>();                  // stages past the row's end are copied too, as zeros
+        kw_barrier();
+
+        // ---- the waves of a query tile become one: outputs side by side in LDS, 16-byte chunk c of query q at c XOR q ----
+        l += __shfl_xor(l, 32);
+        if (hi == 0) {
+            red_m[wave][ql] = m;
+            red_l[wave][ql] = l;
+        }
+        constexpr int QC = DV / 4;            // chunks of a query's output
+        f32x4 *buf = reinterpret_cast<f32x4 *>(ring);
+#pragma unroll
+        for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                buf[(wave * 32 + ql) * QC + ((8 * x + 2 * i + hi) ^ (ql & (QC - 1)))] =
+                    f32x4{o[x][4 * i], o[x][4 * i + 1], o[x][4 * i + 2], o[x][4 * i + 3]};
+        kw_barrier();
+        const bool whole = s0 == 0 && s1 == steps;
+        const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+        const int live = min(32 * WQ, tile.queries - tile.q0);
+        for (int i = tid; i < live * QC; i += 64 * NW) {
+            const int q = i / QC, c = i % QC, qi = q & 31;
+            if (4 * c >= a.Dv) continue;
+            float mq = red_m[q >> 5][qi], lq = 0.f;
+#pragma unroll
+            for (int x = 1; x < WK; ++x) mq = fmaxf(mq, red_m[x * WQ + (q >> 5)][qi]);
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < WK; ++x) {
+                const int wv = x * WQ + (q >> 5);
+                const float f = red_m[wv][qi] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(red_m[wv][qi] - mq);
+                lq += red_l[wv][qi] * f;
+                v += buf[(wv * 32 + qi) * QC + (c ^ (qi & (QC - 1)))] * f;
+            }
+            const size_t at = whole ? kv_query_row(a, first, h, tile.q0 + q) : (size_t)slot * a.tile_rows + q;
+            float *ml = whole ? a.full_ml : a.part_ml;
+            *reinterpret_cast<f32x4 *>((whole ? a.full_o : a.part_o) + at * a.Dv + 4 * c) = v;
+            if (c == 0) {
+                ml[2 * at] = mq;
+                ml[2 * at + 1] = lq;
+            }
+        }
+        __syncthreads();                      // the ring is free again
+    }
+}
+
 // One (sequence, query head) a workgroup.  The own parts come first, then the
 // shared pages'.
 template <bool WIDE>
@@ -130,6 +376,14 @@ SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, b
         p.n_wg = 256 * (d <= (bf16 ? 128 : 64) ? 2 : 1);
         p.min_units = 4;
         s.own = s.pre = p;
+        // Two query tiles and more: through LDS.
+        if (bf16 && d <= 256 && queries > 32) {
+            s.pre.wide = true;                // (tier: the widths, as above)
+            s.pre.wq = queries <= 64 ? 2 : queries <= 128 || d > 192 || (d > 128 && Dv > 128) ? 4 : 8;
+            s.pre.tile_rows = 32 * s.pre.wq;
+            s.pre.n_wg = KW_MAX_WG;
+            s.pre.min_units = KV_ROW_UNITS;
+        }
     }
     s.own.q_tiles = (G + s.own.tile_rows - 1) / s.own.tile_rows;
     s.pre.q_tiles = 0;                        // each group's own
@@ -165,6 +419,16 @@ static void launch_wide(const AttnLaunch &a, int wq, hipStream_t st)
     else launch_wide<DK, DV, 4, PART>(a, st);
 }
 
+template <int DK, int DV, int NW>
+static void launch_prefix(const AttnLaunch &a, int wq, hipStream_t st)
+{
+    // (192-wide keys: six stages in LDS, too few for four at a time)
+    constexpr int N2 = DK == 192 ? 4 : NW;
+    if (wq == 2) attn_prefix_kernel<DK, DV, 2, N2><<<a.n_wg, 64 * N2, 0, st>>>(a);
+    else if (wq == 4) attn_prefix_kernel<DK, DV, 4, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
+    else if constexpr (NW == 8) attn_prefix_kernel<DK, DV, 8, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
+}
+
 template <KvPart PART>
 static void launch_part(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 {
@@ -177,7 +441,14 @@ static void launch_part(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, const SharedPlan &p, hipStream_t st)
 {
     launch_part<KV_OWN>(own, p.own, st);
-    launch_part<KV_PREFIX>(pre, p.pre, st);
+    if (p.pre.wide && !p.own.wide) {
+        if (p.pre.tier == 64) launch_prefix<64, 64, 8>(pre, p.pre.wq, st);
+        else if (p.pre.tier == 128) launch_prefix<128, 128, 8>(pre, p.pre.wq, st);
+        else if (pre.Dk <= 192 && pre.Dv <= 128) launch_prefix<192, 128, 8>(pre, p.pre.wq, st);
+        else launch_prefix<256, 256, 4>(pre, p.pre.wq, st);
+    } else {
+        launch_part<KV_PREFIX>(pre, p.pre, st);
+    }
     if (p.own.wide) attn_shared_join_kernel<true><<<own.B * own.Hq, KV_NT, 0, st>>>(own, pre);
     else attn_shared_join_kernel<false><<<own.B * own.Hq, KV_NT, 0, st>>>(own, pre);
     return hipGetLastError();

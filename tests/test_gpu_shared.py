@@ -78,6 +78,25 @@ def test_group_sizes(dtype, Hq, Hkv, Dk, Dv, latent, n):
     run(c, Hq, 2.0 / np.sqrt(Dk))
 
 
+@pytest.mark.parametrize("Hq,Hkv,Dk,Dv", [(8, 2, 128, 128), (4, 1, 64, 64), (8, 2, 256, 256), (4, 1, 192, 128), (4, 1, 80, 104),
+                                          (4, 1, 40, 24), (4, 2, 128, 200), (32, 1, 96, 96)])
+@pytest.mark.parametrize("n,pages", [(9, 40), (17, 3), (24, 70), (33, 21), (65, 129), (80, 2)])
+def test_one_large_group(Hq, Hkv, Dk, Dv, n, pages):
+    # every number of query tiles a workgroup has, and of waves that split the positions
+    rng = np.random.default_rng(n + Dk)
+    run(make_shared([(pages, list(rng.integers(0, 50, size=n)))], Hkv, Dk, Dv, 16, "bf16", seed=n), Hq, 2.0 / np.sqrt(Dk))
+
+
+def test_one_large_group_of_small_pages():
+    # the shared pages end inside a stage; pages that do not exist
+    rng = np.random.default_rng(3)
+    for page, pages in ((1, 77), (2, 1030), (8, 5)):
+        c = make_shared([(pages, list(rng.integers(0, 9, size=40)))], 1, 128, 128, page, "bf16", seed=page)
+        run(c, 4, 0.2)
+        c["table"][:, [0, 3, pages - 1]] = -1
+        run(c, 4, 0.2)
+
+
 @pytest.mark.parametrize("dtype,latent,Hq,Hkv,Dk,Dv", [("bf16", False, 8, 2, 128, 128), ("f32", False, 2, 2, 64, 64),
                                                        ("bf16", True, 64, 1, 576, 512), ("bf16", False, 2, 1, 256, 256)])
 def test_long_prefix(dtype, latent, Hq, Hkv, Dk, Dv):
