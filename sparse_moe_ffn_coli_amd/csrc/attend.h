@@ -48,10 +48,16 @@ typedef short bf16x8s __attribute__((ext_vector_type(8)));
 enum KvPart { KV_ALL, KV_OWN, KV_PREFIX };
 
 // Sequences of group g: the groups are a partition of the batch.
-__device__ __forceinline__ int kv_group_first(const AttnLaunch &a, int g) { return g <= 0 ? 0 : min(max(a.group_start[g], 0), a.B); }
+// (Loads without branches, so that they are in flight together.)
+__device__ __forceinline__ int kv_group_first(const AttnLaunch &a, int g)
+{
+    const int at = a.group_start[g];
+    return g == 0 ? 0 : min(max(at, 0), a.B);
+}
 __device__ __forceinline__ int kv_group_end(const AttnLaunch &a, int g)
 {
-    return g + 1 >= a.n_groups ? a.B : min(max(a.group_start[g + 1], 0), a.B);
+    const int at = a.group_start[g + 1];
+    return g + 1 == a.n_groups ? a.B : min(max(at, 0), a.B);
 }
 // Pages that sequence b shares with its group, and the ones that its own part
 // leaves to it: none where the sequence ends before them (it is then taken
@@ -69,8 +75,9 @@ __device__ __forceinline__ int kv_len(const AttnLaunch &a, int b)
 {
     if constexpr (PART == KV_OWN) return min(max(a.lens[b], 0), a.cap) - (kv_left(a, b) << a.page_shift);
     if constexpr (PART == KV_PREFIX) {
-        const int first = kv_group_first(a, b);
-        return first < kv_group_end(a, b) ? kv_shared(a, first) << a.page_shift : 0;
+        const int first = kv_group_first(a, b), end = kv_group_end(a, b);
+        const int pages = kv_shared(a, min(first, a.B - 1));
+        return first < end ? pages << a.page_shift : 0;
     }
     return a.idx ? a.idx_k : min(max(a.lens[b], 0), a.cap);
 }

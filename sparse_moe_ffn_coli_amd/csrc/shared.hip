@@ -49,7 +49,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     constexpr int CPW = CPS * WK / NW;                        // of a wave in a round
     constexpr int OUT = 32 * DV;                              // floats of a query tile's output
     constexpr int RING = 147456 / STAGE < 8 ? 147456 / STAGE : 8;                 // stages in LDS; a row's outputs fit too
-    constexpr int AHEAD = RING / WK - 1;                      // rounds in flight beside the one computed
+    // The second half of the waves, which share the SIMDs with the first, begin
+    // a round between their softmax and their output products, so that one
+    // multiplies while the other weighs.  The round before is still read then.
+    constexpr bool LATE = NW == 8 && RING / WK >= 3;
+    constexpr int AHEAD = RING / WK - (LATE ? 2 : 1);         // rounds in flight beside the one computed
     constexpr int KS = DK / 16, DT = DV / 32;
     static_assert(CPS * WK % NW == 0 && AHEAD >= 1 && (AHEAD - 1) * CPW < 64, "copies of a round");
     static_assert(NW * OUT * 4 <= RING * STAGE, "outputs of all waves");
@@ -109,24 +113,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                 rows_s[(t0 / KP_BLOCK) & 1][tid + x * (64 * NW)] =
                     p[x] < end && pg[x] >= 0 && pg[x] < a.n_pages ? kv_pool_row(a, pg[x], h, p[x]) : -1;
         };
-        // the wave's copies of round r
-        auto issue = [&](int r) {
-#pragma unroll
-            for (int x = 0; x < CPW; ++x) {
-                const int j = wave + x * NW, t = r * WK + j / CPS, i = j % CPS;
-                const bool key = i < CK;
-                const int32_t *rows = rows_s[(t / KP_BLOCK) & 1] + (t % KP_BLOCK) * KW_ROWS;
-                const uint32_t dst = ring_at + (t % RING) * STAGE;
-                auto copy = [&](auto chunks, int i, uint64_t pool, uint32_t bytes, uint32_t width, uint32_t dst) {
-                    constexpr int R = decltype(chunks)::value;
-                    const int at = i * (64 / R) + lane / R;
-                    const uint32_t off = ((lane % R) ^ kp_swz<R>(at)) << 4;
-                    const int from = rows[at];
-                    kw_copy(from >= 0 && off < width ? pool + (uint64_t)(uint32_t)from * bytes + off : (uint64_t)kv_zeros, dst + i * 1024);
-                };
-                if (key) copy(KwInt<RK>{}, i, kpool, k_bytes, k_bytes, dst);
-                else copy(KwInt<RV>{}, i - CK, vpool, v_bytes, a.Dv * 2, dst + KB);
-            }
+        // The wave's copies of round r.  Copy x of a wave is number NW x + wave of the round's.
+        auto row_of = [&](int r, int x) {     // pool row that the lane's chunk comes from
+            const int t = r * WK + NW * x / CPS, i = NW * x % CPS + wave;
+            const int at = i < CK ? i * (64 / RK) + lane / RK : (i - CK) * (64 / RV) + lane / RV;
+            return rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + at];
+        };
+        auto copy = [&](int r, int x, int from) {
+            const int t = r * WK + NW * x / CPS, i = NW * x % CPS + wave;
+            const uint32_t dst = ring_at + (t % RING) * STAGE;
+            auto part = [&](auto chunks, int i, uint64_t pool, uint32_t bytes, uint32_t width, uint32_t dst) {
+                constexpr int R = decltype(chunks)::value;
+                const uint32_t off = ((lane % R) ^ kp_swz<R>(i * (64 / R) + lane / R)) << 4;
+                kw_copy(from >= 0 && off < width ? pool + (uint64_t)(uint32_t)from * bytes + off : (uint64_t)kv_zeros, dst + i * 1024);
+            };
+            if (CK % NW == 0 ? NW * x % CPS < CK : i < CK) part(KwInt<RK>{}, i, kpool, k_bytes, k_bytes, dst);
+            else part(KwInt<RV>{}, i - CK, vpool, v_bytes, a.Dv * 2, dst + KB);
         };
 
         f32x16 o[DT];
@@ -138,31 +140,65 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         look_up(0);
         kw_barrier();
 #pragma unroll 1
-        for (int r = 0; r < AHEAD; ++r) issue(r);
-        for (int r = 0; r < rounds; ++r) {
-            // this wave's copies of round r have landed, then everyone's; round r - 1 is done with its stages
+        for (int r = 0; r < AHEAD; ++r) {
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) copy(r, x, row_of(r, x));
+        }
+        // Begin of round r: its copies have landed, the wave's and then everyone's, and all are done with the slots
+        // that the copies of a later round, which go out now, are to fill.
+        auto begin = [&](int r) {
             kw_wait_copies<(AHEAD - 1) * CPW>();
             kw_barrier();
-            const int ahead = (r + AHEAD) * WK;
-            if (ahead % KP_BLOCK == 0) {
-                look_up(ahead);
+            const int ahead = r + AHEAD;
+            if (ahead * WK % KP_BLOCK == 0) {
+                look_up(ahead * WK);
                 kw_barrier();
             }
-            issue(r + AHEAD);
+            int from[CPW];
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) from[x] = row_of(ahead, x);
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) copy(ahead, x, from[x]);
+        };
+        if (LATE && wave >= NW / 2) begin(0);
+#pragma unroll 1
+        for (int r = 0; r < rounds; ++r) {
+            if (!(LATE && wave >= NW / 2)) begin(r);
             const int t = r * WK + kb;
             const char *st = ring + (t % RING) * STAGE;
-            const uint32_t hid = (uint32_t)__ballot(rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + ql] < 0) >> (4 * hi);
 
-            // ---- scores ----
+            // ---- scores: eight fragments in a ring, the order is fixed (left to itself the compiler reads each
+            // fragment just before its product) ----
+            constexpr int KF = KS < 8 ? KS : 8;
+            bf16x8 kf[KF];
+            auto frag = [&](int c) { return *reinterpret_cast<const bf16x8 *>(st + (key_at ^ (32 * (c & 7))) + (c >> 3) * 256); };
+            const int mine = rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + ql];
+#pragma unroll
+            for (int c = 0; c < KF; ++c) kf[c] = frag(c);
+            __builtin_amdgcn_sched_barrier(0);
             f32x16 sc;
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
-                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(st + (key_at ^ (32 * (c & 7))) + (c >> 3) * 256);
-                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[c], sc, 0, 0, 0);
+                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % KF], qf[c], sc, 0, 0, 0);
+                if (c + KF < KS) kf[c % KF] = frag(c + KF);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            // values of the first two column tiles, on their way during the softmax: read number y of eight
+            s16x4 vf[2][2][2][2];
+            auto column = [&](int x, int y) {
+                const int odd = y & 1, half = (y >> 1) & 1, ks = y >> 2, tile = 2 * x + odd;
+                // row 8 further: the swizzle's second bit; a column tile is four chunks
+                const int at = (val_at ^ (32 * half) ^ (64 * (tile & 3))) + (tile >> 2) * 256 + (16 * ks + 8 * half) * (RV * 16);
+                vf[x & 1][odd][ks][half] =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
+            };
+#pragma unroll
+            for (int y = 0; y < 8; ++y) column(0, y);
+            __builtin_amdgcn_sched_barrier(0);
             // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
+            const uint32_t hid = (uint32_t)__ballot(mine < 0) >> (4 * hi);
             float w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = kv_scaled(a, sc[i]);
@@ -196,22 +232,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                 whi[i / 8][i / 2 % 4] = p;
                 wlo[i / 8][i / 2 % 4] = pack_bf16(w0 - __uint_as_float(p << 16), w1 - __uint_as_float(p & 0xffff0000u));
             }
-            // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further ----
+            if (LATE && wave >= NW / 2 && r + 1 < rounds) begin(r + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further; two column
+            // tiles at a time, read one pair ahead, their products taken in turn ----
 #pragma unroll
-            for (int x = 0; x < DT; ++x)
+            for (int x = 0; x < DT / 2; ++x) {
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    s16x4 half[2];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        // row 8 y further: the swizzle's second bit; column tile x: four chunks each
-                        const int at = (val_at ^ (32 * y) ^ (64 * (x & 3))) + (x >> 2) * 256 + (16 * ks + 8 * y) * (RV * 16);
-                        half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
-                    }
-                    const bf16x8 vb = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                    o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(whi[ks]), o[x], 0, 0, 0);
-                    o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(wlo[ks]), o[x], 0, 0, 0);
+                for (int y = 0; y < 8; ++y) {
+                    const int odd = y & 1, ks = y >> 2;
+                    const bf16x8 vb = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(
+                        vf[x & 1][odd][ks][0], vf[x & 1][odd][ks][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    o[2 * x + odd] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16((y & 2) ? wlo[ks] : whi[ks]),
+                                                                            o[2 * x + odd], 0, 0, 0);
+                    if (x + 1 < DT / 2) column(x + 1, y);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            }
         }
         kw_wait_copies<0>();                  // stages past the row's end are copied too, as zeros
         kw_barrier();
@@ -260,92 +297,119 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     }
 }
 
-// One (sequence, query head) a workgroup.  The own parts come first, then the
-// shared pages'.
+// Joins the parts of `per` query heads of one sequence and cache head, the own
+// parts first, then the shared pages'.  A wave looks up one head's parts and
+// forms their factors; groups of threads then take every ng-th part, 4 columns
+// a thread.
+constexpr int SJ_HEADS = 4;                   // most heads of a workgroup
+
 template <bool WIDE>
-__global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own, AttnLaunch pre)
+__global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own, AttnLaunch pre, int per)
 {
     __shared__ __attribute__((aligned(16))) float red[KV_NT * 4];
-    __shared__ float factor[2 * KV_MAX_WG];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int bq = blockIdx.x, b = bq / own.Hq, hq = bq - b * own.Hq;
-    const int G = own.Hq / own.Hkv, h = hq / G, qi = hq - h * G;
-    int before, total;
-    kv_prefix<KV_OWN>(own, b, &before, &total);
-    const KvParts p = kv_parts<KV_OWN>(own, b, h * own.q_tiles + qi / own.tile_rows, before, total);
-    const int n_own = p.steps == 0 ? 0 : p.w1 - p.w0 + 1, q_own = qi % own.tile_rows;
-    // (a row that is not cut is one part, in its queries' places)
-    int n_pre = 0, q_pre = 0;
-    KvParts pp{};
-    const int pages = kv_shared(own, b);
-    if (pages > 0 && kv_left(own, b) == pages) {
-        int g = -1;
-        for (int c = 0; g < 0 && c < pre.n_groups; c += 64) {
-            const bool here = c + lane < pre.n_groups && kv_group_first(pre, c + lane) <= b && b < kv_group_end(pre, c + lane);
-            const uint64_t mask = __ballot(here);
-            if (mask) g = c + __ffsll((unsigned long long)mask) - 1;
-        }
-        if (g >= 0) {
-            kv_prefix<KV_PREFIX>(pre, g, &before, &total);
-            const int i = (b - kv_group_first(pre, g)) * G + qi;
-            pp = kv_parts<KV_PREFIX>(pre, g, h * kv_tiles<KV_PREFIX>(pre, g) + i / pre.tile_rows, before, total);
-            n_pre = pp.steps == 0 ? 0 : pp.w1 - pp.w0 + 1;
-            q_pre = i % pre.tile_rows;
-        }
-    }
-    const int n = n_own + n_pre;
-    if (n == 0) return kv_write_empty(own, bq, 1);
-    auto query = [&](int w) {                 // of part w, that of a cut row: row of part_ml
-        return w < n_own ? (size_t)p.slot(p.w0 + w) * own.tile_rows + q_own
-                         : (size_t)pp.slot(pp.w0 + w - n_own) * pre.tile_rows + q_pre;
+    __shared__ float factor[SJ_HEADS][2 * KV_MAX_WG];
+    __shared__ float inverse[SJ_HEADS];
+    struct Parts {
+        int n_own, n_pre;                     // 1: a row that is not cut, by its query
+        int own0, own1, pre0, pre1;           // rows of part_ml: of the first part, and of the second less 2 tile rows a range
     };
-    auto whole = [&](int w) { return w < n_own ? n_own == 1 : n_pre == 1; };
-    auto ml = [&](int w) {
-        return whole(w) ? (w < n_own ? own.full_ml : pre.full_ml) + 2 * (size_t)bq
-                        : (w < n_own ? own.part_ml : pre.part_ml) + 2 * query(w);
-    };
+    __shared__ Parts parts[SJ_HEADS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int G = own.Hq / own.Hkv, chunks = (G + per - 1) / per;
+    const int bh = blockIdx.x / chunks, b = bh / own.Hkv, h = bh - b * own.Hkv;
+    const int i0 = (blockIdx.x - bh * chunks) * per, heads = min(per, G - i0);
+    const size_t bq0 = (size_t)b * own.Hq + h * G + i0;
+    const float *own_ml = own.part_ml, *own_full_ml = own.full_ml, *pre_ml = pre.part_ml, *pre_full_ml = pre.full_ml;
 
-    float mx = -INFINITY;
-    for (int w = lane; w < n; w += 64) mx = fmaxf(mx, ml(w)[0]);
+    if (wave < heads) {
+        const int qi = i0 + wave;
+        const size_t bq = bq0 + wave;
+        Parts x{};
+        int before, total;
+        kv_prefix<KV_OWN>(own, b, &before, &total);
+        const KvParts p = kv_parts<KV_OWN>(own, b, h * own.q_tiles + qi / own.tile_rows, before, total);
+        x.n_own = p.steps == 0 ? 0 : p.w1 - p.w0 + 1;
+        x.own0 = p.first * own.tile_rows + qi % own.tile_rows;
+        x.own1 = 2 * p.w0 * own.tile_rows + qi % own.tile_rows;
+        const int pages = kv_shared(own, b);
+        if (pages > 0 && kv_left(own, b) == pages) {
+            int g = -1;
+            for (int c = 0; g < 0 && c < pre.n_groups; c += 64) {
+                const int at = min(c + lane, pre.n_groups - 1);
+                const uint64_t mask = __ballot(c + lane < pre.n_groups && kv_group_first(pre, at) <= b && b < kv_group_end(pre, at));
+                if (mask) g = c + __ffsll((unsigned long long)mask) - 1;
+            }
+            if (g >= 0) {
+                kv_prefix<KV_PREFIX>(pre, g, &before, &total);
+                const int i = (b - kv_group_first(pre, g)) * G + qi, tile = i / pre.tile_rows;
+                const KvParts pp = kv_parts<KV_PREFIX>(pre, g, h * kv_tiles<KV_PREFIX>(pre, g) + tile, before, total);
+                x.n_pre = pp.steps == 0 ? 0 : pp.w1 - pp.w0 + 1;
+                x.pre0 = pp.first * pre.tile_rows + i - tile * pre.tile_rows;
+                x.pre1 = 2 * pp.w0 * pre.tile_rows + i - tile * pre.tile_rows;
+            }
+        }
+        const int n = x.n_own + x.n_pre, own_step = 2 * own.tile_rows, pre_step = 2 * pre.tile_rows;
+        auto ml = [&](int w) -> const float * {
+            if (w < x.n_own) return x.n_own == 1 ? own_full_ml + 2 * bq : own_ml + 2 * (size_t)(w == 0 ? x.own0 : x.own1 + w * own_step);
+            w -= x.n_own;
+            return x.n_pre == 1 ? pre_full_ml + 2 * bq : pre_ml + 2 * (size_t)(w == 0 ? x.pre0 : x.pre1 + w * pre_step);
+        };
+        float mx = -INFINITY;
+        for (int w = lane; w < n; w += 64) mx = fmaxf(mx, ml(w)[0]);
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float l = 0.f;
-    for (int w = lane; w < n; w += 64) {
-        const float f = __builtin_amdgcn_exp2f(ml(w)[0] - ref);
-        l += ml(w)[1] * f;
-        if (tid < 64) factor[w] = f;
+        for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float l = 0.f;
+        for (int w = lane; w < n; w += 64) {
+            const float f = __builtin_amdgcn_exp2f(ml(w)[0] - ref);
+            l += ml(w)[1] * f;
+            factor[wave][w] = f;
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
+        if (lane == 0) {
+            parts[wave] = x;
+            inverse[wave] = kv_inverse(l);
+            kv_write_lse(own, bq, mx, l);
+        }
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
     __syncthreads();
 
-    // groups of threads take every ng-th part, 4 columns a thread
-    const int cols = own.Dv / 4, ng = KV_NT / cols, grp = tid / cols, col = tid % cols;
+    const int cols = own.Dv / 4, grp = tid / cols, col = tid - grp * cols;
+    const int ng = KV_NT / cols / heads;      // groups a head (per is at most KV_NT / cols)
+    const int v = grp / ng, sub = grp - v * ng;
+    const bool mine = v < heads;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    if (grp < ng) {
-#pragma unroll 4
-        for (int w = grp; w < n; w += ng) {
-            const float *part = w < n_own ? (whole(w) ? own.full_o : own.part_o) : whole(w) ? pre.full_o : pre.part_o;
-            const size_t q = whole(w) ? (size_t)bq : query(w);
-            // (the wide kernel's parts: lanes side by side, 32 queries at a time)
-            const size_t at = WIDE && !whole(w) ? (q >> 5) * 32 * own.out_cols + ((size_t)(col >> 1) * 64 + (col & 1) * 32 + (q & 31)) * 4
-                                                : q * own.Dv + 4 * col;
-            acc += *reinterpret_cast<const f32x4 *>(part + at) * factor[w];
-        }
+    if (mine) {
+        const Parts x = parts[v];
+        const size_t bq = bq0 + v;
+        // (the wide kernel's parts: lanes side by side, 32 queries at a time)
+        auto at = [&](size_t q) {
+            return WIDE ? (q >> 5) * 32 * own.out_cols + ((size_t)(col >> 1) * 64 + (col & 1) * 32 + (q & 31)) * 4 : q * own.Dv + 4 * col;
+        };
+        auto add = [&](const float *part, const float *full, int n, int row0, int row1, int step, const float *f) {
+            if (n == 1) {
+                if (sub == 0) acc += *reinterpret_cast<const f32x4 *>(full + bq * own.Dv + 4 * col) * f[0];
+                return;
+            }
+#pragma unroll 8
+            for (int w = sub; w < n; w += ng)
+                acc += *reinterpret_cast<const f32x4 *>(part + at((size_t)(w == 0 ? row0 : row1 + w * step))) * f[w];
+        };
+        add(own.part_o, own.full_o, x.n_own, x.own0, x.own1, 2 * own.tile_rows, factor[v]);
+        add(pre.part_o, pre.full_o, x.n_pre, x.pre0, x.pre1, 2 * pre.tile_rows, factor[v] + x.n_own);
         *reinterpret_cast<f32x4 *>(red + 4 * tid) = acc;
     }
     __syncthreads();
-    if (tid < cols) {
-        for (int x = 1; x < ng; ++x) acc += *reinterpret_cast<const f32x4 *>(red + 4 * (x * cols + col));
-        const float inv = kv_inverse(l);
-        const size_t at = (size_t)bq * own.Dv + 4 * col;
+    if (mine && sub == 0) {
+        for (int x = 1; x < ng; ++x) acc += *reinterpret_cast<const f32x4 *>(red + 4 * (tid + x * cols));
+        const float inv = inverse[v];
+        const size_t to = (bq0 + v) * own.Dv + 4 * col;
         if (own.bf16)
-            *reinterpret_cast<u32x2 *>((uint16_t *)own.out + at) =
+            *reinterpret_cast<u32x2 *>((uint16_t *)own.out + to) =
                 u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
-        else *reinterpret_cast<f32x4 *>((float *)own.out + at) = acc * inv;
+        else *reinterpret_cast<f32x4 *>((float *)own.out + to) = acc * inv;
     }
-    if (tid == 0) kv_write_lse(own, bq, mx, l);
 }
 
 SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int n_groups, int entries)
@@ -449,8 +513,13 @@ hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, cons
     } else {
         launch_part<KV_PREFIX>(pre, p.pre, st);
     }
-    if (p.own.wide) attn_shared_join_kernel<true><<<own.B * own.Hq, KV_NT, 0, st>>>(own, pre);
-    else attn_shared_join_kernel<false><<<own.B * own.Hq, KV_NT, 0, st>>>(own, pre);
+    // Heads of a join's workgroup: more share what is looked up, fewer are more workgroups.
+    const int G = own.Hq / own.Hkv;
+    int per = SJ_HEADS;
+    while (per > 1 && (per * (own.Dv / 4) > KV_NT || per > G || own.B * own.Hq / per < 512)) per /= 2;
+    const int n_join = own.B * own.Hkv * ((G + per - 1) / per);
+    if (p.own.wide) attn_shared_join_kernel<true><<<n_join, KV_NT, 0, st>>>(own, pre, per);
+    else attn_shared_join_kernel<false><<<n_join, KV_NT, 0, st>>>(own, pre, per);
     return hipGetLastError();
 }
 
