@@ -250,6 +250,7 @@ bool set_scale(coli::AttnLaunch &a, double sc)
     // scale * log2(e) as the sum of two floats, without the error that one
     // rounded factor would put on every large score
     a.scale_hi = (float)sc;
+    a.scale_size = fabsf(a.scale_hi);
     a.scale_lo = (float)(sc - (double)a.scale_hi);
     a.scale_cap = (float)(3e38 / fmax(1.0, fabs((double)a.scale_lo)));
     return true;

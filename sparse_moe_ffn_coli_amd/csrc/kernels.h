@@ -92,6 +92,7 @@ struct AttnLaunch {
     int out_cols;          // columns of a part's rows
     float *full_o;         // workspace [B][Hq][Dv]: unnormalised outputs of rows that are not cut
     float *full_ml;        // workspace [B][Hq][2]
+    float scale_size;      // |scale_hi|
 };
 
 // Which kernel an attention call takes and how its workspace is laid out.

@@ -39,6 +39,67 @@ __device__ __forceinline__ int kp_swz(int row)
 }
 constexpr int kp_chunks(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
 
+// 2^(score scale - ref), the product rounded as the reference is: a fused one
+// would leave the largest score of some 2^30 the product's rounding, 2^64 and
+// more of it.
+__device__ __forceinline__ float kp_weight(float score, float scale, float ref)
+{
+#pragma clang fp contract(off)
+    const float t = score * scale;
+    return __builtin_amdgcn_exp2f(t - ref);
+}
+
+// Two fp32 to bf16 in one instruction (pack_bf16 takes four).
+__device__ __forceinline__ uint32_t kp_pack(float lo, float hi)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// The range of a workgroup: kv_first, of up to 64 groups in one look at them.
+struct KpGroup {
+    int first, queries, tiles;                // first sequence, query heads of a cache head, their tiles
+};
+__device__ __forceinline__ KpGroup kp_group(const AttnLaunch &a, int b)
+{
+    KpGroup g;
+    g.first = kv_group_first(a, b);
+    g.queries = (kv_group_end(a, b) - g.first) * (a.Hq / a.Hkv);
+    g.tiles = (g.queries + a.tile_rows - 1) / a.tile_rows;
+    return g;
+}
+__device__ __forceinline__ bool kp_first(const AttnLaunch &a, KvRange &rg, KpGroup &grp)
+{
+    if (a.n_groups > 64) {
+        if (!kv_first<KV_PREFIX>(a, 1, rg)) return false;
+        grp = kp_group(a, rg.b);
+        return true;
+    }
+    const int lane = threadIdx.x & 63;
+    const KpGroup g = kp_group(a, min(lane, a.n_groups - 1));
+    const bool some = lane < a.n_groups && g.queries > 0;
+    const int n = some ? kv_shared(a, min(g.first, a.B - 1)) << a.page_shift : 0;
+    const int st = kv_units(n) * a.Hkv * (some ? g.tiles : 0);
+    const int incl = wave_scan_incl(st), total = __builtin_amdgcn_readlane(incl, 63);
+    const int range = kv_range(a, total), u = blockIdx.x * range;
+    if (u >= total) return false;
+    const int x = __ffsll((unsigned long long)__ballot(u < incl)) - 1;
+    const int base = __builtin_amdgcn_readlane(incl - st, x);
+    grp.first = __builtin_amdgcn_readlane(g.first, x);
+    grp.queries = __builtin_amdgcn_readlane(g.queries, x);
+    grp.tiles = __builtin_amdgcn_readlane(g.tiles, x);
+    rg.u = u;
+    rg.u_end = min(u + range, total);
+    rg.b = x;
+    rg.n = __builtin_amdgcn_readlane(n, x);
+    rg.steps = kv_steps(rg.n);
+    const int per = kv_units(rg.n);
+    rg.row = (u - base) / per;
+    rg.s0 = (u - base) - rg.row * per;
+    return true;
+}
+
 template <int DK, int DV, int WQ, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attn_prefix_kernel(AttnLaunch a)
 {
@@ -46,16 +107,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     constexpr int RK = kp_chunks(DK), RV = kp_chunks(DV);
     constexpr int KB = KW_ROWS * RK * 16, STAGE = KB + KW_ROWS * RV * 16;         // bytes of a stage's keys, and of all
     constexpr int CK = RK / 2, CPS = CK + RV / 2;             // copy instructions of a stage
-    constexpr int CPW = CPS * WK / NW;                        // of a wave in a round
     constexpr int OUT = 32 * DV;                              // floats of a query tile's output
     constexpr int RING = 147456 / STAGE < 8 ? 147456 / STAGE : 8;                 // stages in LDS; a row's outputs fit too
-    // The second half of the waves, which share the SIMDs with the first, begin
-    // a round between their softmax and their output products, so that one
-    // multiplies while the other weighs.  The round before is still read then.
-    constexpr bool LATE = NW == 8 && RING / WK >= 3;
-    constexpr int AHEAD = RING / WK - (LATE ? 2 : 1);         // rounds in flight beside the one computed
+    // A round is a stage for each of the WK position groups, a barrier every PB
+    // rounds.  A round's output products follow in the next round, between its
+    // weights, so that the matrix cores run during the softmax.  (Half of the
+    // waves a phase later than the others, 64 sequences of 4 heads behind 32768
+    // positions: 64.0 us, 63.1 without.)
+    constexpr int PB = RING / WK >= 6 ? 2 : 1, BLOCKS = RING / (WK * PB);         // barriers' spans in the ring
+    constexpr int AHEAD = BLOCKS - 2;                         // spans in flight beside the one computed and the one before
+    constexpr int CPW = CPS * WK * PB / NW;                   // copies of a wave in a span
     constexpr int KS = DK / 16, DT = DV / 32;
-    static_assert(CPS * WK % NW == 0 && AHEAD >= 1 && (AHEAD - 1) * CPW < 64, "copies of a round");
+    static_assert(CPS * WK * PB % NW == 0 && AHEAD >= 1 && (AHEAD - 1) * CPW < 64, "copies of a round");
     static_assert(NW * OUT * 4 <= RING * STAGE, "outputs of all waves");
     __shared__ __attribute__((aligned(256))) char ring[RING * STAGE];
     __shared__ int32_t rows_s[2][KP_BLOCK * KW_ROWS];         // pool rows of the stages' positions, -1: hidden
@@ -66,11 +129,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const int qt = wave % WQ, kb = wave / WQ;
     const int ql = lane & 31, hi = lane >> 5;
     KvRange rg;
-    if (!kv_first<KV_PREFIX>(a, 1, rg)) return;
+    KpGroup grp;
+    if (!kp_first(a, rg, grp)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
     const uint64_t kpool = (uint64_t)a.k, vpool = (uint64_t)(a.v ? a.v : a.k);
+    // A score in units of log2 e is one product here, by scale's size alone: the
+    // rounded factor is off by half a step of the score, the sum of the products
+    // by more.  The queries take its sign, so the largest product is the largest
+    // score.
+    const float scale = a.scale_size;
+    const uint32_t flip = a.scale_hi < 0.f ? 0x80008000u : 0u;
     const uint32_t k_bytes = a.Dk * 2, v_bytes = a.v ? a.Dv * 2 : k_bytes;        // from a row to the next
 
     // this lane's places in a stage: key row ql, chunk hi; and the transposing reads' rows 4 hi + rr, of whose columns
@@ -80,22 +150,29 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const int val_at = KB + (4 * hi + rr) * (RV * 16) +
                        (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ kp_swz<RV>(4 * hi + rr)) << 4) + (lane & 1) * 8;
 
-    for (; u < u_end; u += kv_units(n) - s0, s0 = 0, kv_next_row<KV_PREFIX>(a, 1, b, n, steps, row)) {
+    auto advance = [&] {
+        u += kv_units(n) - s0;
+        s0 = 0;
+        const int was = b;
+        kv_next_row<KV_PREFIX>(a, 1, b, n, steps, row);
+        if (b != was && u < u_end) grp = kp_group(a, b);
+    };
+    for (;; advance()) {
+        if (u >= u_end) return;
         const int s1 = min(steps, s0 + (u_end - u));
         if (s0 >= steps) continue;            // a row's units past its steps
-        const KvTileOf tile = kv_tile_of<KV_PREFIX>(a, b, row);
-        const int first = kv_group_first(a, b), h = tile.h, q0 = tile.q0 + 32 * qt;
-        const int nq = tile.queries - q0;     // query heads of this wave's tile (may be none)
-        const int seg = s1 - s0, rounds = (seg + WK - 1) / WK;
+        const int first = grp.first, h = row / grp.tiles, tq0 = (row - h * grp.tiles) * (32 * WQ), q0 = tq0 + 32 * qt;
+        const int nq = grp.queries - q0;      // query heads of this wave's tile (may be none)
+        const int seg = s1 - s0, rounds = (seg + 2 * WK - 1) / (2 * WK) * 2;     // (pairs: a stage past the end is hidden)
 
-        bf16x8 qf[KS];
+        u32x4 qr[KS];
         {
             const uint16_t *q = (const uint16_t *)a.q + kv_query_row(a, first, h, q0 + min(ql, max(nq, 1) - 1)) * a.Dk;
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
                 const int d = 16 * c + 8 * hi;
-                qf[c] = bf16x8{};
-                if (ql < nq && d < a.Dk) qf[c] = *reinterpret_cast<const bf16x8 *>(q + d);
+                qr[c] = u32x4{0u, 0u, 0u, 0u};
+                if (ql < nq && d < a.Dk) qr[c] = *reinterpret_cast<const u32x4 *>(q + d);
             }
         }
         // pool rows of the block of stages that holds stage t0 (a multiple of KP_BLOCK)
@@ -113,22 +190,31 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                 rows_s[(t0 / KP_BLOCK) & 1][tid + x * (64 * NW)] =
                     p[x] < end && pg[x] >= 0 && pg[x] < a.n_pages ? kv_pool_row(a, pg[x], h, p[x]) : -1;
         };
-        // The wave's copies of round r.  Copy x of a wave is number NW x + wave of the round's.
-        auto row_of = [&](int r, int x) {     // pool row that the lane's chunk comes from
-            const int t = r * WK + NW * x / CPS, i = NW * x % CPS + wave;
-            const int at = i < CK ? i * (64 / RK) + lane / RK : (i - CK) * (64 / RV) + lane / RV;
-            return rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + at];
+        // The wave's copies of span r: copy x of a wave is number NW x + wave of the span's.  Their addresses are formed
+        // a span ahead.
+        uint64_t from[CPW];
+        auto address = [&](int r) {
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) {
+                const int t = r * (WK * PB) + NW * x / CPS, i = NW * x % CPS + wave;
+                const int32_t *rows = rows_s[(t / KP_BLOCK) & 1] + (t % KP_BLOCK) * KW_ROWS;
+                auto part = [&](auto chunks, int i, uint64_t pool, uint32_t bytes, uint32_t width) {
+                    constexpr int R = decltype(chunks)::value;
+                    const int at = i * (64 / R) + lane / R;
+                    const uint32_t off = ((lane % R) ^ kp_swz<R>(at)) << 4;
+                    const int row = rows[at];
+                    from[x] = row >= 0 && off < width ? pool + (uint64_t)(uint32_t)row * bytes + off : (uint64_t)kv_zeros;
+                };
+                if (CK % NW == 0 ? NW * x % CPS < CK : i < CK) part(KwInt<RK>{}, i, kpool, k_bytes, k_bytes);
+                else part(KwInt<RV>{}, i - CK, vpool, v_bytes, a.Dv * 2);
+            }
         };
-        auto copy = [&](int r, int x, int from) {
-            const int t = r * WK + NW * x / CPS, i = NW * x % CPS + wave;
-            const uint32_t dst = ring_at + (t % RING) * STAGE;
-            auto part = [&](auto chunks, int i, uint64_t pool, uint32_t bytes, uint32_t width, uint32_t dst) {
-                constexpr int R = decltype(chunks)::value;
-                const uint32_t off = ((lane % R) ^ kp_swz<R>(i * (64 / R) + lane / R)) << 4;
-                kw_copy(from >= 0 && off < width ? pool + (uint64_t)(uint32_t)from * bytes + off : (uint64_t)kv_zeros, dst + i * 1024);
-            };
-            if (CK % NW == 0 ? NW * x % CPS < CK : i < CK) part(KwInt<RK>{}, i, kpool, k_bytes, k_bytes, dst);
-            else part(KwInt<RV>{}, i - CK, vpool, v_bytes, a.Dv * 2, dst + KB);
+        auto issue = [&](int r) {
+#pragma unroll
+            for (int x = 0; x < CPW; ++x) {
+                const int t = r * (WK * PB) + NW * x / CPS, i = NW * x % CPS + wave;     // (keys first, values behind them)
+                kw_copy(from[x], ring_at + (t % RING) * STAGE + i * 1024);
+            }
         };
 
         f32x16 o[DT];
@@ -141,42 +227,58 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         kw_barrier();
 #pragma unroll 1
         for (int r = 0; r < AHEAD; ++r) {
-#pragma unroll
-            for (int x = 0; x < CPW; ++x) copy(r, x, row_of(r, x));
+            address(r);
+            issue(r);
         }
-        // Begin of round r: its copies have landed, the wave's and then everyone's, and all are done with the slots
-        // that the copies of a later round, which go out now, are to fill.
+        address(AHEAD);
+        // Begin of span r: its copies have landed, the wave's and then everyone's, and all are done with the slots that
+        // the copies of a later span, which go out now, are to fill.
         auto begin = [&](int r) {
             kw_wait_copies<(AHEAD - 1) * CPW>();
             kw_barrier();
             const int ahead = r + AHEAD;
-            if (ahead * WK % KP_BLOCK == 0) {
-                look_up(ahead * WK);
+            if (ahead * (WK * PB) % KP_BLOCK == 0) {
+                look_up(ahead * (WK * PB));
                 kw_barrier();
+                address(ahead);
             }
-            int from[CPW];
-#pragma unroll
-            for (int x = 0; x < CPW; ++x) from[x] = row_of(ahead, x);
-#pragma unroll
-            for (int x = 0; x < CPW; ++x) copy(ahead, x, from[x]);
+            issue(ahead);
+            address(ahead + 1);               // (at a block's end: of rows that are not looked up yet, formed again then)
         };
-        if (LATE && wave >= NW / 2) begin(0);
-#pragma unroll 1
-        for (int r = 0; r < rounds; ++r) {
-            if (!(LATE && wave >= NW / 2)) begin(r);
-            const int t = r * WK + kb;
-            const char *st = ring + (t % RING) * STAGE;
-
-            // ---- scores: eight fragments in a ring, the order is fixed (left to itself the compiler reads each
-            // fragment just before its product) ----
+        bf16x8 qf[KS];
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qr[c][i] ^= flip;
+            qf[c] = as_bf16(qr[c]);
+        }
+        // Scores and their maximum; the reference, and by what the output is to be multiplied where it has moved (only where
+        // a score passes it by 2^8: weights stay below 256 and the sums far inside fp32).
+        f32x16 sc;
+        float ref = 0.f, moved = 1.f;
+        s16x4 vf[2][2][2][2];
+        // Values of column tiles 2 x and 2 x + 1, read number y of eight.  Slots 0-3 of a lane are positions 16 ks + 4 hi
+        // + 0..3, slots 4-7 the ones 8 further (the swizzle's second bit); a column tile is four chunks.
+        auto column = [&](const char *st, int x, int y) {
+            const int odd = y & 1, half = (y >> 1) & 1, ks = y >> 2, tile = 2 * x + odd;
+            const int at = (val_at ^ (32 * half) ^ (64 * (tile & 3))) + (tile >> 2) * 256 + (16 * ks + 8 * half) * (RV * 16);
+            vf[x & 1][odd][ks][half] =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
+        };
+        auto scores = [&](int t, const char *st, const char *prev, auto second) {     // second: there is a round before
+            // eight fragments in a ring, the order is fixed (left to itself the compiler reads each fragment just before
+            // its product)
             constexpr int KF = KS < 8 ? KS : 8;
             bf16x8 kf[KF];
             auto frag = [&](int c) { return *reinterpret_cast<const bf16x8 *>(st + (key_at ^ (32 * (c & 7))) + (c >> 3) * 256); };
             const int mine = rows_s[(t / KP_BLOCK) & 1][(t % KP_BLOCK) * KW_ROWS + ql];
 #pragma unroll
             for (int c = 0; c < KF; ++c) kf[c] = frag(c);
+            if constexpr (decltype(second)::value) {
+#pragma unroll
+                for (int y = 0; y < 8; ++y) column(prev, 0, y);
+            }
             __builtin_amdgcn_sched_barrier(0);
-            f32x16 sc;
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = 0.f;
 #pragma unroll
@@ -185,57 +287,46 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                 if (c + KF < KS) kf[c % KF] = frag(c + KF);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            // values of the first two column tiles, on their way during the softmax: read number y of eight
-            s16x4 vf[2][2][2][2];
-            auto column = [&](int x, int y) {
-                const int odd = y & 1, half = (y >> 1) & 1, ks = y >> 2, tile = 2 * x + odd;
-                // row 8 further: the swizzle's second bit; a column tile is four chunks
-                const int at = (val_at ^ (32 * half) ^ (64 * (tile & 3))) + (tile >> 2) * 256 + (16 * ks + 8 * half) * (RV * 16);
-                vf[x & 1][odd][ks][half] =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(st + at));
-            };
-#pragma unroll
-            for (int y = 0; y < 8; ++y) column(0, y);
-            __builtin_amdgcn_sched_barrier(0);
-            // ---- weights: query ql, position 8 (i >> 2) + 4 hi + (i & 3) ----
             const uint32_t hid = (uint32_t)__ballot(mine < 0) >> (4 * hi);
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = kv_scaled(a, sc[i]);
             if (__ballot(hid != 0)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (hid >> (8 * (i >> 2) + (i & 3)) & 1) w[i] = -INFINITY;
+                    if (hid >> (8 * (i >> 2) + (i & 3)) & 1) sc[i] = -INFINITY;
             }
-            float mx = w[0];
+            float mx = sc[0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, w[i]);
-            // The reference moves only when a score passes it by 2^8: weights
-            // stay below 256 and the sums far inside fp32.
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
+            mx *= scale;
+            moved = 1.f;
             if (__ballot(mx > m + 8.f)) {
                 const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
-                const float f = (mn == -INFINITY) ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                moved = (mn == -INFINITY) ? 1.f : __builtin_amdgcn_exp2f(m - mn);
                 m = mn;
-                l *= f;
-#pragma unroll
-                for (int t = 0; t < DT; ++t) o[t] *= f;
+                l *= moved;
             }
-            const float ref = (m == -INFINITY) ? 0.f : m;
-            // each weight as two bf16 parts: 16 bits of it enter the products
-            u32x4 whi[2], wlo[2];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float w0 = __builtin_amdgcn_exp2f(w[i] - ref), w1 = __builtin_amdgcn_exp2f(w[i + 1] - ref);
-                l += w0;
-                l += w1;
-                const uint32_t p = pack_bf16(w0, w1);
-                whi[i / 8][i / 2 % 4] = p;
-                wlo[i / 8][i / 2 % 4] = pack_bf16(w0 - __uint_as_float(p << 16), w1 - __uint_as_float(p & 0xffff0000u));
+            ref = (m == -INFINITY) ? 0.f : m;
+        };
+        // Weight i (query ql, position 8 (i >> 2) + 4 hi + (i & 3)) as two bf16 parts: 16 bits of it enter the products.
+        u32x4 parts[2][2][2];                 // of two rounds: high and low parts of 8 positions each
+        float even;
+        auto weight = [&](int i, auto to) {
+            const float w = kp_weight(sc[i], scale, ref);
+            l += w;
+            if (i % 2 == 0) {
+                even = w;
+                return;
             }
-            if (LATE && wave >= NW / 2 && r + 1 < rounds) begin(r + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            // ---- output: slots 0-3 of a lane are positions 16 ks + 4 hi + 0..3, slots 4-7 the ones 8 further; two column
-            // tiles at a time, read one pair ahead, their products taken in turn ----
+            uint32_t hi2 = kp_pack(even, w);
+            uint32_t lo2 = kp_pack(even - __uint_as_float(hi2 << 16), w - __uint_as_float(hi2 & 0xffff0000u));
+            // (pinned: the compiler would move all of it behind the products, to where it is used)
+            asm volatile("" : "+v"(hi2), "+v"(lo2), "+v"(l));
+            parts[decltype(to)::value][0][i / 8][i / 2 % 4] = hi2;
+            parts[decltype(to)::value][1][i / 8][i / 2 % 4] = lo2;
+        };
+        // Output products of one round's weights, two column tiles at a time and read one pair ahead; a weight of the next
+        // round between them.
+        auto output = [&](const char *st, auto of, auto with) {
+            constexpr int N = 4 * DT, W = decltype(of)::value;
 #pragma unroll
             for (int x = 0; x < DT / 2; ++x) {
 #pragma unroll
@@ -243,13 +334,49 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                     const int odd = y & 1, ks = y >> 2;
                     const bf16x8 vb = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(
                         vf[x & 1][odd][ks][0], vf[x & 1][odd][ks][1], 0, 1, 2, 3, 4, 5, 6, 7));
-                    o[2 * x + odd] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16((y & 2) ? wlo[ks] : whi[ks]),
+                    o[2 * x + odd] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb, as_bf16(parts[W][(y >> 1) & 1][ks]),
                                                                             o[2 * x + odd], 0, 0, 0);
-                    if (x + 1 < DT / 2) column(x + 1, y);
+                    if (x + 1 < DT / 2) column(st, x + 1, y);
+                    if constexpr (decltype(with)::value) {
+#pragma unroll
+                        for (int i = (8 * x + y) * 16 / N; i < (8 * x + y + 1) * 16 / N; ++i) weight(i, KwInt<1 - W>{});
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
+        };
+        const char *prev;
+        // Round r, whose weights go to `to`; `second`: there is a round before, whose output products are due.
+        auto round = [&](int r, auto to, auto second) {
+            constexpr int W = decltype(to)::value;            // (r's parity)
+            if (PB == 1 || W == 0) begin(r / PB);
+            const int t = r * WK + kb;
+            const char *st = ring + (t % RING) * STAGE;
+            scores(t, st, prev, second);
+            if constexpr (decltype(second)::value) {
+                __builtin_amdgcn_s_setprio(1);                // (before the other wave's scores: 63.1 -> 61.2 us)
+                output(prev, KwInt<1 - W>{}, KwInt<1>{});
+                __builtin_amdgcn_s_setprio(0);
+                if (__ballot(moved != 1.f)) {
+#pragma unroll
+                    for (int x = 0; x < DT; ++x) o[x] *= moved;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) weight(i, to);
+            }
+            prev = st;
+        };
+        round(0, KwInt<0>{}, KwInt<0>{});
+#pragma unroll 1
+        for (int r = 1; r + 1 < rounds; r += 2) {
+            round(r, KwInt<1>{}, KwInt<1>{});
+            round(r + 1, KwInt<0>{}, KwInt<1>{});
         }
+        round(rounds - 1, KwInt<1>{}, KwInt<1>{});
+#pragma unroll
+        for (int y = 0; y < 8; ++y) column(prev, 0, y);
+        output(prev, KwInt<1>{}, KwInt<0>{});
         kw_wait_copies<0>();                  // stages past the row's end are copied too, as zeros
         kw_barrier();
 
@@ -270,7 +397,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         kw_barrier();
         const bool whole = s0 == 0 && s1 == steps;
         const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
-        const int live = min(32 * WQ, tile.queries - tile.q0);
+        const int live = min(32 * WQ, grp.queries - tq0);
         for (int i = tid; i < live * QC; i += 64 * NW) {
             const int q = i / QC, c = i % QC, qi = q & 31;
             if (4 * c >= a.Dv) continue;
@@ -285,7 +412,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
                 lq += red_l[wv][qi] * f;
                 v += buf[(wv * 32 + qi) * QC + (c ^ (qi & (QC - 1)))] * f;
             }
-            const size_t at = whole ? kv_query_row(a, first, h, tile.q0 + q) : (size_t)slot * a.tile_rows + q;
+            const size_t at = whole ? kv_query_row(a, first, h, tq0 + q) : (size_t)slot * a.tile_rows + q;
             float *ml = whole ? a.full_ml : a.part_ml;
             *reinterpret_cast<f32x4 *>((whole ? a.full_o : a.part_o) + at * a.Dv + 4 * c) = v;
             if (c == 0) {
@@ -297,13 +424,69 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     }
 }
 
+// The group of sequence b among the groups (looked at by the whole wave): its
+// first sequence, tiles, pages' steps and units, and the units before it and in
+// all.
+struct KpFound {
+    int first, tiles, steps, units, before, total;
+};
+__device__ __forceinline__ KpFound kp_find(const AttnLaunch &pre, int b)
+{
+    const int lane = threadIdx.x & 63, G = pre.Hq / pre.Hkv;
+    KpFound f{};
+    for (int c = 0; c < pre.n_groups; c += 64) {
+        const KpGroup g = kp_group(pre, min(c + lane, pre.n_groups - 1));
+        const bool some = c + lane < pre.n_groups && g.queries > 0;
+        const int n = some ? kv_shared(pre, min(g.first, pre.B - 1)) << pre.page_shift : 0;
+        const int st = kv_units(n) * pre.Hkv * (some ? g.tiles : 0);
+        const int incl = wave_scan_incl(st) + f.total;
+        const uint64_t here = __ballot(some && g.first <= b && b < g.first + g.queries / G);
+        if (here) {
+            const int x = __ffsll((unsigned long long)here) - 1;
+            f.before = __builtin_amdgcn_readlane(incl - st, x);
+            f.first = __builtin_amdgcn_readlane(g.first, x);
+            f.tiles = __builtin_amdgcn_readlane(g.tiles, x);
+            const int pages = __builtin_amdgcn_readlane(n, x);
+            f.steps = kv_steps(pages);
+            f.units = kv_units(pages);
+        }
+        f.total = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return f;
+}
+
+// Where the parts are that the shared pages left for query head qi of cache
+// head h of sequence b (none where its own part holds all): row0 is the row of
+// part_ml of the first, row1 + 2 w tile rows that of part w.
+struct KpParts {
+    int n, row0, row1;
+};
+__device__ __forceinline__ KpParts kp_parts(const AttnLaunch &pre, const KpFound &f, bool joined, int b, int h, int qi)
+{
+    KpParts p{};
+    if (f.steps == 0 || !joined) return p;
+    const int i = (b - f.first) * (pre.Hq / pre.Hkv) + qi, tile = i / pre.tile_rows, q = i - tile * pre.tile_rows;
+    const int range = kv_range(pre, f.total), u0 = f.before + (h * f.tiles + tile) * f.units;
+    // (groups that are no partition have sums past every range)
+    const int w0 = min(max(u0 / range, 0), pre.n_wg - 1), w1 = min(max((u0 + f.steps - 1) / range, w0), pre.n_wg - 1);
+    p.n = w1 - w0 + 1;
+    p.row0 = (2 * w0 + (u0 == w0 * range ? 0 : 1)) * pre.tile_rows + q;
+    p.row1 = 2 * w0 * pre.tile_rows + q;
+    return p;
+}
+// Whether sequence b leaves its shared pages to its group.
+__device__ __forceinline__ bool kp_joined(const AttnLaunch &own, int b)
+{
+    const int pages = kv_shared(own, b);
+    return pages > 0 && kv_left(own, b) == pages;
+}
+
 // Joins the parts of `per` query heads of one sequence and cache head, the own
 // parts first, then the shared pages'.  A wave looks up one head's parts and
 // forms their factors; groups of threads then take every ng-th part, 4 columns
 // a thread.
 constexpr int SJ_HEADS = 4;                   // most heads of a workgroup
 
-template <bool WIDE>
 __global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own, AttnLaunch pre, int per)
 {
     __shared__ __attribute__((aligned(16))) float red[KV_NT * 4];
@@ -326,28 +509,16 @@ __global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own,
         const size_t bq = bq0 + wave;
         Parts x{};
         int before, total;
+        const KpFound grp = kp_find(pre, b);
         kv_prefix<KV_OWN>(own, b, &before, &total);
         const KvParts p = kv_parts<KV_OWN>(own, b, h * own.q_tiles + qi / own.tile_rows, before, total);
         x.n_own = p.steps == 0 ? 0 : p.w1 - p.w0 + 1;
         x.own0 = p.first * own.tile_rows + qi % own.tile_rows;
         x.own1 = 2 * p.w0 * own.tile_rows + qi % own.tile_rows;
-        const int pages = kv_shared(own, b);
-        if (pages > 0 && kv_left(own, b) == pages) {
-            int g = -1;
-            for (int c = 0; g < 0 && c < pre.n_groups; c += 64) {
-                const int at = min(c + lane, pre.n_groups - 1);
-                const uint64_t mask = __ballot(c + lane < pre.n_groups && kv_group_first(pre, at) <= b && b < kv_group_end(pre, at));
-                if (mask) g = c + __ffsll((unsigned long long)mask) - 1;
-            }
-            if (g >= 0) {
-                kv_prefix<KV_PREFIX>(pre, g, &before, &total);
-                const int i = (b - kv_group_first(pre, g)) * G + qi, tile = i / pre.tile_rows;
-                const KvParts pp = kv_parts<KV_PREFIX>(pre, g, h * kv_tiles<KV_PREFIX>(pre, g) + tile, before, total);
-                x.n_pre = pp.steps == 0 ? 0 : pp.w1 - pp.w0 + 1;
-                x.pre0 = pp.first * pre.tile_rows + i - tile * pre.tile_rows;
-                x.pre1 = 2 * pp.w0 * pre.tile_rows + i - tile * pre.tile_rows;
-            }
-        }
+        const KpParts pp = kp_parts(pre, grp, kp_joined(own, b), b, h, qi);
+        x.n_pre = pp.n;
+        x.pre0 = pp.row0;
+        x.pre1 = pp.row1;
         const int n = x.n_own + x.n_pre, own_step = 2 * own.tile_rows, pre_step = 2 * pre.tile_rows;
         auto ml = [&](int w) -> const float * {
             if (w < x.n_own) return x.n_own == 1 ? own_full_ml + 2 * bq : own_ml + 2 * (size_t)(w == 0 ? x.own0 : x.own1 + w * own_step);
@@ -383,10 +554,7 @@ __global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own,
     if (mine) {
         const Parts x = parts[v];
         const size_t bq = bq0 + v;
-        // (the wide kernel's parts: lanes side by side, 32 queries at a time)
-        auto at = [&](size_t q) {
-            return WIDE ? (q >> 5) * 32 * own.out_cols + ((size_t)(col >> 1) * 64 + (col & 1) * 32 + (q & 31)) * 4 : q * own.Dv + 4 * col;
-        };
+        auto at = [&](size_t q) { return q * own.Dv + 4 * col; };
         auto add = [&](const float *part, const float *full, int n, int row0, int row1, int step, const float *f) {
             if (n == 1) {
                 if (sub == 0) acc += *reinterpret_cast<const f32x4 *>(full + bq * own.Dv + 4 * col) * f[0];
@@ -410,6 +578,108 @@ __global__ __launch_bounds__(KV_NT) void attn_shared_join_kernel(AttnLaunch own,
                 u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
         else *reinterpret_cast<f32x4 *>((float *)own.out + to) = acc * inv;
     }
+}
+
+// Joins the latent kernel's parts, whose lanes lie side by side: a workgroup
+// takes 32 query heads of a sequence and COLS 32-column tiles, so that it reads
+// whole lines of them.
+template <int DV, int COLS>
+__global__ __launch_bounds__(KV_NT) void attn_shared_wide_join_kernel(AttnLaunch own, AttnLaunch pre)
+{
+    constexpr int COL_SPLIT = DV / 32 / COLS, NF = KV_NT / 32;
+    __shared__ float factor[2 * KW_MAX_WG + 2][32], red[NF][32];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, ql = lane & 31, hi = lane >> 5, grp = tid >> 5;
+    const int G = own.Hq / own.Hkv, tiles = (G + 31) / 32;
+    int at = blockIdx.x;
+    const int cs = at % COL_SPLIT;
+    at /= COL_SPLIT;
+    const int q0 = at % tiles * 32;
+    at /= tiles;
+    const int h = at % own.Hkv, b = at / own.Hkv, nq = min(32, G - q0), qi = q0 + min(ql, nq - 1);
+    const size_t bq = (size_t)b * own.Hq + h * G + qi;
+    const KpFound f = kp_find(pre, b);
+    int before, total;
+    kv_prefix<KV_OWN>(own, b, &before, &total);
+    const KvParts p = kv_parts<KV_OWN>(own, b, h * own.q_tiles + q0 / own.tile_rows, before, total);
+    const KpParts pp = kp_parts(pre, f, kp_joined(own, b), b, h, qi);        // (a lane's own: tiles of a group may end among the heads)
+    const int n_own = p.steps == 0 ? 0 : p.w1 - p.w0 + 1;
+    int most = pp.n;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) most = max(most, __shfl_xor(most, off));
+    const int n = n_own + most;
+    // rows of the parts' references; of a row that is not cut its query's
+    auto own_row = [&](int w) { return (size_t)p.slot(p.w0 + w) * own.tile_rows + qi % own.tile_rows; };
+    auto pre_row = [&](int w) { return (size_t)(w == 0 ? pp.row0 : pp.row1 + 2 * w * pre.tile_rows); };
+    auto ml = [&](int w, float &m, float &l) {
+        m = -INFINITY;
+        l = 0.f;
+        if (w < n_own) {
+            const float *x = n_own == 1 ? own.full_ml + 2 * bq : own.part_ml + 2 * own_row(w);
+            m = x[0], l = x[1];
+        } else if (w - n_own < pp.n) {
+            const float *x = pp.n == 1 ? pre.full_ml + 2 * bq : pre.part_ml + 2 * pre_row(w - n_own);
+            m = x[0], l = x[1];
+        }
+    };
+    float mx = -INFINITY;
+    for (int w = grp; w < n; w += NF) {
+        float m, l;
+        ml(w, m, l);
+        mx = fmaxf(mx, m);
+    }
+    red[grp][ql] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NF; ++x) mx = fmaxf(mx, red[x][ql]);
+    __syncthreads();
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    for (int w = grp; w < n; w += NF) {
+        float m, l;
+        ml(w, m, l);
+        const float x = __builtin_amdgcn_exp2f(m - ref);
+        sum += l * x;
+        factor[w][ql] = x;
+    }
+    red[grp][ql] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < NF; ++x) sum += red[x][ql];
+
+    // wave i holds the i-th 8 columns of each tile: its lanes' are 8 i + 4 hi + 0..3
+    f32x4 acc[COLS];
+#pragma unroll
+    for (int x = 0; x < COLS; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto lanes = [&](size_t row) { return (row >> 5) * (32 * DV) + ((size_t)(cs * COLS * 4 + wave) * 64 + hi * 32 + (row & 31)) * 4; };
+    auto add = [&](const float *part, const float *full, int n, int w, size_t row, float f) {
+        if (n == 1) {
+#pragma unroll
+            for (int x = 0; x < COLS; ++x) {
+                const int d = 32 * (cs * COLS + x) + 8 * wave + 4 * hi;
+                if (d < own.Dv) acc[x] += *reinterpret_cast<const f32x4 *>(full + bq * own.Dv + d) * f;
+            }
+            return;
+        }
+        const float *src = part + lanes(row);
+#pragma unroll
+        for (int x = 0; x < COLS; ++x) acc[x] += *reinterpret_cast<const f32x4 *>(src + x * 1024) * f;
+    };
+#pragma unroll 4
+    for (int w = 0; w < n_own; ++w) add(own.part_o, own.full_o, n_own, w, own_row(w), factor[w][ql]);
+#pragma unroll 4
+    for (int w = 0; w < most; ++w)
+        if (w < pp.n) add(pre.part_o, pre.full_o, pp.n, w, pre_row(w), factor[n_own + w][ql]);
+    if (ql >= nq) return;
+    const float inv = kv_inverse(sum);
+#pragma unroll
+    for (int x = 0; x < COLS; ++x) {
+        const int d = 32 * (cs * COLS + x) + 8 * wave + 4 * hi;
+        if (d < own.Dv)
+            *reinterpret_cast<u32x2 *>((uint16_t *)own.out + bq * own.Dv + d) =
+                u32x2{pack_bf16(acc[x][0] * inv, acc[x][1] * inv), pack_bf16(acc[x][2] * inv, acc[x][3] * inv)};
+    }
+    if (cs == 0 && wave == 0 && hi == 0) kv_write_lse(own, bq, mx, sum);
 }
 
 SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, bool latent, int n_groups, int entries)
@@ -443,7 +713,8 @@ SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, b
         // Two query tiles and more: through LDS.
         if (bf16 && d <= 256 && queries > 32) {
             s.pre.wide = true;                // (tier: the widths, as above)
-            s.pre.wq = queries <= 64 ? 2 : queries <= 128 || d > 192 || (d > 128 && Dv > 128) ? 4 : 8;
+            const bool narrow = d <= 128 || (Dk <= 192 && Dv <= 128);        // (256-wide rows: four waves, all with queries of their own)
+            s.pre.wq = !narrow ? 4 : queries <= 64 && d <= 128 ? 2 : queries <= 128 ? 4 : 8;
             s.pre.tile_rows = 32 * s.pre.wq;
             s.pre.n_wg = KW_MAX_WG;
             s.pre.min_units = KV_ROW_UNITS;
@@ -486,10 +757,10 @@ static void launch_wide(const AttnLaunch &a, int wq, hipStream_t st)
 template <int DK, int DV, int NW>
 static void launch_prefix(const AttnLaunch &a, int wq, hipStream_t st)
 {
-    // (192-wide keys: six stages in LDS, too few for four at a time)
-    constexpr int N2 = DK == 192 ? 4 : NW;
-    if (wq == 2) attn_prefix_kernel<DK, DV, 2, N2><<<a.n_wg, 64 * N2, 0, st>>>(a);
-    else if (wq == 4) attn_prefix_kernel<DK, DV, 4, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
+    if constexpr (NW == 8 && DK < 192) {      // (two stages a round: LDS does not hold three rounds of four)
+        if (wq == 2) return attn_prefix_kernel<DK, DV, 2, 4><<<a.n_wg, 256, 0, st>>>(a);
+    }
+    if (wq == 4) attn_prefix_kernel<DK, DV, 4, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
     else if constexpr (NW == 8) attn_prefix_kernel<DK, DV, 8, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
 }
 
@@ -513,13 +784,17 @@ hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, cons
     } else {
         launch_part<KV_PREFIX>(pre, p.pre, st);
     }
-    // Heads of a join's workgroup: more share what is looked up, fewer are more workgroups.
     const int G = own.Hq / own.Hkv;
+    if (p.own.wide) {
+        const int tiles = own.B * own.Hkv * ((G + 31) / 32);
+        if (p.own.out_cols == 256) attn_shared_wide_join_kernel<256, 2><<<tiles * 4, KV_NT, 0, st>>>(own, pre);
+        else attn_shared_wide_join_kernel<512, 2><<<tiles * 8, KV_NT, 0, st>>>(own, pre);
+        return hipGetLastError();
+    }
+    // Heads of a workgroup: more share what is looked up, fewer are more workgroups.
     int per = SJ_HEADS;
     while (per > 1 && (per * (own.Dv / 4) > KV_NT || per > G || own.B * own.Hq / per < 512)) per /= 2;
-    const int n_join = own.B * own.Hkv * ((G + per - 1) / per);
-    if (p.own.wide) attn_shared_join_kernel<true><<<n_join, KV_NT, 0, st>>>(own, pre, per);
-    else attn_shared_join_kernel<false><<<n_join, KV_NT, 0, st>>>(own, pre, per);
+    attn_shared_join_kernel<<<own.B * own.Hkv * ((G + per - 1) / per), KV_NT, 0, st>>>(own, pre, per);
     return hipGetLastError();
 }
 
