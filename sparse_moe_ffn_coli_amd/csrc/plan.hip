@@ -8,9 +8,10 @@
 // of the step's rows lies; the shares are then written flat, an entry a
 // thread, whose owner is found by halving over the sums in LDS.  What bounds
 // it is the chain of dependent reads (lengths, sums, ring, slots), so one
-// workgroup does all of it and nothing is synchronised across workgroups;
-// only the rows of large steps, which are most of the bytes, are left to a
-// second launch of many workgroups.
+// workgroup does all of it and nothing is synchronised across workgroups; the
+// rows and new table entries of large steps, which are most of the bytes, are
+// left to a second launch of many workgroups, which finds the sums again from
+// the first one's outputs.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -19,9 +20,9 @@ namespace coli {
 constexpr int PL_NT = 1024;
 constexpr int PL_ROWS_NT = 256;
 constexpr int PL_EACH = 4;               // rows of a thread in the second launch
-constexpr int PL_STARTS = 4096;          // starts that its LDS holds
+constexpr int PL_STARTS = 4096;          // sequences whose sums its LDS holds (of more the first launch writes the tables)
 // Rows that the first launch writes itself (one workgroup, 12 bytes a row and
-// a halving over the sums).
+// a halving over the sums: 10351 rows 16 us, 11.5 in two launches).
 constexpr int PL_ONE_LAUNCH = 4096;
 
 // Sums saturate at 2^31 - 1, past every ring (2^30 pages) and step (2^25
@@ -99,7 +100,7 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanLaunch &a, int b)
 // In place (new_lens = lens, new_state = state) is safe: the state is read by
 // everyone before the first barrier and written behind the last, a length by
 // the thread that writes it.
-__global__ __launch_bounds__(PL_NT) void kv_plan_kernel(PlanLaunch a, bool rows_too)
+__global__ __launch_bounds__(PL_NT) void kv_plan_kernel(PlanLaunch a, bool rows_too, bool table_too)
 {
     __shared__ uint32_t ws[3][3][PL_NT / 64];
     __shared__ uint32_t sum_a[PL_NT], sum_b[PL_NT];          // inclusive sums of the chunk's sequences
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(PL_NT) void kv_plan_kernel(PlanLaunch a, bool rows_
             a.start[b] = (int)min(upto_t - news, granted[1]);
         }
         // The table's new entries.
-        for (uint32_t i = pages + tid; i < end_p; i += PL_NT) {
+        for (uint32_t i = pages + tid; table_too && i < end_p; i += PL_NT) {
             const int x = sum_owner(sum_a, PL_NT, i - pages);
             const uint32_t before = x ? sum_a[x - 1] : 0u;
             a.table[(size_t)(b0 + x) * a.max_pages + at_a[x] + (int)(i - pages - before)] = a.ring[wrap(head + i)];
@@ -206,17 +207,38 @@ __global__ __launch_bounds__(PL_NT) void kv_plan_kernel(PlanLaunch a, bool rows_
 }
 
 // The rows of a large step, PL_EACH a thread: the sequence of the first is
-// found by halving over the starts, the next ones follow it.
+// found by halving over the starts, the next ones follow it.  A new page's
+// first position is a new token's: its row writes the table's entry (TABLE;
+// the pages taken before a sequence are the sum, over the sequences before, of
+// what their new tokens needed more than their old lengths held).
+template <bool TABLE>
 __global__ __launch_bounds__(PL_ROWS_NT) void kv_plan_rows_kernel(PlanLaunch a)
 {
-    __shared__ int32_t starts[PL_STARTS + 1];
+    __shared__ int32_t starts[TABLE ? PL_STARTS + 1 : 1], taken[TABLE ? PL_STARTS + 1 : 1], ws[PL_ROWS_NT / 64];
     const int tid = threadIdx.x;
-    const bool lds = a.B <= PL_STARTS;
-    if (lds) {
-        for (int i = tid; i <= a.B; i += PL_ROWS_NT) starts[i] = a.start[i];
+    const uint32_t N = (uint32_t)a.n_pages;
+    uint32_t head = 0;
+    if constexpr (TABLE) {
+        int sum = 0;                                         // of the chunks before
+        for (int c = 0; c < a.B; c += PL_ROWS_NT) {
+            const int b = c + tid;
+            int more = 0;
+            if (b < a.B) {
+                const int s0 = a.start[b], news = a.start[b + 1] - s0, t = a.new_lens[b];
+                more = ((t + (1 << a.page_shift) - 1) >> a.page_shift) - ((t - news + (1 << a.page_shift) - 1) >> a.page_shift);
+                starts[b] = s0;
+            }
+            const int incl = block_scan_incl<PL_ROWS_NT / 64>(more, ws) + sum;
+            if (b < a.B) taken[b] = incl - more;
+            sum += ws[PL_ROWS_NT / 64 - 1];
+            __syncthreads();                                 // ws is free again
+        }
+        if (tid == 0) starts[a.B] = a.start[a.B];
         __syncthreads();
+        head = (uint32_t)a.new_state[0] + (N - (uint32_t)sum);       // the ring's head before the step
+        if (head >= N) head -= N;
     }
-    auto start = [&](int i) { return lds ? starts[i] : a.start[i]; };
+    auto start = [&](int i) { return TABLE ? starts[TABLE ? i : 0] : a.start[i]; };
     const int live = start(a.B);
     const int r0 = (blockIdx.x * PL_ROWS_NT + tid) * PL_EACH;
     if (r0 >= a.rows) return;
@@ -231,7 +253,13 @@ __global__ __launch_bounds__(PL_ROWS_NT) void kv_plan_rows_kernel(PlanLaunch a)
             else hi = mid;
         }
         int end = start(b + 1), shift = a.new_lens[b] - end; // position of row r: r + shift
-        int col = -1, id = -1;
+        int held = 0, col = -1, id = -1;
+        auto sequence = [&] {
+            shift = a.new_lens[b] - end;
+            held = (start(b) + shift + (1 << a.page_shift) - 1) >> a.page_shift;
+            col = -1;
+        };
+        sequence();
 #pragma unroll
         for (int x = 0; x < PL_EACH; ++x) {
             const int r = r0 + x;
@@ -239,14 +267,20 @@ __global__ __launch_bounds__(PL_ROWS_NT) void kv_plan_rows_kernel(PlanLaunch a)
             if (r >= end) {
                 do end = start(++b + 1);
                 while (r >= end);
-                shift = a.new_lens[b] - end;
-                col = -1;
+                sequence();
             }
             const int p = r + shift;
+            int32_t *entry = a.table + (size_t)b * a.max_pages + (p >> a.page_shift);
             if ((p >> a.page_shift) != col) {
                 col = p >> a.page_shift;
-                id = a.table[(size_t)b * a.max_pages + col];
+                if (!TABLE || col < held) {
+                    id = *entry;
+                } else {
+                    uint32_t i = head + (uint32_t)(taken[TABLE ? b : 0] + col - held);
+                    id = a.ring[i >= N ? i - N : i];
+                }
             }
+            if (TABLE && col >= held && (p & ((1 << a.page_shift) - 1)) == 0) *entry = id;
             pos[x] = p;
             slot[x] = id >= 0 && id < a.n_pages ? (id << a.page_shift) | (p & ((1 << a.page_shift) - 1)) : -1;
         }
@@ -265,10 +299,13 @@ __global__ __launch_bounds__(PL_ROWS_NT) void kv_plan_rows_kernel(PlanLaunch a)
 hipError_t launch_kv_plan(const PlanLaunch &a, hipStream_t st)
 {
     const bool one = a.rows <= PL_ONE_LAUNCH;
-    kv_plan_kernel<<<1, PL_NT, 0, st>>>(a, one);
+    const bool sums = a.B <= PL_STARTS;
+    kv_plan_kernel<<<1, PL_NT, 0, st>>>(a, one, one || !sums);
     if (!one) {
         constexpr int per = PL_ROWS_NT * PL_EACH;
-        kv_plan_rows_kernel<<<(a.rows + per - 1) / per, PL_ROWS_NT, 0, st>>>(a);
+        const int n = (a.rows + per - 1) / per;
+        if (sums) kv_plan_rows_kernel<true><<<n, PL_ROWS_NT, 0, st>>>(a);
+        else kv_plan_rows_kernel<false><<<n, PL_ROWS_NT, 0, st>>>(a);
     }
     return hipGetLastError();
 }
