@@ -466,6 +466,10 @@ class KvShape:
     max_pages: int
     dtype: int = COLI_BF16
 
+    def __getstate__(self):
+        # a copy forms its own C form
+        return {n: v for n, v in self.__dict__.items() if n != "_ref"}
+
     def c(self) -> CKvShape:
         return CKvShape(self.B, self.Hq, self.Hkv, self.Dk, self.Dv, self.page, self.n_pages, self.max_pages,
                         self.dtype)
@@ -502,6 +506,15 @@ def _kv_arg(where: str, at: int, name: str, t, dtype, size) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
     return t.data_ptr()
+
+
+def _shape_ref(shape: KvShape):
+    """Reference to a shape's C form, formed once (a shape's fields do not change)."""
+    ref = shape.__dict__.get("_ref")
+    if ref is None:
+        ref = C.byref(shape.c())
+        object.__setattr__(shape, "_ref", ref)
+    return ref
 
 
 def _kv_handles(where: str, shape: KvShape, cache: KvCache):
@@ -617,22 +630,18 @@ def coli_kv_plan(shape: KvShape, table, lens, want, ring, state, start, slot, po
     [4], start [B + 1], slot and pos [rows].  new_lens or new_state None: lens or state is written in place."""
     me = "coli_kv_plan"
     import torch
-    i32, B, rows = torch.int32, (shape.B,), slot.shape
-    if ring.device.type != "cuda":
+    i32, arg, at, B, rows = torch.int32, _kv_arg, ring.get_device(), (shape.B,), slot.shape
+    if at < 0:
         raise ValueError(f"{me}: ring must be on a GPU, not on {ring.device}")
     if len(rows) != 1:
         raise ValueError(f"{me}: slot must have one dimension")
-    at = ring.get_device()
-
-    def arg(name, t, size):
-        return _kv_arg(me, at, name, t, i32, size)
-
-    plens, pstate = arg("lens", lens, B), arg("state", state, (4,))
-    _kv_call(torch, me, at, stream, C.byref(shape.c()), arg("table", table, (shape.B, shape.max_pages)), plens,
-             arg("want", want, B), arg("shared", shared, B), arg("ring", ring, (shape.n_pages,)), pstate,
-             plens if new_lens is None else arg("new_lens", new_lens, B),
-             pstate if new_state is None else arg("new_state", new_state, (4,)), arg("start", start, (shape.B + 1,)), rows[0],
-             arg("slot", slot, rows), arg("pos", pos, rows))
+    plens, pstate = arg(me, at, "lens", lens, i32, B), arg(me, at, "state", state, i32, (4,))
+    _kv_call(torch, me, at, stream, _shape_ref(shape), arg(me, at, "table", table, i32, (shape.B, shape.max_pages)), plens,
+             arg(me, at, "want", want, i32, B), arg(me, at, "shared", shared, i32, B), arg(me, at, "ring", ring, i32, (shape.n_pages,)),
+             pstate, plens if new_lens is None else arg(me, at, "new_lens", new_lens, i32, B),
+             pstate if new_state is None else arg(me, at, "new_state", new_state, i32, (4,)),
+             arg(me, at, "start", start, i32, (shape.B + 1,)), rows[0], arg(me, at, "slot", slot, i32, rows),
+             arg(me, at, "pos", pos, i32, rows))
 
 
 ROPE_SCALINGS = ("plain", "linear", "ntk", "yarn")
@@ -657,6 +666,12 @@ class Rope:
     interleaved: bool = False
     amp: float = 1.0
 
+    def c(self, where: str, at: int, f64) -> CRope:
+        n = self.freq.shape
+        if len(n) != 1:
+            raise ValueError(f"{where}: rope.freq must have one dimension")
+        return CRope(_kv_arg(where, at, "rope.freq", self.freq, f64, n), 2 * n[0], self.rot_at, 1 if self.interleaved else 0, self.amp)
+
 
 @dataclass(frozen=True)
 class QkNorm:
@@ -664,6 +679,12 @@ class QkNorm:
     q_w: object = None
     k_w: object = None
     eps: float = 1e-6
+
+    def c(self, where: str, at: int, dt) -> CQkNorm:
+        n = (self.k_w if self.q_w is None else self.q_w).shape
+        if len(n) != 1:
+            raise ValueError(f"{where}: the norm's weights must have one dimension")
+        return CQkNorm(_kv_arg(where, at, "norm.q_w", self.q_w, dt, n), _kv_arg(where, at, "norm.k_w", self.k_w, dt, n), n[0], self.eps)
 
 
 def _kv_rows(where: str, at: int, name: str, t, dtype, size):
@@ -674,12 +695,12 @@ def _kv_rows(where: str, at: int, name: str, t, dtype, size):
         raise ValueError(f"{where}: {name} must be {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
     if t.get_device() != at:
         raise ValueError(f"{where}: {name} is on {t.device}, the other tensors on device {at}")
-    ld, *rest = t.stride()
-    H, D = size[1:]
-    if size[0] < 2:
-        ld = max(ld, H * D)                          # (of one row the stride says nothing)
-    if (D > 1 and rest[1] != 1) or (H > 1 and rest[0] != D):
+    _, H, D = size
+    ld, across, along = t.stride()
+    if (D > 1 and along != 1) or (H > 1 and across != D):
         raise ValueError(f"{where}: the heads of a row of {name} must lie side by side")
+    if size[0] < 2 and ld < H * D:                   # (of one row the stride says nothing)
+        ld = H * D
     return t.data_ptr(), ld
 
 
@@ -692,31 +713,21 @@ def coli_kv_rope(shape: KvShape, q, k, v, q_out, pos=None, rope: Optional[Rope] 
     some = k if q is None else q
     if some is None:
         raise ValueError(f"{me}: q or k must be given")
-    if some.device.type != "cuda":
-        raise ValueError(f"{me}: the tensors must be on a GPU, not on {some.device}")
     at, rows = some.get_device(), some.shape[0]
-    dt, i32 = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32
+    if at < 0:
+        raise ValueError(f"{me}: the tensors must be on a GPU, not on {some.device}")
+    dt, i32, row, arg = torch.float32 if shape.dtype == COLI_F32 else torch.bfloat16, torch.int32, (rows,), _kv_arg
     Hq, H, Dk, Dv = shape.Hq, shape.Hkv, shape.Dk, shape.Dv
-    pool = (shape.n_pages, H, shape.page)
     pq, q_ld = _kv_rows(me, at, "q", q, dt, (rows, Hq, Dk))
     pk, k_ld = _kv_rows(me, at, "k", k, dt, (rows, H, Dk))
     pv, v_ld = _kv_rows(me, at, "v", v, dt, (rows, H, Dv))
-    cn = cr = None
-    if norm is not None and not (norm.q_w is None and norm.k_w is None):
-        n = (norm.k_w if norm.q_w is None else norm.q_w).shape
-        if len(n) != 1:
-            raise ValueError(f"{me}: the norm's weights must have one dimension")
-        cn = C.byref(CQkNorm(_kv_arg(me, at, "norm.q_w", norm.q_w, dt, n), _kv_arg(me, at, "norm.k_w", norm.k_w, dt, n), n[0], norm.eps))
-    if rope is not None:
-        n = rope.freq.shape
-        if len(n) != 1:
-            raise ValueError(f"{me}: rope.freq must have one dimension")
-        cr = C.byref(CRope(_kv_arg(me, at, "rope.freq", rope.freq, torch.float64, n), 2 * n[0], rope.rot_at,
-                           1 if rope.interleaved else 0, rope.amp))
-    _kv_call(torch, me, at, stream, C.byref(shape.c()), rows, pq, q_ld, pk, k_ld, pv, v_ld, cn, cr,
-             _kv_arg(me, at, "pos", pos, i32, (rows,)), _kv_arg(me, at, "slot", slot, i32, (rows,)),
-             _kv_arg(me, at, "q_out", q_out, dt, (rows, Hq, Dk)), _kv_arg(me, at, "k_out", k_out, dt, (rows, H, Dk)),
-             _kv_arg(me, at, "pool_k", pool_k, dt, pool + (Dk,)), _kv_arg(me, at, "pool_v", pool_v, dt, pool + (Dv,)))
+    cn = None if norm is None or (norm.q_w is None and norm.k_w is None) else C.byref(norm.c(me, at, dt))
+    cr = None if rope is None else C.byref(rope.c(me, at, torch.float64))
+    _kv_call(torch, me, at, stream, _shape_ref(shape), rows, pq, q_ld, pk, k_ld, pv, v_ld, cn, cr,
+             arg(me, at, "pos", pos, i32, row), arg(me, at, "slot", slot, i32, row),
+             arg(me, at, "q_out", q_out, dt, (rows, Hq, Dk)), arg(me, at, "k_out", k_out, dt, (rows, H, Dk)),
+             arg(me, at, "pool_k", pool_k, dt, (shape.n_pages, H, shape.page, Dk)),
+             arg(me, at, "pool_v", pool_v, dt, (shape.n_pages, H, shape.page, Dv)))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -149,13 +149,13 @@ struct KvRange {
 // False: the range is empty.  R rows a sequence (groups: 1, their units are
 // all rows').  The same for every wave.
 template <KvPart PART = KV_ALL>
-__device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg)
+__device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg, int blk = blockIdx.x)
 {
     int before, total;
     kv_prefix<PART>(a, 0, &before, &total);
     total *= R;
     const int range = kv_range(a, total);
-    const int u = blockIdx.x * range;         // below total + n_wg * (KV_ROW_UNITS + 1), and 2^31 by the host's check
+    const int u = blk * range;         // below total + n_wg * (KV_ROW_UNITS + 1), and 2^31 by the host's check
     if (u >= total) return false;
     int base = 0;
     if (PART == KV_ALL && a.idx) {
@@ -190,11 +190,11 @@ __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg
 
 // A workgroup's range, or (direct) its row, which may be empty.
 template <KvPart PART = KV_ALL>
-__device__ __forceinline__ bool kv_begin(const AttnLaunch &a, int R, KvRange &rg)
+__device__ __forceinline__ bool kv_begin(const AttnLaunch &a, int R, KvRange &rg, int blk = blockIdx.x)
 {
-    if (!a.direct) return kv_first<PART>(a, PART == KV_PREFIX ? 1 : R, rg);
-    rg.b = blockIdx.x / R;
-    rg.row = blockIdx.x - rg.b * R;
+    if (!a.direct) return kv_first<PART>(a, PART == KV_PREFIX ? 1 : R, rg, blk);
+    rg.b = blk / R;
+    rg.row = blk - rg.b * R;
     rg.n = kv_len<PART>(a, rg.b);
     rg.steps = kv_steps(rg.n);
     rg.u = rg.s0 = 0;
@@ -356,8 +356,8 @@ __device__ __forceinline__ void kv_write_empty(const AttnLaunch &a, size_t qrow,
 // NW waves; `a.direct`: a workgroup per row, none of them cut.
 // PART other than KV_ALL: rows that are not cut are left as parts too, by their
 // queries (a.full_o, a.full_ml).
-template <bool BF16, int DK, int DV, int NW, KvPart PART = KV_ALL>
-__global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
+template <bool BF16, int DK, int DV, int NW, KvPart PART>
+__device__ __forceinline__ void attn_rows(const AttnLaunch &a, int blk)
 {
     using KT = KvTile<BF16, DK, DV>;
     using T = typename KT::T;
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     const int R = a.Hkv * a.q_tiles;
 
     KvRange rg;
-    if (!kv_begin<PART>(a, R, rg)) return;
+    if (!kv_begin<PART>(a, R, rg, blk)) return;
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
 
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
         }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == steps;
-        const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+        const int slot = 2 * blk + (u == u_begin ? 0 : 1);
         // four columns of a query a thread
         for (int i = tid; i < nq * (DV / 4); i += 64 * NW) {
             const int q = i / (DV / 4), d = i % (DV / 4) * 4;
@@ -673,6 +673,12 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
         if (a.direct) return;
         __syncthreads();                      // the join buffer is free again
     }
+}
+
+template <bool BF16, int DK, int DV, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
+{
+    attn_rows<BF16, DK, DV, NW, KV_ALL>(a, blockIdx.x);
 }
 
 // Where the parts of a row are: ranges w0 .. w1 hold some of it (w0 = w1: one

@@ -139,7 +139,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     // rounded factor is off by half a step of the score, the sum of the products
     // by more.  The queries take its sign, so the largest product is the largest
     // score.
-    const float scale = a.scale_size;
+    // A scale of zero becomes zero queries (of which an infinity is no number, as its product with the scale): the
+    // scores of hidden positions are infinities.
+    const bool zero = a.scale_size == 0.f;
+    const float scale = zero ? 1.f : a.scale_size;
     const uint32_t flip = a.scale_hi < 0.f ? 0x80008000u : 0u;
     const uint32_t k_bytes = a.Dk * 2, v_bytes = a.v ? a.Dv * 2 : k_bytes;        // from a row to the next
 
@@ -249,7 +252,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qr[c][i] ^= flip;
+            for (int i = 0; i < 4; ++i) {
+                qr[c][i] ^= flip;
+                if (zero) {
+                    const uint32_t lo = (qr[c][i] & 0x7f80u) == 0x7f80u ? 0x7fc0u : 0u;
+                    qr[c][i] = lo | ((qr[c][i] & 0x7f800000u) == 0x7f800000u ? 0x7fc00000u : 0u);
+                }
+            }
             qf[c] = as_bf16(qr[c]);
         }
         // Scores and their maximum; the reference, and by what the output is to be multiplied where it has moved (only where
@@ -710,8 +719,15 @@ SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, b
         p.n_wg = 256 * (d <= (bf16 ? 128 : 64) ? 2 : 1);
         p.min_units = 4;
         s.own = s.pre = p;
-        // Two query tiles and more: through LDS.
-        if (bf16 && d <= 256 && queries > 32) {
+        // More than two query tiles, and enough work that their reading the
+        // pages once each counts for more than the LDS kernel's start and its
+        // larger parts.  Whole calls, 8 cache heads, us with tiles / through
+        // LDS: 48 queries a head, 128 wide, 512 positions 15 / 25, 4096 22 /
+        // 27, 32768 74 / 47; 96 queries 4096 26 / 30; 160 queries 512 21 / 30,
+        // 4096 36 / 36, 32768 113 / 69; 64 wide 160 queries 4096 26 / 28,
+        // 32768 81 / 51; 256 wide 96 queries 4096 46 / 47, 32768 156 / 100.
+        const long work = (long)n_groups * Hkv * ((queries + KV_QT - 1) / KV_QT) * ((entries + KV_STEP - 1) / KV_STEP);
+        if (bf16 && d <= 256 && queries > 32 && work >= 8192) {
             s.pre.wide = true;                // (tier: the widths, as above)
             const bool narrow = d <= 128 || (Dk <= 192 && Dv <= 128);        // (256-wide rows: four waves, all with queries of their own)
             s.pre.wq = !narrow ? 4 : queries <= 64 && d <= 128 ? 2 : queries <= 128 ? 4 : 8;
@@ -725,16 +741,46 @@ SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, b
     return s;
 }
 
-template <bool BF16, KvPart PART>
-static void launch_tiles(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
+// Own parts and shared pages of 16-head tiles in one launch: the shared pages'
+// ranges first (four samples of one prompt: 8.4 and 7.9 us in two).
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(KV_NT) void attn_parts_kernel(AttnLaunch own, AttnLaunch pre)
 {
-    if (p.tier == 64) attn_kernel<BF16, 64, 64, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if (p.tier == 128) attn_kernel<BF16, 128, 128, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if (p.tier == 256) attn_kernel<BF16, 256, 256, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
+    const int blk = (int)blockIdx.x - pre.n_wg;
+    if (blk < 0) attn_rows<BF16, DK, DV, KV_WAVES, KV_PREFIX>(pre, blockIdx.x);
+    else attn_rows<BF16, DK, DV, KV_WAVES, KV_OWN>(own, blk);
+}
+template <bool BF16, int DK, int DV, KvPart PART>
+__global__ __launch_bounds__(KV_NT) void attn_part_kernel(AttnLaunch a)
+{
+    attn_rows<BF16, DK, DV, KV_WAVES, PART>(a, blockIdx.x);
+}
+
+// both: the shared pages too.
+template <bool BF16, int DK, int DV>
+static void launch_tile(const AttnLaunch &own, const AttnLaunch &pre, bool both, hipStream_t st)
+{
+    if constexpr (DK > 320) {                 // (two join buffers do not fit LDS)
+        attn_part_kernel<BF16, DK, DV, KV_OWN><<<own.n_wg, KV_NT, 0, st>>>(own);
+        attn_part_kernel<BF16, DK, DV, KV_PREFIX><<<pre.n_wg, KV_NT, 0, st>>>(pre);
+    } else {
+        if constexpr (BF16) {                 // (in fp32 always both)
+            if (!both) return attn_part_kernel<BF16, DK, DV, KV_OWN><<<own.n_wg, KV_NT, 0, st>>>(own);
+        }
+        attn_parts_kernel<BF16, DK, DV><<<own.n_wg + pre.n_wg, KV_NT, 0, st>>>(own, pre);
+    }
+}
+
+template <bool BF16>
+static void launch_tiles(const AttnLaunch &own, const AttnLaunch &pre, const AttnPlan &p, bool both, hipStream_t st)
+{
+    if (p.tier == 64) launch_tile<BF16, 64, 64>(own, pre, both, st);
+    else if (p.tier == 128) launch_tile<BF16, 128, 128>(own, pre, both, st);
+    else if (p.tier == 256) launch_tile<BF16, 256, 256>(own, pre, both, st);
     else if constexpr (!BF16) {
-        if (p.tier == 192) attn_kernel<BF16, 192, 192, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-        else if (p.tier == 320) attn_kernel<BF16, 320, 256, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-        else attn_kernel<BF16, 576, 512, KV_WAVES, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
+        if (p.tier == 192) launch_tile<BF16, 192, 192>(own, pre, both, st);
+        else if (p.tier == 320) launch_tile<BF16, 320, 256>(own, pre, both, st);
+        else launch_tile<BF16, 576, 512>(own, pre, both, st);
     }
 }
 
@@ -765,24 +811,26 @@ static void launch_prefix(const AttnLaunch &a, int wq, hipStream_t st)
 }
 
 template <KvPart PART>
-static void launch_part(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
+static void launch_latent(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
 {
-    if (p.wide && p.out_cols == 256) launch_wide<320, 256, PART>(a, p.wq, st);
-    else if (p.wide) launch_wide<576, 512, PART>(a, p.wq, st);
-    else if (a.bf16) launch_tiles<true, PART>(a, p, st);
-    else launch_tiles<false, PART>(a, p, st);
+    if (p.out_cols == 256) launch_wide<320, 256, PART>(a, p.wq, st);
+    else launch_wide<576, 512, PART>(a, p.wq, st);
 }
 
 hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, const SharedPlan &p, hipStream_t st)
 {
-    launch_part<KV_OWN>(own, p.own, st);
-    if (p.pre.wide && !p.own.wide) {
-        if (p.pre.tier == 64) launch_prefix<64, 64, 8>(pre, p.pre.wq, st);
+    if (p.own.wide) {
+        launch_latent<KV_OWN>(own, p.own, st);
+        launch_latent<KV_PREFIX>(pre, p.pre, st);
+    } else {
+        const bool both = !p.pre.wide;
+        if (own.bf16) launch_tiles<true>(own, pre, p.own, both, st);
+        else launch_tiles<false>(own, pre, p.own, both, st);
+        if (both) {
+        } else if (p.pre.tier == 64) launch_prefix<64, 64, 8>(pre, p.pre.wq, st);
         else if (p.pre.tier == 128) launch_prefix<128, 128, 8>(pre, p.pre.wq, st);
         else if (pre.Dk <= 192 && pre.Dv <= 128) launch_prefix<192, 128, 8>(pre, p.pre.wq, st);
         else launch_prefix<256, 256, 4>(pre, p.pre.wq, st);
-    } else {
-        launch_part<KV_PREFIX>(pre, p.pre, st);
     }
     const int G = own.Hq / own.Hkv;
     if (p.own.wide) {

@@ -79,9 +79,10 @@ def to_np(t):
     return t.detach().cpu().to(torch.float64).numpy()
 
 
-def make_shared(groups, Hkv, Dk, Dv, page, dtype="bf16", latent=False, seed=0):
+def make_shared(groups, Hkv, Dk, Dv, page, dtype="bf16", latent=False, seed=0, room=0):
     """A cache for kv_reference.attn whose sequences share pages: groups [(pages, [positions behind them])].  A value of
-    (n,) in place of a number: a sequence of n positions all in all, within its group's pages."""
+    (n,) in place of a number: a sequence of n positions all in all, within its group's pages.  room: positions that the
+    table has columns for at least (how a call is cut goes by them)."""
     import kv_reference as kv
     tails = [t for _, ts in groups for t in ts]
     own = [0 if isinstance(t, tuple) else t for t in tails]
@@ -90,7 +91,7 @@ def make_shared(groups, Hkv, Dk, Dv, page, dtype="bf16", latent=False, seed=0):
     shared = np.repeat([p for p, _ in groups], [len(ts) for _, ts in groups]).astype(np.int32)
     group = np.repeat(np.arange(G), [len(ts) for _, ts in groups])
     mp = max(int(s) + -(-t // page) for s, t in zip(shared, own)) + 1
-    mp = max(mp, 1)
+    mp = max(mp, 1, -(-room // page))
     new = np.full((len(tails), mp), -1, np.int32)
     lens = np.zeros(len(tails), np.int32)
     for b, t in enumerate(tails):

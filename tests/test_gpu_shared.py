@@ -73,9 +73,10 @@ def test_layouts(dtype, Hq, Hkv, Dk, Dv, page, latent):
 def test_group_sizes(dtype, Hq, Hkv, Dk, Dv, latent, n):
     # from one query tile that is not full to several, beside groups of other sizes
     rng = np.random.default_rng(n)
-    c = make_shared([(20, list(rng.integers(0, 60, size=n))), (3, [9]), (11, list(rng.integers(0, 9, size=3)))], Hkv, Dk, Dv, 16, dtype,
-                    latent, seed=n)
-    run(c, Hq, 2.0 / np.sqrt(Dk))
+    for room in (0, 100000):
+        c = make_shared([(20, list(rng.integers(0, 60, size=n))), (3, [9]), (11, list(rng.integers(0, 9, size=3)))], Hkv, Dk, Dv, 16,
+                        dtype, latent, seed=n, room=room)
+        run(c, Hq, 2.0 / np.sqrt(Dk))
 
 
 @pytest.mark.parametrize("Hq,Hkv,Dk,Dv", [(8, 2, 128, 128), (4, 1, 64, 64), (8, 2, 256, 256), (4, 1, 192, 128), (4, 1, 80, 104),
@@ -84,21 +85,24 @@ def test_group_sizes(dtype, Hq, Hkv, Dk, Dv, latent, n):
 def test_one_large_group(Hq, Hkv, Dk, Dv, n, pages):
     # every number of query tiles a workgroup has, and of waves that split the positions
     rng = np.random.default_rng(n + Dk)
-    run(make_shared([(pages, list(rng.integers(0, 50, size=n)))], Hkv, Dk, Dv, 16, "bf16", seed=n), Hq, 2.0 / np.sqrt(Dk))
+    # (as wide a table as a long prefix has, and one that ends behind the sequences)
+    for room in (200000, 0):
+        run(make_shared([(pages, list(rng.integers(0, 50, size=n)))], Hkv, Dk, Dv, 16, "bf16", seed=n, room=room), Hq, 2.0 / np.sqrt(Dk))
 
 
 def test_one_large_group_of_small_pages():
     # the shared pages end inside a stage; pages that do not exist
     rng = np.random.default_rng(3)
     for page, pages in ((1, 77), (2, 1030), (8, 5)):
-        c = make_shared([(pages, list(rng.integers(0, 9, size=40)))], 1, 128, 128, page, "bf16", seed=page)
+        c = make_shared([(pages, list(rng.integers(0, 9, size=40)))], 1, 128, 128, page, "bf16", seed=page, room=60000)
         run(c, 4, 0.2)
         c["table"][:, [0, 3, pages - 1]] = -1
         run(c, 4, 0.2)
 
 
 @pytest.mark.parametrize("dtype,latent,Hq,Hkv,Dk,Dv", [("bf16", False, 8, 2, 128, 128), ("f32", False, 2, 2, 64, 64),
-                                                       ("bf16", True, 64, 1, 576, 512), ("bf16", False, 2, 1, 256, 256)])
+                                                       ("bf16", True, 64, 1, 576, 512), ("bf16", False, 2, 1, 256, 256),
+                                                       ("bf16", False, 48, 1, 128, 128), ("bf16", False, 64, 1, 64, 64)])
 def test_long_prefix(dtype, latent, Hq, Hkv, Dk, Dv):
     # cut over every range
     run(make_shared([(1251, [1, 700, 40, 3])], Hkv, Dk, Dv, 16, dtype, latent, seed=5), Hq, 2.0 / np.sqrt(Dk))
@@ -108,6 +112,7 @@ def test_long_prefix(dtype, latent, Hq, Hkv, Dk, Dv):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scales(scale, dtype):
     run(make_shared([(30, [9, 100, 0]), (2, [1, 1])], 2, 128, 128, 16, dtype, seed=4), 8, scale)
+    run(make_shared([(30, [9, 100, 0] * 5), (2, [1, 1])], 2, 128, 128, 16, dtype, seed=4, room=100000), 16, scale)
     run(make_shared([(30, [9, 100, 0]), (2, [1, 1])], 1, 576, 512, 16, dtype, True, seed=4), 16, scale / 3)
 
 
@@ -116,6 +121,8 @@ def test_many_sequences_and_groups(dtype, Hq, Hkv, D):
     rng = np.random.default_rng(6)
     groups = [(int(rng.integers(0, 12)), [int(x) if x < 40 else (0,) for x in rng.integers(0, 50, size=rng.integers(1, 9))]) for _ in range(130)]
     run(make_shared(groups, Hkv, D, D, 8, dtype, seed=6), Hq, 0.2)
+    if D == 128:
+        run(make_shared(groups[:70], Hkv, D, D, 8, dtype, seed=6, room=3000), 20, 0.2)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -135,8 +142,8 @@ def test_hidden_pages(dtype, latent, Hq, Dk, Dv):
 def test_values_outside_a_query_do_not_reach_it():
     """NaN and infinities in shared rows behind a short sequence's end, in other sequences' rows, behind the lengths."""
     import torch
-    for latent, Hq, Dk, Dv in ((False, 8, 128, 128), (True, 32, 576, 512)):
-        c = make_shared([(8, [5, (70,), (0,), 0]), (2, [9])], 1 if latent else 2, Dk, Dv, 16, "bf16", latent, seed=11)
+    for latent, Hq, Dk, Dv, room in ((False, 8, 128, 128, 0), (False, 40, 128, 128, 200000), (True, 32, 576, 512, 0)):
+        c = make_shared([(8, [5, (70,), (0,), 0]), (2, [9])], 1 if latent else 2, Dk, Dv, 16, "bf16", latent, seed=11, room=room)
         a = run(c, Hq, 0.1)
         for pool in (c["k"], c["v"]):
             if pool is not None:
@@ -151,27 +158,28 @@ def test_values_outside_a_query_do_not_reach_it():
 def test_infinite_and_missing_scores():
     import torch
     for dtype in ("bf16", "f32"):
-        c = make_shared([(4, [20, 33, 0]), (4, [3])], 1, 64, 64, 16, dtype, seed=12)
-        q = queries(c, 4, 2)
-        q[:, :, 1:] = 0
-        q[:, :, 0] = 1
-        c["k"][:, :, :, 0] = float("-inf")
-        out, lse = run(c, 2, 0.5, q=q, want=False)                     # no weight anywhere
-        assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
-        c["k"][c["table"][0, 2].long(), :, 7, 0] = 3.0                 # one score in the first group's pages
-        out, lse = run(c, 2, 0.5, q=q, want=False)
-        v = c["v"][c["table"][0, 2].long(), 0, 7]
-        assert bool((out[:3] == v).all()) and torch.allclose(lse[:3], torch.full_like(lse[:3], 1.5)) and bool((out[3] == 0).all())
-        c["k"][c["table"][0, 2].long(), :, 9, 0] = float("inf")
-        out, lse = run(c, 2, 0.5, q=q, want=False)
-        assert bool(lse[:3].isnan().all()) and bool(out[:3].isnan().all()) and bool((lse[3] == float("-inf")).all())
+        for Hq, room in ((2, 0), (40, 300000)):
+            c = make_shared([(4, [20, 33, 0]), (4, [3])], 1, 64, 64, 16, dtype, seed=12, room=room)
+            q = queries(c, 4, Hq)
+            q[:, :, 1:] = 0
+            q[:, :, 0] = 1
+            c["k"][:, :, :, 0] = float("-inf")
+            out, lse = run(c, Hq, 0.5, q=q, want=False)                     # no weight anywhere
+            assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+            c["k"][c["table"][0, 2].long(), :, 7, 0] = 3.0                 # one score in the first group's pages
+            out, lse = run(c, Hq, 0.5, q=q, want=False)
+            v = c["v"][c["table"][0, 2].long(), 0, 7]
+            assert bool((out[:3] == v).all()) and torch.allclose(lse[:3], torch.full_like(lse[:3], 1.5)) and bool((out[3] == 0).all())
+            c["k"][c["table"][0, 2].long(), :, 9, 0] = float("inf")
+            out, lse = run(c, Hq, 0.5, q=q, want=False)
+            assert bool(lse[:3].isnan().all()) and bool(out[:3].isnan().all()) and bool((lse[3] == float("-inf")).all())
 
 
 def test_the_largest_score_anywhere():
     """A score far above the rest, in the pages or behind them, early or late."""
-    for latent, Hq, Dk, Dv in ((False, 16, 128, 128), (True, 16, 576, 512)):
+    for latent, Hq, Dk, Dv, room in ((False, 16, 128, 128, 0), (False, 16, 128, 128, 200000), (False, 16, 256, 256, 200000), (True, 16, 576, 512, 0)):
         for pos in (0, 40, 511, 512, 520):
-            c = make_shared([(32, [30, 31, 45, 9, 10, 11])], 1, Dk, Dv, 16, "bf16", latent, seed=pos)
+            c = make_shared([(32, [30, 31, 45, 9, 10, 11])], 1, Dk, Dv, 16, "bf16", latent, seed=pos, room=room)
             for b in range(6):
                 c["k"][c["table"][b, pos // 16].long(), :, pos % 16] *= 30
             run(c, Hq, 1.0)
@@ -195,12 +203,13 @@ def test_like_the_attention_over_each_row():
 def test_groups_that_are_no_partition_stay_inside():
     """Descending borders, borders outside the batch, counts outside the table: no fault, nothing outside the outputs."""
     import torch
-    c = make_shared([(8, [5, 9]), (2, [9, 1, 4])], 2, 64, 64, 16, "bf16", seed=14)
-    for start in ([0, -5, 99], [3, 1, 0], [5, 5, 5], [0, 5, 0], [2, 4, 4]):
-        for shared in ([8, 8, 2, 2, 2], [-1, 100, 0, 1 << 30, -(1 << 31)]):
-            c["group_start"], c["shared"] = torch.tensor(start, dtype=torch.int32), torch.tensor(shared, dtype=torch.int32)
-            c["table"] = c["table"].clamp(min=0)
-            run(c, 4, 0.1, want=False)
+    for Hq, room in ((4, 0), (80, 200000)):
+        c = make_shared([(8, [5, 9]), (2, [9, 1, 4])], 2, 64, 64, 16, "bf16", seed=14, room=room)
+        for start in ([0, -5, 99], [3, 1, 0], [5, 5, 5], [0, 5, 0], [2, 4, 4]):
+            for shared in ([8, 8, 2, 2, 2], [-1, 100, 0, 1 << 30, -(1 << 31)]):
+                c["group_start"], c["shared"] = torch.tensor(start, dtype=torch.int32), torch.tensor(shared, dtype=torch.int32)
+                c["table"] = c["table"].clamp(min=0)
+                run(c, Hq, 0.1, want=False)
 
 
 def test_repeats_streams_and_graphs():
@@ -208,11 +217,15 @@ def test_repeats_streams_and_graphs():
     c = make_shared([(100, [300, 17, 9, 1]), (7, [4])], 2, 128, 128, 16, "bf16", seed=16)
     a = run(c, 8, 0.2, want=False)
     side = torch.cuda.Stream()
+    wide = make_shared([(100, [300, 17, 9, 1] * 8), (7, [4])], 2, 128, 128, 16, "bf16", seed=16, room=200000)
+    for _ in range(3):
+        x, y = run(wide, 8, 0.2, want=False), run(wide, 8, 0.2, want=False, stream=side)
+        assert torch.equal(bits(x[0]), bits(y[0])) and torch.equal(bits(x[1]), bits(y[1]))
     for st in (None, side, None):
         b = run(c, 8, 0.2, want=False, stream=st)
         assert torch.equal(bits(a[0]), bits(b[0])) and torch.equal(bits(a[1]), bits(b[1]))
-    for latent, Hq, Hkv, Dk, Dv in ((False, 8, 2, 128, 128), (True, 64, 1, 576, 512)):
-        c = make_shared([(30, [40, 17, 9, 1]), (7, [4])], Hkv, Dk, Dv, 16, "bf16", latent, seed=17)
+    for latent, Hq, Hkv, Dk, Dv, room in ((False, 8, 2, 128, 128, 0), (False, 64, 2, 128, 128, 200000), (True, 64, 1, 576, 512, 0)):
+        c = make_shared([(30, [40, 17, 9, 1]), (7, [4])], Hkv, Dk, Dv, 16, "bf16", latent, seed=17, room=room)
         s, cache, shared, start = handles(c, Hq)
         q = queries(c, 5, Hq).cuda()
         # two captured calls, each with a workspace, replayed at once
