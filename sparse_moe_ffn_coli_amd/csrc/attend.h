@@ -123,11 +123,15 @@ __device__ __forceinline__ void kv_prefix(const AttnLaunch &a, int b, int *befor
     }
     const int lane = threadIdx.x & 63;
     int lo = 0, all = 0;
+    bool falls = false;
     for (int i = lane; i < kv_items<PART>(a); i += 64) {
         const int st = kv_item_units<PART>(a, i);
         all += st;
         lo += (i < b) ? st : 0;
+        if constexpr (PART == KV_PREFIX) falls |= kv_group_end(a, i) < kv_group_first(a, i);
     }
+    // Borders that fall somewhere can count sequences any number of times, past 2^31 units: nothing is taken.
+    if (PART == KV_PREFIX && __ballot(falls)) lo = all = 0;
     *before = __builtin_amdgcn_readlane(wave_scan_incl(lo), 63);
     *total = __builtin_amdgcn_readlane(wave_scan_incl(all), 63);
 }

@@ -78,6 +78,7 @@ __device__ __forceinline__ bool kp_first(const AttnLaunch &a, KvRange &rg, KpGro
     }
     const int lane = threadIdx.x & 63;
     const KpGroup g = kp_group(a, min(lane, a.n_groups - 1));
+    if (__ballot(g.queries < 0)) return false;               // (as in kv_prefix)
     const bool some = lane < a.n_groups && g.queries > 0;
     const int n = some ? kv_shared(a, min(g.first, a.B - 1)) << a.page_shift : 0;
     const int st = kv_units(n) * a.Hkv * (some ? g.tiles : 0);

@@ -212,6 +212,43 @@ def test_groups_that_are_no_partition_stay_inside():
                 run(c, Hq, 0.1, want=False)
 
 
+@pytest.mark.parametrize("dtype,latent,n_groups", [("bf16", False, 64), ("bf16", False, 400), ("f32", False, 300), ("bf16", True, 64)])
+def test_falling_borders_of_more_units_than_a_number_holds(dtype, latent, n_groups):
+    """Borders 0, B, 0, B, .. of 4096 sequences count the batch n_groups / 2 times: some 2^33 units."""
+    import torch
+    B, Hq, page, mp, Dk, Dv = 4096, 8, 4096, 63, 264 if latent else 8, 8
+    Hkv = 1 if latent else 8
+    s = KvShape(B, Hq, Hkv, Dk, Dv, page, 2, mp, COLI_F32 if dtype == "f32" else COLI_BF16)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    zeros = lambda *n, dt=torch.int32: torch.zeros(n, dtype=dt, device="cuda")
+    cache = KvCache(zeros(2, Hkv, page, Dk, dt=dt), None if latent else zeros(2, Hkv, page, Dv, dt=dt), zeros(B, mp), zeros(B))
+    start = zeros(n_groups + 1)
+    start[1::2] = B
+    q, out, lse = zeros(B, Hq, Dk, dt=dt), zeros(B, Hq, Dv, dt=dt), zeros(B, Hq, dt=torch.float32)
+    ws = zeros(coli_kv_attn_shared_workspace_bytes(s, n_groups), dt=torch.uint8)
+    coli_kv_attn_shared(s, q, cache, out, 0.1, zeros(B) + mp, start, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == -np.inf).all())       # (no sequence has a position)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 40), (128, 128), (128, 64), (96, 72)])
+@pytest.mark.parametrize("n", [11, 30, 70])
+def test_narrow_latent_groups_of_many_heads(Dk, Dv, n):
+    rng = np.random.default_rng(n)
+    c = make_shared([(70, list(rng.integers(0, 50, size=n))), (2, [5])], 1, Dk, Dv, 16, "bf16", True, seed=n, room=200000)
+    run(c, 8, 2.0 / np.sqrt(Dk))
+
+
+def test_no_sequences():
+    import torch
+    s = KvShape(0, 4, 2, 64, 64, 16, 4, 2, COLI_F32)
+    z = lambda *n, dt=torch.float32: torch.zeros(n, dtype=dt, device="cuda")
+    i = lambda *n: z(*n, dt=torch.int32)
+    cache = KvCache(z(4, 2, 16, 64), z(4, 2, 16, 64), i(0, 2), i(0))
+    coli_kv_attn_shared(s, z(0, 4, 64), cache, z(0, 4, 64), 0.1, i(0), i(1), ws=z(coli_kv_attn_shared_workspace_bytes(s, 0), dt=torch.uint8))
+    torch.cuda.synchronize()
+
+
 def test_repeats_streams_and_graphs():
     import torch
     c = make_shared([(100, [300, 17, 9, 1]), (7, [4])], 2, 128, 128, 16, "bf16", seed=16)
