@@ -597,7 +597,7 @@ def coli_kv_attn_shared(shape: KvShape, q, cache: KvCache, out, scale: float, sh
     """q [B][Hq][Dk], out [B][Hq][Dv], lse fp32 [B][Hq], shared int32 [B], group_start int32 [n_groups + 1]."""
     me = "coli_kv_attn_shared"
     cs, cc, dt, at, torch = _kv_handles(me, shape, cache)
-    B, Hq, i32, groups = shape.B, shape.Hq, torch.int32, group_start.shape
+    B, Hq, i32, groups = shape.B, shape.Hq, torch.int32, () if group_start is None else group_start.shape
     if len(groups) != 1 or groups[0] < 1:
         raise ValueError(f"{me}: group_start must have one dimension and at least one entry")
     if ws is not None and ws.get_device() != at:
@@ -630,6 +630,8 @@ def coli_kv_plan(shape: KvShape, table, lens, want, ring, state, start, slot, po
     [4], start [B + 1], slot and pos [rows].  new_lens or new_state None: lens or state is written in place."""
     me = "coli_kv_plan"
     import torch
+    if ring is None or slot is None:
+        raise ValueError(f"{me}: ring and slot must be given")
     i32, arg, at, B, rows = torch.int32, _kv_arg, ring.get_device(), (shape.B,), slot.shape
     if at < 0:
         raise ValueError(f"{me}: ring must be on a GPU, not on {ring.device}")
@@ -699,7 +701,7 @@ def _kv_rows(where: str, at: int, name: str, t, dtype, size):
     ld, across, along = t.stride()
     if (D > 1 and along != 1) or (H > 1 and across != D):
         raise ValueError(f"{where}: the heads of a row of {name} must lie side by side")
-    if size[0] < 2 and ld < H * D:                   # (of one row the stride says nothing)
+    if size[0] < 2:                                  # (of one row the stride says nothing)
         ld = H * D
     return t.data_ptr(), ld
 

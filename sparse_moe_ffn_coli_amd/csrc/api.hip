@@ -888,6 +888,7 @@ coli_status coli_rope_freqs(int32_t rot, double base, int32_t scaling, double fa
         return COLI_E_SHAPE;
     if (!freq || !amp) return COLI_E_NULL;
     if (scaling == COLI_ROPE_NTK) base *= pow(factor, (double)rot / (rot - 2));
+    if (!(base < INFINITY)) return COLI_E_SHAPE;
     for (int i = 0; i < rot / 2; ++i) {
         double f = pow(base, -2.0 * i / rot);
         if (scaling == COLI_ROPE_LINEAR) f /= factor;
@@ -908,7 +909,7 @@ coli_status coli_kv_rope(const coli_kv_shape *s, int32_t rows, const void *q, in
                          void *stream)
 {
     coli_status st = check_kv_shape(s, !v);
-    if (st == COLI_E_SHAPE && !k && !v) st = check_kv_shape(s, false);   // queries alone: for either kind of cache
+    if (st == COLI_E_SHAPE && !v && !slot) st = check_kv_shape(s, false);   // nothing for a cache: of either kind
     if (st != COLI_OK) return st;
     if (rows < 0 || rows > (1 << 25)) return COLI_E_SHAPE;
     const int64_t qw = (int64_t)s->Hq * s->Dk, kw = (int64_t)s->Hkv * s->Dk, vw = (int64_t)s->Hkv * s->Dv;

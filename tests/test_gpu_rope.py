@@ -189,6 +189,22 @@ def test_other_heads_do_not_leak():
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+def test_one_row_of_any_stride():
+    # a single row says nothing about where the next one would be
+    import torch
+    shape = KvShape(B=0, Hq=2, Hkv=2, Dk=64, Dv=64, page=16, n_pages=1, max_pages=1, dtype=COLI_F32)
+    x = torch.randn(2 * 64 + 4, device="cuda").as_strided((1, 2, 64), (132, 64, 1))
+    out, want = torch.empty(1, 2, 64, device="cuda"), torch.empty(1, 2, 64, device="cuda")
+    freq, pos = coli_rope_freqs(64)[0].cuda(), dev(np.array([77], np.int32))
+    assert x.stride(0) % 8 == 4
+    coli_kv_rope(shape, x, None, None, out, pos=pos, rope=Rope(freq))
+    coli_kv_rope(shape, x.contiguous().view(1, 2, 64), None, None, want, pos=pos, rope=Rope(freq))
+    assert torch.equal(out, want)
+    two = torch.randn(2, 2 * 64 + 4, device="cuda")[:, :128].unflatten(1, (2, 64))
+    with pytest.raises(ColiError):
+        coli_kv_rope(shape, two, None, None, torch.empty(2, 2, 64, device="cuda"), pos=pos.repeat(2), rope=Rope(freq))
+
+
 def test_queries_alone_and_keys_alone():
     import torch
     shape = KvShape(B=0, Hq=4, Hkv=2, Dk=64, Dv=64, page=16, n_pages=1, max_pages=1, dtype=COLI_F32)

@@ -2,6 +2,7 @@
 fails a check before the library reaches the device (and those tests run only where there is none).  Then the angles of
 the rotation, and the plain forms by hand."""
 import ctypes as C
+import dataclasses
 import math
 
 import numpy as np
@@ -133,6 +134,33 @@ def test_shared_attention_refusals():
 
 
 @no_gpu
+def test_keys_that_go_to_no_cache():
+    # normed and rotated keys of a cache of pairs whose values are the wider ones, which no latent cache has
+    pair = dict(s=shape(Dk=64, Dv=128), q_ld=32 * 64, k_ld=8 * 64, rot=(fake(6), 64, 0, 0, 1.0), norm=None)
+    out = dict(v=None, slot=None, pool_k=None, pool_v=None, k_out=fake(10))
+    assert rope(**pair) == E_DEVICE and rope(**pair, **out) == E_DEVICE and rope(**pair, **(out | dict(q=None, q_out=None))) == E_DEVICE
+    assert rope(**pair, v=None, pool_v=None) == E_SHAPE                              # with places: latent rows only
+
+
+def test_a_shapes_copies_form_their_own_c_form():
+    import copy
+    import pickle
+    s = shape()
+    ref = pkg._shape_ref(s)
+    assert pkg._shape_ref(s) is ref
+    for t in (copy.copy(s), copy.deepcopy(s), pickle.loads(pickle.dumps(s)), dataclasses.replace(s, B=9)):
+        assert "_ref" not in t.__dict__ and hash(t) is not None and (t == s or t.B == 9)
+        assert pkg._shape_ref(t) is not ref and pkg._shape_ref(t)._obj.B == t.B
+
+
+def test_the_binding_names_what_is_missing():
+    i = torch.zeros(64, dtype=torch.int32)
+    for ring, slot in ((None, i), (i, None)):
+        with pytest.raises(ValueError, match="ring and slot"):
+            pkg.coli_kv_plan(shape(), i.view(1, 64), i, i, ring, i, i, slot, i)
+
+
+@no_gpu
 def test_the_binding_takes_gpu_tensors_only():
     i = torch.zeros(64, dtype=torch.int32)
     with pytest.raises(ValueError, match="GPU"):
@@ -159,6 +187,14 @@ def test_freqs():
     for scaling in pkg.ROPE_SCALINGS:                                                # a factor of one changes nothing
         g, amp = pkg.coli_rope_freqs(40, 500000.0, scaling, 1.0, 8192)
         assert amp == 1 and np.allclose(g.numpy(), 500000.0 ** (-2 * np.arange(20) / 40), rtol=1e-14, atol=0)
+
+
+def test_freqs_whose_base_passes_the_end():
+    # base * factor^(rot / (rot - 2)) past the largest number would leave every angle but the first at 0
+    with pytest.raises(pkg.ColiError):
+        pkg.coli_rope_freqs(8, 1e300, "ntk", 1e7)
+    f, _ = pkg.coli_rope_freqs(8, 1e300, "yarn", 1e7)
+    assert f[0] == 1 and np.allclose(f[1:].numpy() * 1e7, 1e300 ** (-np.arange(1, 4) / 4), rtol=1e-13, atol=0)
 
 
 def test_freqs_refusals():
