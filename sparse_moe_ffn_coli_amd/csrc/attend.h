@@ -155,6 +155,28 @@ struct KvRange {
 template <KvPart PART = KV_ALL>
 __device__ __forceinline__ bool kv_first(const AttnLaunch &a, int R, KvRange &rg, int blk = blockIdx.x)
 {
+    if constexpr (PART != KV_ALL) {           // up to 64 items: in one look at them
+        if (kv_items<PART>(a) <= 64) {
+            const int lane = threadIdx.x & 63, i = min(lane, kv_items<PART>(a) - 1);
+            const bool some = lane < kv_items<PART>(a);
+            const int n = some ? kv_len<PART>(a, i) : 0;
+            const int st = kv_units(n) * (PART == KV_PREFIX ? a.Hkv * kv_tiles<PART>(a, i) : 1);
+            if (PART == KV_PREFIX && __ballot(kv_group_end(a, i) < kv_group_first(a, i))) return false;
+            const int incl = wave_scan_incl(st), total = __builtin_amdgcn_readlane(incl, 63) * R;
+            const int range = kv_range(a, total), u = blk * range;
+            if (u >= total) return false;
+            const int x = __ffsll((unsigned long long)__ballot(u < incl * R)) - 1;
+            const int at = u - __builtin_amdgcn_readlane(incl - st, x) * R;
+            rg.u = u;
+            rg.u_end = min(u + range, total);
+            rg.b = x;
+            rg.n = __builtin_amdgcn_readlane(n, x);
+            rg.steps = kv_steps(rg.n);
+            rg.row = at / kv_units(rg.n);
+            rg.s0 = at - rg.row * kv_units(rg.n);
+            return true;
+        }
+    }
     int before, total;
     kv_prefix<PART>(a, 0, &before, &total);
     total *= R;

@@ -57,7 +57,6 @@ __device__ __forceinline__ uint32_t kp_pack(float lo, float hi)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// The range of a workgroup: kv_first, of up to 64 groups in one look at them.
 struct KpGroup {
     int first, queries, tiles;                // first sequence, query heads of a cache head, their tiles
 };
@@ -69,38 +68,6 @@ __device__ __forceinline__ KpGroup kp_group(const AttnLaunch &a, int b)
     g.tiles = (g.queries + a.tile_rows - 1) / a.tile_rows;
     return g;
 }
-__device__ __forceinline__ bool kp_first(const AttnLaunch &a, KvRange &rg, KpGroup &grp)
-{
-    if (a.n_groups > 64) {
-        if (!kv_first<KV_PREFIX>(a, 1, rg)) return false;
-        grp = kp_group(a, rg.b);
-        return true;
-    }
-    const int lane = threadIdx.x & 63;
-    const KpGroup g = kp_group(a, min(lane, a.n_groups - 1));
-    if (__ballot(g.queries < 0)) return false;               // (as in kv_prefix)
-    const bool some = lane < a.n_groups && g.queries > 0;
-    const int n = some ? kv_shared(a, min(g.first, a.B - 1)) << a.page_shift : 0;
-    const int st = kv_units(n) * a.Hkv * (some ? g.tiles : 0);
-    const int incl = wave_scan_incl(st), total = __builtin_amdgcn_readlane(incl, 63);
-    const int range = kv_range(a, total), u = blockIdx.x * range;
-    if (u >= total) return false;
-    const int x = __ffsll((unsigned long long)__ballot(u < incl)) - 1;
-    const int base = __builtin_amdgcn_readlane(incl - st, x);
-    grp.first = __builtin_amdgcn_readlane(g.first, x);
-    grp.queries = __builtin_amdgcn_readlane(g.queries, x);
-    grp.tiles = __builtin_amdgcn_readlane(g.tiles, x);
-    rg.u = u;
-    rg.u_end = min(u + range, total);
-    rg.b = x;
-    rg.n = __builtin_amdgcn_readlane(n, x);
-    rg.steps = kv_steps(rg.n);
-    const int per = kv_units(rg.n);
-    rg.row = (u - base) / per;
-    rg.s0 = (u - base) - rg.row * per;
-    return true;
-}
-
 template <int DK, int DV, int WQ, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attn_prefix_kernel(AttnLaunch a)
 {
@@ -130,8 +97,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const int qt = wave % WQ, kb = wave / WQ;
     const int ql = lane & 31, hi = lane >> 5;
     KvRange rg;
-    KpGroup grp;
-    if (!kp_first(a, rg, grp)) return;
+    if (!kv_first<KV_PREFIX>(a, 1, rg)) return;
+    KpGroup grp = kp_group(a, rg.b);
     int u = rg.u, b = rg.b, n = rg.n, steps = rg.steps, row = rg.row, s0 = rg.s0;
     const int u_begin = u, u_end = rg.u_end;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
