@@ -755,20 +755,39 @@ static void launch_tiles(const AttnLaunch &own, const AttnLaunch &pre, const Att
     }
 }
 
-template <int DK, int DV, int WQ, KvPart PART>
-static void launch_wide(const AttnLaunch &a, hipStream_t st)
+// Both parts of latent rows in one launch: the ring fills a CU's LDS, so the own
+// parts' ranges follow where the shared pages leave CUs free (four sequences of
+// 64 heads behind 2048 positions: 42 us, 57 in two; 32 behind 32768: 222, 226).
+// Ranges of four units at least, not eight: 39 us there, but 16 sequences
+// behind two prompts of 4096 70 for 53.
+template <int DK, int DV, int WO, int WP, KwPast PAST>
+__global__ __launch_bounds__(KV_NT) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_wide_parts_kernel(AttnLaunch own, AttnLaunch pre)
 {
-    if (a.Dk == DK) attn_wide_kernel<DK, DV, WQ, KW_NONE, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else if (a.Dk >= DV) attn_wide_kernel<DK, DV, WQ, KW_TAIL, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
-    else attn_wide_kernel<DK, DV, WQ, KW_BOTH, PART><<<a.n_wg, KV_NT, 0, st>>>(a);
+    const int blk = (int)blockIdx.x - pre.n_wg;
+    if (blk < 0) attn_wide_rows<DK, DV, WP, PAST, KV_PREFIX>(pre, blockIdx.x);
+    else attn_wide_rows<DK, DV, WO, PAST, KV_OWN>(own, blk);
 }
 
-template <int DK, int DV, KvPart PART>
-static void launch_wide(const AttnLaunch &a, int wq, hipStream_t st)
+template <int DK, int DV, int WO, int WP>
+static void launch_wide(const AttnLaunch &own, const AttnLaunch &pre, hipStream_t st)
 {
-    if (wq == 1) launch_wide<DK, DV, 1, PART>(a, st);
-    else if (wq == 2) launch_wide<DK, DV, 2, PART>(a, st);
-    else launch_wide<DK, DV, 4, PART>(a, st);
+    const int n = own.n_wg + pre.n_wg;
+    if (own.Dk == DK) attn_wide_parts_kernel<DK, DV, WO, WP, KW_NONE><<<n, KV_NT, 0, st>>>(own, pre);
+    else if (own.Dk >= DV) attn_wide_parts_kernel<DK, DV, WO, WP, KW_TAIL><<<n, KV_NT, 0, st>>>(own, pre);
+    else attn_wide_parts_kernel<DK, DV, WO, WP, KW_BOTH><<<n, KV_NT, 0, st>>>(own, pre);
+}
+
+// (a group has at least as many query heads as a sequence)
+template <int DK, int DV>
+static void launch_wide(const AttnLaunch &own, const AttnLaunch &pre, const SharedPlan &p, hipStream_t st)
+{
+    const int wo = p.own.wq, wp = p.pre.wq;
+    if (wo == 4) launch_wide<DK, DV, 4, 4>(own, pre, st);
+    else if (wo == 2 && wp == 4) launch_wide<DK, DV, 2, 4>(own, pre, st);
+    else if (wo == 2) launch_wide<DK, DV, 2, 2>(own, pre, st);
+    else if (wp == 4) launch_wide<DK, DV, 1, 4>(own, pre, st);
+    else if (wp == 2) launch_wide<DK, DV, 1, 2>(own, pre, st);
+    else launch_wide<DK, DV, 1, 1>(own, pre, st);
 }
 
 template <int DK, int DV, int NW>
@@ -781,18 +800,11 @@ static void launch_prefix(const AttnLaunch &a, int wq, hipStream_t st)
     else if constexpr (NW == 8) attn_prefix_kernel<DK, DV, 8, NW><<<a.n_wg, 64 * NW, 0, st>>>(a);
 }
 
-template <KvPart PART>
-static void launch_latent(const AttnLaunch &a, const AttnPlan &p, hipStream_t st)
-{
-    if (p.out_cols == 256) launch_wide<320, 256, PART>(a, p.wq, st);
-    else launch_wide<576, 512, PART>(a, p.wq, st);
-}
-
 hipError_t launch_attn_shared(const AttnLaunch &own, const AttnLaunch &pre, const SharedPlan &p, hipStream_t st)
 {
     if (p.own.wide) {
-        launch_latent<KV_OWN>(own, p.own, st);
-        launch_latent<KV_PREFIX>(pre, p.pre, st);
+        if (p.own.out_cols == 256) launch_wide<320, 256>(own, pre, p, st);
+        else launch_wide<576, 512>(own, pre, p, st);
     } else {
         const bool both = !p.pre.wide;
         if (own.bf16) launch_tiles<true>(own, pre, p.own, both, st);
