@@ -2,8 +2,10 @@
  * coli_moe.h -- C ABI of the MI355X (gfx950) routed mixture-of-experts FFN
  * layer used by GLM-5.3-Flash-style models, with the pieces around it that
  * the same pages describe: the dense FFN of the first layers, a double-banked
- * device expert cache, the sparse attention's index top-k selection, and the
- * paged key-value cache with the attention of new tokens over it.
+ * device expert cache, the sparse attention's index top-k selection, the
+ * paged key-value cache with the attention of new tokens over it, and a serving
+ * step around that: its plan over the free pages, norm and rotation of queries
+ * and keys, attention where sequences share pages.
  *
  * The layer, per token x (length D):
  *   z      = W_router x + b                         (E logits, bias inside the sigmoid)

@@ -29,6 +29,11 @@ namespace coli {
 // LDS rows are RK or RV chunks of 16 bytes (a power of two), chunk c of row r
 // at c XOR kp_swz(r): 16 rows of one chunk (scores) and 4 rows of 4 chunks
 // (output) fall in distinct banks.
+// 64 sequences of 4 heads a cache head behind 32768 positions, 8 cache heads of
+// 128: 61 us, 52 GFLOP with the weights' second parts (0.85 PFLOP/s; the
+// library's large product reaches 1.32).  A round of 1536 cycles of products
+// takes some 3000: a weight's multiply, exponential, sum and two roundings are
+// 16 to 20 issue cycles, of two waves a SIMD.
 constexpr int KP_BLOCK = 32;                  // stages whose rows are looked up at a time
 
 template <int R>
