@@ -525,8 +525,11 @@ __device__ __forceinline__ void attn_rows(const AttnLaunch &a, int blk)
         for (; s < s1; s += NW) {
             const bool more = s + NW < s1;
             // ---- scores: D[key][query] = K Q^T, two tiles of 16 keys ----
-            f32x4 sc[2];
-            sc[0] = sc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // fp32 parts of wide rows: two sums, which halves what a long chain rounds away (rows of 512: outputs 8.3e-7
+            // off, 2.0e-6 with one; the times are the same, but 64-wide rows would lose a wave a SIMD: 18.6 -> 21.4 us).
+            constexpr int SUMS = !BF16 && PART != KV_ALL && DK > 64 ? 2 : 1;
+            f32x4 sc[2], sc2[2];
+            sc[0] = sc[1] = sc2[0] = sc2[1] = f32x4{0.f, 0.f, 0.f, 0.f};
             auto product = [&](const u32x4 &k0, const u32x4 &k1, int c) {
                 if constexpr (BF16) {
                     sc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k0), as_bf16(qf[c]), sc[0], 0, 0, 0);
@@ -534,8 +537,9 @@ __device__ __forceinline__ void attn_rows(const AttnLaunch &a, int blk)
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k0[e]), __uint_as_float(qf[c][e]), sc[0], 0, 0, 0);
-                        sc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k1[e]), __uint_as_float(qf[c][e]), sc[1], 0, 0, 0);
+                        f32x4 *d = SUMS == 2 && e & 1 ? sc2 : sc;
+                        d[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k0[e]), __uint_as_float(qf[c][e]), d[0], 0, 0, 0);
+                        d[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k1[e]), __uint_as_float(qf[c][e]), d[1], 0, 0, 0);
                     }
                 }
             };
@@ -551,6 +555,10 @@ __device__ __forceinline__ void attn_rows(const AttnLaunch &a, int blk)
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
                     if (c < key_chunks) product(kf[0][c], kf[1][c], c);
+            }
+            if constexpr (SUMS == 2) {
+                sc[0] += sc2[0];
+                sc[1] += sc2[1];
             }
             const int rows_now = rows;
             rows = rows_next;
