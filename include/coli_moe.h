@@ -439,14 +439,23 @@ coli_status coli_kv_evict(const coli_kv_shape *s, const coli_kv_cache *c, const 
  * new token of the step goes.  For each sequence b of lens[b] positions:
  *   want[b] <  lens[b]: it is cut to want[b] positions (0: it has ended); the
  *     pages behind them go to the tail of the ring of free pages, except the
- *     first shared[b] of its row, which are not its own (shared nullable: all
- *     are; shared[b] is at most the pages it holds, before and after);
+ *     first shared[b] of its row, which others read too (shared nullable: none
+ *     are);
  *   want[b] >  lens[b]: it grows by want[b] - lens[b] new tokens and takes the
  *     pages it needs more from the head of the ring, in the order of the
  *     sequences and of their positions.
  * Pages that go back can be taken in the same call.  First come, first served:
  * the first growing sequence that the ring cannot serve, or whose tokens pass
  * the step's `rows`, stays as it is, and so does every growing one after it.
+ * Shared pages: every sequence that reads them has their number in shared[b],
+ * the one that brought them too, and keeps it when it is cut below them or has
+ * ended, as long as another reads them.  The last one gives them back: it
+ * passes 0 in the call that ends it (at a length that still covers them).  A
+ * sequence that holds fewer pages than shared[b] does not grow: it stays as it
+ * is, is counted as refused and keeps no other waiting (to begin anew in its
+ * place, or to go on behind a copy of its own of those pages, pass 0).  One
+ * that ends inside the last of shared[b] pages grows in that page: where
+ * others read it, a growing sequence has lens[b] >= shared[b] * page.
  *   ring [n_pages] int32: free page ids, the first at ring[head], from the
  *     array's end on to its start.  Every page is at most once in the ring or
  *     in one sequence's hands

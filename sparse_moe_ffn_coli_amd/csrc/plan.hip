@@ -82,6 +82,7 @@ __device__ __forceinline__ int sum_owner(const uint32_t *sums, int n, uint32_t i
 
 struct PlanSeq {
     int n, t, held, need, from;          // lengths, pages, first page that may go back
+    bool below;                          // would grow, but holds fewer pages than it shares: stays as it is
 };
 
 __device__ __forceinline__ PlanSeq plan_seq(const PlanLaunch &a, int b)
@@ -93,7 +94,11 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanLaunch &a, int b)
     s.t = min(max(a.want[b], 0), a.cap);
     s.held = (s.n + page - 1) >> a.page_shift;
     s.need = (s.t + page - 1) >> a.page_shift;
-    s.from = min(max(s.need, a.shared ? a.shared[b] : 0), s.held);
+    const int shared = a.shared ? a.shared[b] : 0;
+    // New pages in the columns of shared ones would never go back, and those would be lost to the sequence.
+    s.below = s.t > s.n && s.held < shared;
+    if (s.below) s.t = s.n, s.need = s.held;
+    s.from = min(max(s.need, shared), s.held);
     return s;
 }
 
@@ -164,7 +169,7 @@ __global__ __launch_bounds__(PL_NT) void kv_plan_kernel(PlanLaunch a, bool rows_
             atomicMin(&granted[0], upto_p - more);
             atomicMin(&granted[1], upto_t - news);
         }
-        const uint64_t who = __ballot(refused);
+        const uint64_t who = __ballot(refused || s.below);
         if ((tid & 63) == 0 && who) atomicAdd(&n_refused, (int)__popcll(who));
         __syncthreads();
         const uint32_t end_p = min(sat_add(pages, total[0]), granted[0]), end_t = min(sat_add(tokens, total[1]), granted[1]);
