@@ -32,8 +32,9 @@ namespace coli {
 // 64 sequences of 4 heads a cache head behind 32768 positions, 8 cache heads of
 // 128: 61 us, 52 GFLOP with the weights' second parts (0.85 PFLOP/s; the
 // library's large product reaches 1.32).  A round of 1536 cycles of products
-// takes some 3000: a weight's multiply, exponential, sum and two roundings are
-// 16 to 20 issue cycles, of two waves a SIMD.
+// takes some 3000: a weight's two multiplies, exponential, sum and two roundings
+// are 20 to 24 issue cycles, of two waves a SIMD (the second multiply, which
+// makes its score a sequence's own part's to the bit: 91 -> 92 us a call).
 constexpr int KP_BLOCK = 32;                  // stages whose rows are looked up at a time
 
 template <int R>
@@ -44,15 +45,18 @@ __device__ __forceinline__ int kp_swz(int row)
 }
 constexpr int kp_chunks(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
 
-// 2^(score scale - ref), the product rounded as the reference is: a fused one
-// would leave the largest score of some 2^30 the product's rounding, 2^64 and
-// more of it.
-__device__ __forceinline__ float kp_weight(float score, float scale, float ref)
+// A score in units of log2 e, to the bit as kv_scaled gives it to a sequence's
+// own positions: equal scores weigh the same in both parts, however large they
+// are.  The factor's parts have one sign, so an infinite score keeps its own.
+__device__ __forceinline__ float kp_scaled(float score, float scale, float scale_lo)
 {
 #pragma clang fp contract(off)
-    const float t = score * scale;
-    return __builtin_amdgcn_exp2f(t - ref);
+    const float small = score * scale_lo;
+    return __builtin_fmaf(score, scale, small);
 }
+// 2^(t - ref), t rounded as the reference is: fused with the subtraction, the
+// largest score of some 2^30 would leave t's rounding, 2^64 and more of it.
+__device__ __forceinline__ float kp_weight(float t, float ref) { return __builtin_amdgcn_exp2f(t - ref); }
 
 // Two fp32 to bf16 in one instruction (pack_bf16 takes four).
 __device__ __forceinline__ uint32_t kp_pack(float lo, float hi)
@@ -108,14 +112,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const int u_begin = u, u_end = rg.u_end;
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
     const uint64_t kpool = (uint64_t)a.k, vpool = (uint64_t)(a.v ? a.v : a.k);
-    // A score in units of log2 e is one product here, by scale's size alone: the
-    // rounded factor is off by half a step of the score, the sum of the products
-    // by more.  The queries take its sign, so the largest product is the largest
-    // score.
+    // The queries take scale's sign, so that the largest product is the largest
+    // score (kp_scaled does not fall as the score rises).
     // A scale of zero becomes zero queries (of which an infinity is no number, as its product with the scale): the
     // scores of hidden positions are infinities.
     const bool zero = a.scale_size == 0.f;
-    const float scale = zero ? 1.f : a.scale_size;
+    const float scale = zero ? 1.f : a.scale_size, scale_lo = zero ? 1.f : fabsf(a.scale_lo);
     const uint32_t flip = a.scale_hi < 0.f ? 0x80008000u : 0u;
     const uint32_t k_bytes = a.Dk * 2, v_bytes = a.v ? a.Dv * 2 : k_bytes;        // from a row to the next
 
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
             float mx = sc[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-            mx *= scale;
+            mx = kp_scaled(mx, scale, scale_lo);
             moved = 1.f;
             if (__ballot(mx > m + 8.f)) {
                 const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         u32x4 parts[2][2][2];                 // of two rounds: high and low parts of 8 positions each
         float even;
         auto weight = [&](int i, auto to) {
-            const float w = kp_weight(sc[i], scale, ref);
+            const float w = kp_weight(kp_scaled(sc[i], scale, scale_lo), ref);
             l += w;
             if (i % 2 == 0) {
                 even = w;
