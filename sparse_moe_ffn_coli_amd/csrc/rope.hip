@@ -5,7 +5,8 @@
 //   norm      x_i <- x_i w_i / sqrt(mean x^2 + eps)   over the head's first `width` elements
 //   rotation  (x_i, x_j) <- (x_i c - x_j s, x_j c + x_i s),  c, s = amp (cos, sin)(pos freq)
 // All in fp32, rounded once.  The angle is formed in 64 bits, as turns less
-// whole turns: at position 2^24 an fp32 angle would be off by a radian.
+// whole turns (at position 2^24 an fp32 angle would be off by a radian), and
+// nothing of it is lost on the way to fp32 cosines and sines.
 //
 // Bound by the bytes: every element is read and written once.  A head is held
 // by a group of lanes, 16 bytes of it (bf16) each, so the norm's sum and the
@@ -133,8 +134,12 @@ __global__ __launch_bounds__(RP_NT) void kv_rope_kernel(RopeLaunch a)
         for (int i = tid; i < nt * half; i += RP_NT) {
             const int x = one ? 0 : i / half;
             const double turns = (double)(one ? pos_one : a.pos[t0 + x]) * (a.freq[i - x * half] * 0.15915494309189533577);
-            float s, c;
-            sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+            // half turns in fp32, and what that leaves as an angle: (c, s) turned by it
+            const double halves = 2.0 * (turns - rint(turns));
+            const float near = (float)halves, rest = (float)((halves - near) * 3.14159265358979323846);
+            float s0, c0;
+            sincospif(near, &s0, &c0);
+            const float s = fmaf(c0, rest, s0), c = fmaf(-s0, rest, c0);
             angle[i][0] = c * a.amp;
             angle[i][1] = s * a.amp;
         }
