@@ -749,7 +749,7 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
     a.q = q; a.k = c->k; a.v = c->v;
     a.table = c->table; a.lens = c->lens; a.idx = idx; a.idx_k = idx_k;
     a.out = out; a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out; a.ld = (long)ld;
-    a.tile_rows = L.plan.tile_rows; a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
+    a.q_tiles = L.plan.q_tiles; a.direct = L.plan.direct; a.n_wg = L.plan.n_wg; a.min_units = L.plan.min_units;
     char *base = (char *)ws;
     a.part_o = (float *)(base + L.part_o);
     a.part_ml = (float *)(base + L.part_ml);
@@ -802,7 +802,7 @@ coli_status coli_kv_attn_shared(const coli_kv_shape *s, const void *q, const col
     char *base = (char *)ws;
     coli::AttnLaunch pre = a;
     auto part = [&](coli::AttnLaunch &x, const coli::AttnPlan &p, size_t o, size_t ml, size_t full, size_t full_ml) {
-        x.tile_rows = p.tile_rows; x.out_cols = p.out_cols; x.q_tiles = p.q_tiles;
+        x.tile_rows = p.tile_rows; x.q_tiles = p.q_tiles;
         x.n_wg = p.n_wg; x.min_units = p.min_units;
         x.part_o = (float *)(base + o);
         x.part_ml = (float *)(base + ml);

@@ -241,19 +241,19 @@ __device__ __forceinline__ void kv_next_row(const AttnLaunch &a, int R, int &b, 
     steps = kv_steps(n);
 }
 
-// A row's query tile: cache head, the first of its queries and how many the
-// cache head has in all.  Query i of a cache head is row kv_query_row of q.
+// A group's row, a query tile: cache head, the first of its queries and how
+// many the cache head has in all.  Query i of a cache head is row kv_query_row
+// of q.
 struct KvTileOf {
     int h, q0, queries;
 };
-template <KvPart PART = KV_ALL>
-__device__ __forceinline__ KvTileOf kv_tile_of(const AttnLaunch &a, int b, int row)
+__device__ __forceinline__ KvTileOf kv_tile_of(const AttnLaunch &a, int g, int row)
 {
-    const int tiles = kv_tiles<PART>(a, b), G = a.Hq / a.Hkv;
+    const int tiles = kv_tiles<KV_PREFIX>(a, g);
     KvTileOf t;
     t.h = tiles == 1 ? row : row / tiles;
     t.q0 = (row - t.h * tiles) * a.tile_rows;
-    t.queries = PART == KV_PREFIX ? (kv_group_end(a, b) - kv_group_first(a, b)) * G : G;
+    t.queries = (kv_group_end(a, g) - kv_group_first(a, g)) * (a.Hq / a.Hkv);
     return t;
 }
 __device__ __forceinline__ size_t kv_query_row(const AttnLaunch &a, int first, int h, int i)
@@ -421,7 +421,7 @@ __device__ __forceinline__ void attn_rows(const AttnLaunch &a, int blk)
         const int s1 = min(steps, s0 + (u_end - u));
         int h, q0, nq;                        // (nq: query heads of this tile)
         if constexpr (PART == KV_PREFIX) {
-            const KvTileOf t = kv_tile_of<PART>(a, b, row);
+            const KvTileOf t = kv_tile_of(a, b, row);
             h = t.h, q0 = t.q0, nq = min(KV_QT, t.queries - q0);
         } else {
             h = a.q_tiles == 1 ? row : row / a.q_tiles, q0 = (row - h * a.q_tiles) * KV_QT;
@@ -715,7 +715,7 @@ __global__ __launch_bounds__(64 * NW) void attn_kernel(AttnLaunch a)
     attn_rows<BF16, DK, DV, NW, KV_ALL>(a, blockIdx.x);
 }
 
-// Where the parts of a row are: ranges w0 .. w1 hold some of it (w0 = w1: one
+// Where the parts of a sequence's row are: ranges w0 .. w1 hold some of it (w0 = w1: one
 // holds all, and has written the row's results); the first part's slot, the
 // later ranges' being their first ones.
 struct KvParts {
@@ -725,15 +725,13 @@ struct KvParts {
 template <KvPart PART = KV_ALL>
 __device__ __forceinline__ KvParts kv_parts(const AttnLaunch &a, int b, int row, int before, int total)
 {
-    const int R = PART == KV_PREFIX ? 1 : a.Hkv * a.q_tiles, n = kv_len<PART>(a, b);
+    const int R = a.Hkv * a.q_tiles, n = kv_len<PART>(a, b);
     KvParts p{kv_steps(n), 0, 0, 0};
     if (p.steps == 0) return p;
     const int range = kv_range(a, total * R);
     const int u0 = before * R + row * kv_units(n);
     p.w0 = u0 / range;
     p.w1 = (u0 + p.steps - 1) / range;
-    // (groups that are no partition have sums past every range)
-    if constexpr (PART == KV_PREFIX) p.w0 = min(max(p.w0, 0), a.n_wg - 1), p.w1 = min(max(p.w1, p.w0), a.n_wg - 1);
     p.first = 2 * p.w0 + (u0 == p.w0 * range ? 0 : 1);
     return p;
 }

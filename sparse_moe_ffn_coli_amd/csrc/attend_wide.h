@@ -61,7 +61,7 @@
                            (lane & 1) * 8;
         int h, q0, nq;                        // (nq: query heads of this wave's tile, may be none)
         if constexpr (PART == KV_PREFIX) {
-            const KvTileOf t = kv_tile_of<PART>(a, b, row);
+            const KvTileOf t = kv_tile_of(a, b, row);
             h = t.h, q0 = t.q0 + 32 * qt, nq = t.queries - q0;
         } else {
             h = row / a.q_tiles, q0 = (row % a.q_tiles) * (32 * WQ) + 32 * qt;

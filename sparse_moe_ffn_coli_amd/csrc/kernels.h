@@ -89,7 +89,6 @@ struct AttnLaunch {
     const int32_t *shared, *group_start;   // groups of sequences that share their first pages
     int n_groups;
     int tile_rows;         // query heads of a tile
-    int out_cols;          // columns of a part's rows
     float *full_o;         // workspace [B][Hq][Dv]: unnormalised outputs of rows that are not cut
     float *full_ml;        // workspace [B][Hq][2]
     float scale_size;      // |scale_hi|
