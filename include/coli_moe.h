@@ -528,7 +528,12 @@ coli_status coli_kv_rope(const coli_kv_shape *s, int32_t rows, const void *q, in
  *   COLI_ROPE_NTK     base * factor^(rot / (rot - 2)) in base's place
  *   COLI_ROPE_YARN    f_i where length * f_i / 2 pi >= 32 turns, f_i / factor
  *                     where it is at most 1, in between the share of f_i rises
- *                     with the turns; amp = 0.1 ln(factor) + 1
+ *                     linearly with the turns; amp = 0.1 ln(factor) + 1
+ * A checkpoint's angles are the ones it was trained with.  Models that are
+ * called YaRN too may let the share fall linearly with the pair's index i from
+ * the one border to the other, which are other angles there (up to 2.3 times
+ * these, rot 64, base 10000, length 4096, factor 8), or have other borders or
+ * another amplitude: those are a table of the caller's own, in coli_rope.
  * rot a multiple of 8 in [8, 576], base > 1, factor >= 1, length >= 1 (all
  * finite). */
 enum { COLI_ROPE_PLAIN = 0, COLI_ROPE_LINEAR = 1, COLI_ROPE_NTK = 2, COLI_ROPE_YARN = 3 };

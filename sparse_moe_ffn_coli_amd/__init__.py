@@ -650,7 +650,9 @@ ROPE_SCALINGS = ("plain", "linear", "ntk", "yarn")
 
 
 def coli_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, length: float = 4096):
-    """The angle per position of each pair (float64 tensor [rot / 2] on the CPU) and the factor on cosines and sines."""
+    """The angle per position of each pair (float64 tensor [rot / 2] on the CPU) and the factor on cosines and sines.
+    "yarn" blends by turns; a checkpoint that was trained with a blend by the pair's index, or with other borders or
+    another amplitude, needs a table of its own (Rope takes any)."""
     import torch
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"coli_rope_freqs: scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
