@@ -244,16 +244,12 @@ SharedWs shared_ws(const coli_kv_shape *s, int32_t n_groups, bool latent)
     return w;
 }
 
-// one_sign: the sum's first part is rounded towards zero, and below sc, so that
-// the second has its sign (sc of 0 aside).
-bool set_scale(coli::AttnLaunch &a, double sc, bool one_sign = false)
+bool set_scale(coli::AttnLaunch &a, double sc)
 {
     if (!(sc >= -3e38 && sc <= 3e38)) return false;
     // scale * log2(e) as the sum of two floats, without the error that one
     // rounded factor would put on every large score
     a.scale_hi = (float)sc;
-    if (one_sign && (fabs((double)a.scale_hi) > fabs(sc) || (float)(sc - (double)a.scale_hi) == 0.f))
-        a.scale_hi = nextafterf(a.scale_hi, 0.f);
     a.scale_size = fabsf(a.scale_hi);
     a.scale_lo = (float)(sc - (double)a.scale_hi);
     a.scale_cap = (float)(3e38 / fmax(1.0, fabs((double)a.scale_lo)));
@@ -775,7 +771,7 @@ coli_status coli_kv_attn_shared(const coli_kv_shape *s, const void *q, const col
     coli_status st = check_kv_cache(s, c);
     if (st != COLI_OK) return st;
     coli::AttnLaunch a{};
-    if (!set_scale(a, (double)scale * 1.4426950408889634074, true)) return COLI_E_SHAPE;
+    if (!set_scale(a, (double)scale * 1.4426950408889634074)) return COLI_E_SHAPE;
     if (n_groups < 0 || n_groups > s->B || (s->B > 0 && n_groups == 0)) return COLI_E_SHAPE;
     if (s->B == 0) return check_device();
     if (!q || !shared || !group_start || !out || !ws) return COLI_E_NULL;

@@ -32,9 +32,8 @@ namespace coli {
 // 64 sequences of 4 heads a cache head behind 32768 positions, 8 cache heads of
 // 128: 61 us, 52 GFLOP with the weights' second parts (0.85 PFLOP/s; the
 // library's large product reaches 1.32).  A round of 1536 cycles of products
-// takes some 3000: a weight's two multiplies, exponential, sum and two roundings
-// are 20 to 24 issue cycles, of two waves a SIMD (the second multiply, which
-// makes its score a sequence's own part's to the bit: 91 -> 92 us a call).
+// takes some 3000: a weight's multiply, exponential, sum and two roundings are
+// 16 to 20 issue cycles, of two waves a SIMD.
 constexpr int KP_BLOCK = 32;                  // stages whose rows are looked up at a time
 
 template <int R>
@@ -45,18 +44,16 @@ __device__ __forceinline__ int kp_swz(int row)
 }
 constexpr int kp_chunks(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
 
-// A score in units of log2 e, to the bit as kv_scaled gives it to a sequence's
-// own positions: equal scores weigh the same in both parts, however large they
-// are.  The factor's parts have one sign, so an infinite score keeps its own.
-__device__ __forceinline__ float kp_scaled(float score, float scale, float scale_lo)
+// 2^(scale (score - ref)): the reference is a score, and what is scaled is how
+// far the others are from it.  So the factor's rounding (one float) counts for
+// the distance only, equal scores have equal weights however large they are, and
+// only the reference itself needs the factor's two parts (kv_scaled).  (A
+// distance past fp32's end has no weight: a scale that gave it one would be
+// below 1e-36.)
+__device__ __forceinline__ float kp_weight(float score, float scale, float ref)
 {
-#pragma clang fp contract(off)
-    const float small = score * scale_lo;
-    return __builtin_fmaf(score, scale, small);
+    return __builtin_amdgcn_exp2f((score - ref) * scale);
 }
-// 2^(t - ref), t rounded as the reference is: fused with the subtraction, the
-// largest score of some 2^30 would leave t's rounding, 2^64 and more of it.
-__device__ __forceinline__ float kp_weight(float t, float ref) { return __builtin_amdgcn_exp2f(t - ref); }
 
 // Two fp32 to bf16 in one instruction (pack_bf16 takes four).
 __device__ __forceinline__ uint32_t kp_pack(float lo, float hi)
@@ -113,11 +110,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
     const uint64_t kpool = (uint64_t)a.k, vpool = (uint64_t)(a.v ? a.v : a.k);
     // The queries take scale's sign, so that the largest product is the largest
-    // score (kp_scaled does not fall as the score rises).
+    // score.
     // A scale of zero becomes zero queries (of which an infinity is no number, as its product with the scale): the
     // scores of hidden positions are infinities.
     const bool zero = a.scale_size == 0.f;
-    const float scale = zero ? 1.f : a.scale_size, scale_lo = zero ? 1.f : fabsf(a.scale_lo);
+    const float scale = zero ? 1.f : a.scale_size;
     const uint32_t flip = a.scale_hi < 0.f ? 0x80008000u : 0u;
     const uint32_t k_bytes = a.Dk * 2, v_bytes = a.v ? a.Dv * 2 : k_bytes;        // from a row to the next
 
@@ -280,11 +277,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
             float mx = sc[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-            mx = kp_scaled(mx, scale, scale_lo);
             moved = 1.f;
-            if (__ballot(mx > m + 8.f)) {
+            if (__ballot((mx - m) * scale > 8.f)) {
                 const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
-                moved = (mn == -INFINITY) ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+                moved = (mn == -INFINITY) ? 1.f : kp_weight(m, scale, mn);
                 m = mn;
                 l *= moved;
             }
@@ -294,7 +290,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
         u32x4 parts[2][2][2];                 // of two rounds: high and low parts of 8 positions each
         float even;
         auto weight = [&](int i, auto to) {
-            const float w = kp_weight(kp_scaled(sc[i], scale, scale_lo), ref);
+            const float w = kp_weight(sc[i], scale, ref);
             l += w;
             if (i % 2 == 0) {
                 even = w;
@@ -392,7 +388,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 #pragma unroll
             for (int x = 0; x < WK; ++x) {
                 const int wv = x * WQ + (q >> 5);
-                const float f = red_m[wv][qi] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(red_m[wv][qi] - mq);
+                const float f = red_m[wv][qi] == -INFINITY ? 0.f : kp_weight(red_m[wv][qi], scale, mq);
                 lq += red_l[wv][qi] * f;
                 v += buf[(wv * 32 + qi) * QC + (c ^ (qi & (QC - 1)))] * f;
             }
@@ -400,7 +396,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
             float *ml = whole ? a.full_ml : a.part_ml;
             *reinterpret_cast<f32x4 *>((whole ? a.full_o : a.part_o) + at * a.Dv + 4 * c) = v;
             if (c == 0) {
-                ml[2 * at] = mq;
+                // the reference as a sequence's own part has it, to the bit
+                ml[2 * at] = mq == -INFINITY ? mq : kv_scaled(a, flip ? -mq : mq);
                 ml[2 * at + 1] = lq;
             }
         }
