@@ -398,8 +398,13 @@ coli_status coli_kv_attn(const coli_kv_shape *s, const void *q, const coli_kv_ca
  *     has in common with its group, all of them full; the same for all
  *     sequences of a group, 0 for a group that shares nothing (clamped to
  *     [0, max_pages]).  They are read through the group's first row, whatever
- *     that sequence's length.  A sequence that ends before them (an empty slot
+ *     that sequence's length: an ended one's row keeps them as long as its
+ *     group has it (coli_kv_plan gives such a slot no new tokens while
+ *     shared[b] counts them).  A sequence that ends before them (an empty slot
  *     among them) is taken by itself, through its own row
+ * Lengths and groups are on the device, so the kernels go by the table's width
+ * (max_pages * page) and the groups' mean size, B / n_groups: tables no wider
+ * than the longest sequence and groups of like size are read fastest.
  * No listed positions and no running weights.  ws:
  * coli_kv_attn_shared_workspace_bytes(s, n_groups) bytes (0 for an invalid
  * shape or number); calls that may run at the same time need one each. */

@@ -627,7 +627,8 @@ def coli_kv_evict(shape: KvShape, cache: KvCache, acc, k: int, new_table, new_le
 def coli_kv_plan(shape: KvShape, table, lens, want, ring, state, start, slot, pos, shared=None, new_lens=None, new_state=None,
                  stream=None) -> None:
     """All int32 on one GPU: table [B][max_pages], lens, want, shared and new_lens [B], ring [n_pages], state and new_state
-    [4], start [B + 1], slot and pos [rows].  new_lens or new_state None: lens or state is written in place."""
+    [4], start [B + 1], slot and pos [rows].  new_lens or new_state None: lens or state is written in place.  shared: pages
+    that other sequences read too; it stays when a sequence ends, until the last of them passes 0 and gives them back."""
     me = "coli_kv_plan"
     import torch
     if ring is None or slot is None:

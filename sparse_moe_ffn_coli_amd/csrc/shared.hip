@@ -30,10 +30,12 @@ namespace coli {
 // at c XOR kp_swz(r): 16 rows of one chunk (scores) and 4 rows of 4 chunks
 // (output) fall in distinct banks.
 // 64 sequences of 4 heads a cache head behind 32768 positions, 8 cache heads of
-// 128: 61 us, 52 GFLOP with the weights' second parts (0.85 PFLOP/s; the
+// 128: 62 us, 52 GFLOP with the weights' second parts (0.84 PFLOP/s; the
 // library's large product reaches 1.32).  A round of 1536 cycles of products
 // takes some 3000: a weight's multiply, exponential, sum and two roundings are
-// 16 to 20 issue cycles, of two waves a SIMD.
+// 16 to 20 issue cycles, of two waves a SIMD.  At 192 / 128 elements 29 to 35
+// registers spill (24 sequences behind 32768 positions 78 us a call, 256 / 256
+// 107; 192 / 192 runs as 256, 101).
 constexpr int KP_BLOCK = 32;                  // stages whose rows are looked up at a time
 
 template <int R>
@@ -698,6 +700,12 @@ SharedPlan attn_shared_plan(int B, int Hq, int Hkv, int Dk, int Dv, bool bf16, b
         // 27, 32768 74 / 47; 96 queries 4096 26 / 30; 160 queries 512 21 / 30,
         // 4096 36 / 36, 32768 113 / 69; 64 wide 160 queries 4096 26 / 28,
         // 32768 81 / 51; 256 wide 96 queries 4096 46 / 47, 32768 156 / 100.
+        // Lengths and groups are on the device: the positions are the table's
+        // room here and the queries the groups' mean, which is right for
+        // tables as wide as their sequences and groups of like size.  48
+        // queries behind 512 positions in a table of 16384 take 25 us, 160 take
+        // 31 (tiles: 15 and 21); 160 behind 32768 beside 24 sequences that
+        // share nothing keep the tiles (117; alone, through LDS, 68).
         const long work = (long)n_groups * Hkv * ((queries + KV_QT - 1) / KV_QT) * ((entries + KV_STEP - 1) / KV_STEP);
         if (bf16 && d <= 256 && queries > 32 && work >= 8192) {
             s.pre.wide = true;                // (tier: the widths, as above)
